@@ -14,6 +14,13 @@ the library is missing, importing this package fails.
             moe_dispatch_mxfp4(input_tokens, top_k, restore_token_order, out_q, out_scales, flags)
     out  -> moe_combine(y, router_weights, restore_token_order, top_k, output_tokens)
             moe_combine_epilogue(..., scale, residual)
+
+The experts' products between dispatch and combine (``include/moe_experts.h``):
+
+    out -> moe_dispatch_i8(input_tokens, top_k, restore_token_order, out_q, out_scales)
+           moe_quantize_i8(x, out_q, out_scales[, row_count])
+           moe_expert_matmul_i8(a_q, a_scales, expert_start_indices, expert_ids, w_q, w_scales, out[, flags])
+    all -> moe_layer_few(x, topk_ids, router_weights, w_gate_up, w_down, output_tokens, workspace, ...)
 """
 from __future__ import annotations
 
@@ -29,6 +36,8 @@ __all__ = [
     "moe_dispatch", "moe_dispatch_mxfp4", "moe_combine", "moe_combine_epilogue", "moe_error_string",
     "MXFP4_EVEN_SCALE", "MXFP4_PACKED_ROWS",
     "alloc_indices", "alloc_dispatch", "alloc_dispatch_mxfp4", "index_workspace_error",
+    "moe_dispatch_i8", "moe_quantize_i8", "moe_expert_matmul_i8", "moe_layer_few", "moe_layer_few_workspace_bytes",
+    "MATMUL_SWIGLU", "MATMUL_MAX_DEPTH", "FEW_MAX_SLOTS", "alloc_quantized", "alloc_layer_few",
 ]
 
 SENTINEL = 0xFFFFFFFF
@@ -345,3 +354,9 @@ def moe_combine_epilogue(y: torch.Tensor, router_weights: torch.Tensor, restore_
         _check(lib.moe_combine_epilogue(_ptr(y), y.shape[0], _ptr(router_weights), _ptr(restore_token_order), n,
                                         h, int(top_k), float(scale), res, _ptr(output_tokens), _stream(dev)),
                "moe_combine_epilogue")
+
+
+from .experts import (  # noqa: E402  (needs the names above)
+    FEW_MAX_SLOTS, MATMUL_MAX_DEPTH, MATMUL_SWIGLU, alloc_layer_few, alloc_quantized, moe_dispatch_i8,
+    moe_expert_matmul_i8, moe_layer_few, moe_layer_few_workspace_bytes, moe_quantize_i8,
+)

@@ -16,3 +16,10 @@ from .moe_oracle import (  # noqa: F401
     mxfp4_dequantize,
     mxfp4_quantize,
 )
+from .experts_oracle import (  # noqa: F401
+    dispatch_i8,
+    expert_values,
+    layer_few,
+    quantize_i8,
+    swiglu,
+)
