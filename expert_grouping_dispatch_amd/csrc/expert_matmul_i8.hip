@@ -9,6 +9,8 @@
 //                  weights once: they stream into registers (stream.h).
 //   k_matmul_tile  larger groups, in tiles of 256 rows by 256 weight rows,
 //                  bound by the matrix units: both operands go through LDS.
+#include <type_traits>
+
 #include "experts.h"
 #include "rows.h"
 #include "stream.h"
@@ -20,7 +22,7 @@ namespace {
 constexpr int kFewRows = 64;
 constexpr int kFewWaves = 4, kFewThreads = kFewWaves * kWave;
 constexpr int kTile = 256, kStepBytes = 128;  // tile edge, and values of k per step
-constexpr int kTileThreads = 512;
+constexpr int kTileThreads = 256;
 constexpr int kMaxActive = 1024;
 
 // Rows [lo, hi) of active expert j, inside the buffer whatever the starts hold.
@@ -95,7 +97,7 @@ __device__ __forceinline__ void matmul_few_tile(const ExpertMatmul& p, uint32_t 
 }
 
 template <bool kSwiglu>
-__global__ __launch_bounds__(kFewThreads) void k_matmul_few(ExpertMatmul p) {
+__global__ __launch_bounds__(kFewThreads, 4) void k_matmul_few(ExpertMatmul p) {
   __shared__ i32x4 s_part[kFewWaves * 2 * (kFewRows / 16) * kWave];
   uint32_t lo, hi;
   group_rows(p.starts, blockIdx.y, p.a_rows, lo, hi);
@@ -113,167 +115,286 @@ __global__ __launch_bounds__(kFewThreads) void k_matmul_few(ExpertMatmul p) {
 
 namespace {
 
-typedef __attribute__((address_space(3))) uint8_t lds_byte;
-
-// 64 lanes x 16 bytes from `base + off` (per lane) to 1 KB of LDS at `dst`.
-__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t off, uint8_t* dst) {
-  __builtin_amdgcn_global_load_lds(
-      reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(reinterpret_cast<uintptr_t>(base + off)),
-      (__attribute__((address_space(3))) uint32_t*)(dst), 16, 0, 0);
+// A buffer from `base` to the end of `bytes` bytes: reads past it stay away
+// from memory.  A tile reads less than 2^26 bytes from its base.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* base, uint64_t bytes) {
+  const uint32_t size = bytes < (uint64_t(1) << 31) ? uint32_t(bytes) : 0x7FFFFFF0u;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, size, 0x00027000);
 }
+
+// 64 lanes x 16 bytes from `off` (per lane) + `at` to 1 KB of LDS at `dst`.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t off, uint32_t at, uint8_t* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)(dst), 16, off, at, 0, 0);
+}
+
+constexpr int kWaitLoads = 0x0F70;     // s_waitcnt vmcnt(0)
+constexpr int kWaitLdsScalar = 0xC07F;  // s_waitcnt lgkmcnt(0)
 
 }  // namespace
 
-// One workgroup per CU takes tiles in turn.  Eight waves, 2 by 4: each forms
-// 128 rows by 64 weight rows with the 32x32x32 instruction.  A step is 128
-// values of k of 256 rows of both operands, 64 KB, in two buffers.  A row's
-// 128 bytes lie in LDS as eight 16-byte pieces, piece c at c ^ (row % 8), so
-// that the lanes of a read (consecutive rows, one piece) touch all banks.
-// With SwiGLU each 64 weight rows are 32 gate rows and the 32 up rows of the
+// A tile: its rows of the buffer, its first output channel, its expert.
+struct TilePlace {
+  uint32_t row0;
+  int n_rows, c0, e;
+};
+
+struct Walk {
+  uint32_t tile;  // next tile to look at
+  int j;          // place of its expert, found going forward
+};
+
+// One workgroup per CU takes tiles in turn.  Four waves, 2 by 2: each forms
+// 128 rows by 128 weight rows with the 32x32x32 instruction, which halves what
+// has to be read from LDS against eight waves of 128 by 64.
+//
+// A step is 128 values of k of 256 rows of both operands, 64 KB, in two
+// buffers that are filled straight from global memory.  A row's 128 bytes lie
+// in LDS as eight 16-byte pieces, piece c at c ^ (row % 8), so that the lanes
+// of a read (consecutive rows, one piece) touch all banks.
+//
+// A step has four parts of 32 values of k.  The fragments of a part are read
+// while the matrix units work on the part before it; the last part's are in
+// registers before its products start, so there the buffer is free: one
+// barrier, then it is filled for the step after next.  The stream of steps runs
+// on across tiles, so a tile's first steps arrive during the epilogue of the
+// tile before.
+//
+// With SwiGLU each 128 weight rows are 64 gate rows and the 64 up rows of the
 // same channels, so one lane holds both.
 template <bool kSwiglu>
-__global__ __launch_bounds__(kTileThreads, 2) void k_matmul_tile(ExpertMatmul p) {
+__global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p) {
   __shared__ __align__(16) uint8_t s_a[2][kTile * kStepBytes];
   __shared__ __align__(16) uint8_t s_w[2][kTile * kStepBytes];
   __shared__ uint32_t s_first[kMaxActive + 1];  // first tile of each active expert
+  __shared__ uint32_t s_row[kMaxActive + 1];    // its first row
   __shared__ uint32_t s_scan[kTileThreads / kWave];
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
   constexpr int kChannels = kSwiglu ? kTile / 2 : kTile;
   const uint32_t col_tiles = (p.n_out + kChannels - 1) / kChannels;
 
-  uint32_t tiles[2];
+  constexpr int kOwn = kMaxActive / kTileThreads;
+  uint32_t tiles[kOwn], sum = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int j = 2 * tid + i;
-    uint32_t lo = 0, hi = 0;
-    if (j < p.n_experts) group_rows(p.starts, j, p.a_rows, lo, hi);
+  for (int i = 0; i < kOwn; ++i) {
+    const int j = kOwn * tid + i;
+    uint32_t lo, hi;
+    group_rows(p.starts, min(j, p.n_experts - 1), p.a_rows, lo, hi);
+    if (j >= p.n_experts) lo = hi;
+    s_row[j] = lo;
+    if (j == kMaxActive - 1) s_row[kMaxActive] = hi;
     tiles[i] = hi - lo > uint32_t(kFewRows) ? ((hi - lo + kTile - 1) / kTile) * col_tiles : 0u;
+    sum += tiles[i];
   }
-  const uint32_t sum = wave_inclusive_sum(tiles[0] + tiles[1]);
-  if (lane == kWave - 1) s_scan[wave] = sum;
+  const uint32_t upto = wave_inclusive_sum(sum);
+  if (lane == kWave - 1) s_scan[wave] = upto;
   __syncthreads();
-  uint32_t before = sum - tiles[0] - tiles[1], total = 0;
+  uint32_t before = upto - sum, total = 0;
   for (int i = 0; i < kTileThreads / kWave; ++i) {
     if (i < wave) before += s_scan[i];
     total += s_scan[i];
   }
-  s_first[2 * tid] = before;
-  s_first[2 * tid + 1] = before + tiles[0];
-  if (tid == kTileThreads - 1) s_first[kMaxActive] = total;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    s_first[kOwn * tid + i] = before;
+    before += tiles[i];
+  }
+  if (tid == 0) s_first[kMaxActive] = total;
+  total = uniform(total);
   __syncthreads();
 
   // Workgroups of one XCD (blockIdx % 8) take neighbouring tiles.
   const uint32_t grid = gridDim.x, per = grid / 8, rest = grid % 8, xcd = blockIdx.x % 8;
-  const uint32_t place = xcd * per + min(xcd, rest) + blockIdx.x / 8;
-  const int wr = wave / 4, wc = wave % 4;
-  for (uint32_t tile = place; tile < total; tile += grid) {
-    int j = 0;  // the last active expert with s_first[j] <= tile
-    for (int step = kMaxActive / 2; step > 0; step /= 2)
-      if (s_first[j + step] <= tile) j += step;
-    uint32_t lo, hi;
-    group_rows(p.starts, j, p.a_rows, lo, hi);
-    if (hi == lo) continue;
-    const int e = p.expert_ids[j];
-    const uint32_t row_tiles = (hi - lo + kTile - 1) / kTile;
-    const uint32_t in = tile - s_first[j];
-    const uint32_t row0 = lo + (in % row_tiles) * kTile;
-    const int c0 = int(in / row_tiles) * kChannels;
-    if (e < 0 || e >= p.n_experts || row0 >= hi || c0 >= p.n_out) continue;
-    const int n_rows = int(min(hi - row0, uint32_t(kTile)));
-    const int wide = kSwiglu ? 2 * p.n_out : p.n_out;
+  const uint32_t first = xcd * per + min(xcd, rest) + blockIdx.x / 8;
 
-    // This wave fills LDS rows [32*wave, +32) of both operands, eight rows an
-    // instruction; rows past the tile's end repeat its last one.
-    const int piece = (lane % 8) ^ (lane / 8);
-    const uint8_t* a_base = reinterpret_cast<const uint8_t*>(p.a) + int64_t(row0) * p.depth;
-    int w_first = c0 + 32 * wave, w_last = p.n_out - 1, w_shift = 0;
-    if constexpr (kSwiglu) {
-      w_first = c0 + 32 * (wave / 2);
-      w_shift = wave % 2 == 0 ? 0 : p.n_out;
+  // The walk's next tile with work; false when there is none left.
+  auto advance = [&](Walk& at, TilePlace& t) {
+    for (; at.tile < total; at.tile += grid) {
+      while (at.j + 1 < kMaxActive && uniform(s_first[at.j + 1]) <= at.tile) ++at.j;
+      const uint32_t lo = uniform(s_row[at.j]), hi = max(min(uniform(s_row[at.j + 1]), p.a_rows), lo);
+      const uint32_t row_tiles = (hi - lo + kTile - 1) / kTile;
+      if (row_tiles == 0) continue;
+      const uint32_t in = at.tile - uniform(s_first[at.j]);
+      t.row0 = lo + (in % row_tiles) * kTile;
+      t.c0 = int(in / row_tiles) * kChannels;
+      t.e = p.expert_ids[at.j];
+      if (t.e < 0 || t.e >= p.n_experts || t.row0 >= hi || t.c0 >= p.n_out) continue;
+      t.n_rows = int(min(hi - t.row0, uint32_t(kTile)));
+      at.tile += grid;
+      return true;
     }
-    const int w_origin = min(w_first, w_last);
-    const uint8_t* w_base =
-        reinterpret_cast<const uint8_t*>(p.w) + (int64_t(e) * wide + w_shift + w_origin) * p.depth;
-    uint32_t a_off[4], w_off[4];
+    return false;
+  };
+
+  const int wide = kSwiglu ? 2 * p.n_out : p.n_out;
+  const int steps = (p.depth + kStepBytes - 1) / kStepBytes;
+  const bool ragged = p.depth % kStepBytes != 0;
+  const uint64_t a_bytes = uint64_t(p.a_rows) * p.depth, w_bytes = uint64_t(p.n_experts) * wide * p.depth;
+  // This wave fills LDS rows [64*wave, +64) of both operands, eight rows an
+  // instruction.  Rows past the tile's end are whatever follows it, or nothing
+  // past the buffer's end: what they give is not stored.
+  const int piece = (lane % 8) ^ (lane / 8);
+  const uint32_t lane_off = uint32_t(lane / 8) * p.depth + piece * 16;
+  __amdgpu_buffer_rsrc_t a_from, w_from;
+  auto aim = [&](const TilePlace& t) {
+    const uint64_t a0 = (uint64_t(t.row0) + 64 * wave) * p.depth;
+    const int first_w = t.c0 + (kSwiglu ? 64 * (wave / 2) + (wave % 2) * p.n_out : 64 * wave);
+    const uint64_t w0 = (uint64_t(t.e) * wide + first_w) * p.depth;
+    a_from = buffer_of(reinterpret_cast<const uint8_t*>(p.a) + min(a0, a_bytes), a0 < a_bytes ? a_bytes - a0 : 0);
+    w_from = buffer_of(reinterpret_cast<const uint8_t*>(p.w) + min(w0, w_bytes), w0 < w_bytes ? w_bytes - w0 : 0);
+  };
+  // A quarter of a step: 16 of this wave's 64 rows of both operands.
+  auto fetch = [&](int s, int buf, int quarter) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + lane / 8;
-      a_off[i] = uint32_t(min(32 * wave + r, n_rows - 1)) * uint32_t(p.depth);
-      w_off[i] = uint32_t(min(w_first + r, w_last) - w_origin) * uint32_t(p.depth);
+    for (int i = 2 * quarter; i < 2 * quarter + 2; ++i) {
+      const uint32_t at = uint32_t(s) * kStepBytes + uint32_t(8 * i) * p.depth;
+      load_to_lds(a_from, lane_off, at, &s_a[buf][(64 * wave + 8 * i) * kStepBytes]);
+      load_to_lds(w_from, lane_off, at, &s_w[buf][(64 * wave + 8 * i) * kStepBytes]);
     }
-    const int steps = (p.depth + kStepBytes - 1) / kStepBytes;
-    auto fetch = [&](int s, int buf) {
-      const int k = s * kStepBytes;
-      const uint32_t at = uint32_t(k + (k + piece * 16 < p.depth ? piece * 16 : 0));
+  };
+  // Waits for this wave's part of the buffer of step s; pieces past the row's
+  // end become zeros in the weights, so that they add nothing.
+  auto arrived = [&](int s, int buf) {
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    asm volatile("" ::: "memory");
+    if (ragged && s == steps - 1) {
+      if (s * kStepBytes + piece * 16 >= p.depth) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        load_to_lds(a_base, a_off[i] + at, &s_a[buf][(32 * wave + 8 * i) * kStepBytes]);
-        load_to_lds(w_base, w_off[i] + at, &s_w[buf][(32 * wave + 8 * i) * kStepBytes]);
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<u32x4*>(&s_w[buf][(64 * wave + 8 * i) * kStepBytes + lane * 16]) = u32x4{0u, 0u, 0u, 0u};
       }
-    };
-    i32x16 acc[2][4];
+    }
+    __builtin_amdgcn_s_waitcnt(kWaitLdsScalar);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  // `ahead` is the tile being fetched, up to two steps in front of `now`, the
+  // tile being formed; each walks the tiles on its own.  Past the last tile
+  // its steps are fetched again, for nothing.
+  TilePlace now, ahead;
+  Walk at_now{first, 0}, at_ahead{first, 0};
+  if (!advance(at_now, now)) return;
+  advance(at_ahead, ahead);
+  aim(ahead);
+  int fs = 0;  // the next step of `ahead` to fetch
+  auto fetched = [&] {
+    if (++fs == steps) {
+      fs = 0;
+      if (advance(at_ahead, ahead)) aim(ahead);
+      __builtin_amdgcn_s_waitcnt(kWaitLdsScalar);
+    }
+  };
+
+  const int wr = wave / 2, wc = wave % 2;
+  i32x4 fw[2][4], fa[2][4];
+  i32x16 acc[4][4];
+  // The products of the fragments in `set`, while part kk of `buf` is read
+  // into the other set and, with kFetch, the next step is requested.
+  auto part = [&](int set, int buf, int kk, auto fetch_too, auto fresh) {
+    const int at = ((kk * 2 + lane / 32) ^ (lane % 8)) * 16;
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+    for (int f = 0; f < 4; ++f) {
+      fw[set ^ 1][f] = *reinterpret_cast<const i32x4*>(&s_w[buf][(128 * wc + 32 * f + lane % 32) * kStepBytes + at]);
+      fa[set ^ 1][f] = *reinterpret_cast<const i32x4*>(&s_a[buf][(128 * wr + 32 * f + lane % 32) * kStepBytes + at]);
+    }
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
+    for (int f = 0; f < 4; ++f) {
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[f][g][i] = 0;
-    auto compute = [&](int buf, int k, bool last) {
+      for (int g = 0; g < 4; ++g) {
+        i32x16 c = acc[f][g];
+        if constexpr (decltype(fresh)::value)
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const int c = kk * 2 + lane / 32;
-        const int at = (c ^ (lane % 8)) * 16;
-        i32x4 w[2], a[4];
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-          w[f] = *reinterpret_cast<const i32x4*>(&s_w[buf][(64 * wc + 32 * f + lane % 32) * kStepBytes + at]);
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          a[g] = *reinterpret_cast<const i32x4*>(&s_a[buf][(128 * wr + 32 * g + lane % 32) * kStepBytes + at]);
-        if (last && k + c * 16 >= p.depth) {  // pieces past the row's end add nothing
-#pragma unroll
-          for (int f = 0; f < 2; ++f) w[f] = i32x4{0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-            acc[f][g] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[f], a[g], acc[f][g], 0, 0, 0);
+          for (int i = 0; i < 16; ++i) c[i] = 0;
+        acc[f][g] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[set][f], fa[set][g], c, 0, 0, 0);
       }
-    };
-    fetch(0, 0);
+      if constexpr (decltype(fetch_too)::value) {
+        fetch(fs, buf ^ 1, f);
+      }
+    }
+  };
+  constexpr std::integral_constant<bool, true> yes{};
+  constexpr std::integral_constant<bool, false> no{};
+
+#pragma unroll
+  for (int q = 0; q < 4; ++q) fetch(fs, 0, q);
+  fetched();
+  arrived(0, 0);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) fetch(fs, 1, q);
+  fetched();
+  int buf = 0;
+#pragma unroll
+  for (int f = 0; f < 4; ++f) {
+    const int at = ((lane / 32) ^ (lane % 8)) * 16;
+    fw[0][f] = *reinterpret_cast<const i32x4*>(&s_w[0][(128 * wc + 32 * f + lane % 32) * kStepBytes + at]);
+    fa[0][f] = *reinterpret_cast<const i32x4*>(&s_a[0][(128 * wr + 32 * f + lane % 32) * kStepBytes + at]);
+  }
+  do {
     for (int s = 0; s < steps; ++s) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-      if (s + 1 < steps) fetch(s + 1, (s + 1) & 1);
-      compute(s & 1, s * kStepBytes, s + 1 == steps);
+      if (s == 0) part(0, buf, 1, no, yes);
+      else part(0, buf, 1, no, no);
+      part(1, buf, 2, no, no);
+      part(0, buf, 3, no, no);
+      arrived(s + 1 < steps ? s + 1 : 0, buf ^ 1);
+      part(1, buf ^ 1, 0, yes, no);
+      fetched();
+      buf ^= 1;
     }
-    __syncthreads();  // the buffers are refilled for the next tile
 
-    const float* sw = p.w_scales + int64_t(e) * wide;
+    // Stores go through a buffer of the tile's rows: what a lane has for a row
+    // or channel past the end gets an offset past the buffer and is dropped.
+    const float* sw = p.w_scales + int64_t(now.e) * wide;
+    const uint32_t row_bytes = uint32_t(p.n_out) * 2, out_bytes = uint32_t(now.n_rows) * row_bytes;
+    const __amdgpu_buffer_rsrc_t out =
+        __builtin_amdgcn_make_buffer_rsrc(p.out + int64_t(now.row0) * p.n_out, 0, out_bytes, 0x00027000);
+    float sa[4];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int r = 128 * wr + 32 * g + lane % 32;
-      if (r >= n_rows) continue;
-      const float sa = p.a_scales[row0 + r];
-      uint16_t* o = p.out + int64_t(row0 + r) * p.n_out;
+    for (int g = 0; g < 4; ++g)
+      sa[g] = p.a_scales[now.row0 + min(128 * wr + 32 * g + lane % 32, now.n_rows - 1)];
 #pragma unroll
-      for (int f = 0; f < (kSwiglu ? 1 : 2); ++f) {
+    for (int f = 0; f < (kSwiglu ? 2 : 4); ++f) {
+      // 32 channels; a lane has four of each eight: 8*q + (lane/32)*4 + i
+      const int c0 = now.c0 + (kSwiglu ? 64 : 128) * wc + 32 * f;
+      f32x4 s0[4], s1[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = min(c0 + 8 * q, p.n_out - 8) + 4 * (lane / 32);
+        s0[q] = *reinterpret_cast<const f32x4*>(sw + c);
+        if constexpr (kSwiglu) s1[q] = *reinterpret_cast<const f32x4*>(sw + p.n_out + c);
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        // The sums stay in accumulation registers until their turn.
+        asm volatile("" : "+a"(acc[f][g]));
+        if constexpr (kSwiglu) asm volatile("" : "+a"(acc[f + 2][g]));
+        u32x2 v[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int c = c0 + (kSwiglu ? 32 * wc : 64 * wc + 32 * f) + 8 * q + 4 * (lane / 32);
-          if (c >= p.n_out) continue;
-          float v[4];
+          float x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            v[i] = scaled(acc[f][g][4 * q + i], sa, sw[c + i]);
-            if constexpr (kSwiglu) v[i] = silu_times(v[i], scaled(acc[1][g][4 * q + i], sa, sw[p.n_out + c + i]));
+            x[i] = scaled(acc[f][g][4 * q + i], sa[g], s0[q][i]);
+            if constexpr (kSwiglu) x[i] = silu_times(x[i], scaled(acc[f + 2][g][4 * q + i], sa[g], s1[q][i]));
           }
-          *reinterpret_cast<u32x2*>(o + c) = u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+          v[q] = u32x2{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
         }
+        // Lanes l and l+32 hold the two halves of each eight channels of one
+        // row: the lower one takes all of the even q, the upper of the odd.
+        const int r = 128 * wr + 32 * g + lane % 32;
+        const uint32_t at = uint32_t(r) * row_bytes + uint32_t(c0 + 8 * (lane / 32)) * 2;
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          const u32x2 x = permlane32_swap(v[q].x, v[q + 1].x), y = permlane32_swap(v[q].y, v[q + 1].y);
+          const bool some = r < now.n_rows && c0 + 8 * q < p.n_out;
+          __builtin_amdgcn_raw_buffer_store_b128(u32x4{x.x, y.x, x.y, y.y}, out, some ? at + 16 * q : 0xFFFFFFF0u, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);  // one fragment at a time, or the registers do not suffice
       }
     }
-  }
+  } while (advance(at_now, now));
+  __builtin_amdgcn_s_waitcnt(kWaitLoads);  // nothing may still be on its way to LDS
 }
 
 namespace {

@@ -109,7 +109,7 @@ __device__ __forceinline__ void few_up_tile(const uint8_t* x, int hidden, int to
 // are fewer slots than experts, a slot, which stands for its expert if it is
 // the first slot on it.
 template <class C, bool kScaled, typename IdT>
-__global__ __launch_bounds__(kUpThreads) void k_few_up(const uint8_t* __restrict__ x, int n_rows, int hidden,
+__global__ __launch_bounds__(kUpThreads, 4) void k_few_up(const uint8_t* __restrict__ x, int n_rows, int hidden,
                                                        int top_k, const IdT* __restrict__ ids, PadMask pad,
                                                        int n_experts, bool by_slot,
                                                        const uint8_t* __restrict__ w,
@@ -174,7 +174,7 @@ __device__ __forceinline__ void few_down_tile(const uint8_t* h, int inter, const
 
 // s_y (dynamic LDS): parts x slots x 16 channels of fp32.
 template <class C, bool kScaled, typename IdT>
-__global__ __launch_bounds__(kDownThreads) void k_few_down(
+__global__ __launch_bounds__(kDownThreads, 4) void k_few_down(
     const uint8_t* __restrict__ h, int n_rows, int hidden, int top_k, const IdT* __restrict__ ids,
     const float* __restrict__ router_weights, PadMask pad, int n_experts, const uint8_t* __restrict__ w,
     const float* __restrict__ w_scales, int inter, int max_parts, uint16_t* __restrict__ out) {

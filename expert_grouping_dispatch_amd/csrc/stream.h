@@ -70,9 +70,11 @@ struct CoreI8 {  // int8 weights, int8 activations
   }
 };
 
-// 16 bytes of a weight row: read once, so past the caches' reuse.
+// 16 bytes of a weight row.  A lane group's 16 bytes are an eighth of a cache
+// line, whose rest the next step reads: plain loads, which keep the line,
+// reached 6.3 TB/s over 7.5 GB, non-temporal ones 5.4 to 5.7.
 __device__ __forceinline__ u32x4 load_weight(const uint8_t* p) {
-  return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  return *reinterpret_cast<const u32x4*>(p);
 }
 
 // acc[r][g] += the products of the weight rows w[r] and the activation rows
