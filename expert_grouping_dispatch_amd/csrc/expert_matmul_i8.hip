@@ -149,8 +149,8 @@ struct Walk {
 //
 // A step is 128 values of k of 256 rows of both operands, 64 KB, in two
 // buffers that are filled straight from global memory.  A row's 128 bytes lie
-// in LDS as eight 16-byte pieces, piece c at c ^ (row % 8), so that the lanes
-// of a read (consecutive rows, one piece) touch all banks.
+// in LDS as eight 16-byte pieces, piece c at c ^ (row/2 % 8), so that sixteen
+// lanes of a read (consecutive rows, one piece) touch all 64 banks once.
 //
 // A step has four parts of 32 values of k.  The fragments of a part are read
 // while the matrix units work on the part before it; the last part's are in
@@ -163,8 +163,9 @@ struct Walk {
 // same channels, so one lane holds both.
 template <bool kSwiglu>
 __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p) {
-  __shared__ __align__(16) uint8_t s_a[2][kTile * kStepBytes];
-  __shared__ __align__(16) uint8_t s_w[2][kTile * kStepBytes];
+  // Named apart, so that the compiler sees that filling one does not touch the other.
+  __shared__ __align__(16) uint8_t s_a0[kTile * kStepBytes], s_a1[kTile * kStepBytes];
+  __shared__ __align__(16) uint8_t s_w0[kTile * kStepBytes], s_w1[kTile * kStepBytes];
   __shared__ uint32_t s_first[kMaxActive + 1];  // first tile of each active expert
   __shared__ uint32_t s_row[kMaxActive + 1];    // its first row
   __shared__ uint32_t s_scan[kTileThreads / kWave];
@@ -232,8 +233,10 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
   // This wave fills LDS rows [64*wave, +64) of both operands, eight rows an
   // instruction.  Rows past the tile's end are whatever follows it, or nothing
   // past the buffer's end: what they give is not stored.
-  const int piece = (lane % 8) ^ (lane / 8);
-  const uint32_t lane_off = uint32_t(lane / 8) * p.depth + piece * 16;
+  // of an instruction of even and of odd number: the piece this lane fills
+  const int piece[2] = {(lane % 8) ^ (lane / 16), (lane % 8) ^ (4 + lane / 16)};
+  const uint32_t lane_off[2] = {uint32_t(lane / 8) * p.depth + piece[0] * 16,
+                                uint32_t(lane / 8) * p.depth + piece[1] * 16};
   __amdgpu_buffer_rsrc_t a_from, w_from;
   auto aim = [&](const TilePlace& t) {
     const uint64_t a0 = (uint64_t(t.row0) + 64 * wave) * p.depth;
@@ -242,25 +245,22 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
     a_from = buffer_of(reinterpret_cast<const uint8_t*>(p.a) + min(a0, a_bytes), a0 < a_bytes ? a_bytes - a0 : 0);
     w_from = buffer_of(reinterpret_cast<const uint8_t*>(p.w) + min(w0, w_bytes), w0 < w_bytes ? w_bytes - w0 : 0);
   };
-  // A quarter of a step: 16 of this wave's 64 rows of both operands.
-  auto fetch = [&](int s, int buf, int quarter) {
-#pragma unroll
-    for (int i = 2 * quarter; i < 2 * quarter + 2; ++i) {
-      const uint32_t at = uint32_t(s) * kStepBytes + uint32_t(8 * i) * p.depth;
-      load_to_lds(a_from, lane_off, at, &s_a[buf][(64 * wave + 8 * i) * kStepBytes]);
-      load_to_lds(w_from, lane_off, at, &s_w[buf][(64 * wave + 8 * i) * kStepBytes]);
-    }
+  // Eight of this wave's 64 rows of both operands, for a step.
+  auto fetch = [&](int s, uint8_t* to_a, uint8_t* to_w, int i) {
+    const uint32_t at = uint32_t(s) * kStepBytes + uint32_t(8 * i) * p.depth;
+    load_to_lds(a_from, lane_off[i % 2], at, to_a + (64 * wave + 8 * i) * kStepBytes);
+    load_to_lds(w_from, lane_off[i % 2], at, to_w + (64 * wave + 8 * i) * kStepBytes);
   };
   // Waits for this wave's part of the buffer of step s; pieces past the row's
   // end become zeros in the weights, so that they add nothing.
-  auto arrived = [&](int s, int buf) {
+  auto arrived = [&](int s, uint8_t* w) {
     __builtin_amdgcn_s_waitcnt(kWaitLoads);
     asm volatile("" ::: "memory");
     if (ragged && s == steps - 1) {
-      if (s * kStepBytes + piece * 16 >= p.depth) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<u32x4*>(&s_w[buf][(64 * wave + 8 * i) * kStepBytes + lane * 16]) = u32x4{0u, 0u, 0u, 0u};
+      for (int i = 0; i < 8; ++i) {
+        if (s * kStepBytes + piece[i % 2] * 16 >= p.depth)
+          *reinterpret_cast<u32x4*>(w + (64 * wave + 8 * i) * kStepBytes + lane * 16) = u32x4{0u, 0u, 0u, 0u};
       }
     }
     __builtin_amdgcn_s_waitcnt(kWaitLdsScalar);
@@ -289,59 +289,73 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
   const int wr = wave / 2, wc = wave % 2;
   i32x4 fw[2][4], fa[2][4];
   i32x16 acc[4][4];
-  // The products of the fragments in `set`, while part kk of `buf` is read
-  // into the other set and, with kFetch, the next step is requested.
-  auto part = [&](int set, int buf, int kk, auto fetch_too, auto fresh) {
-    const int at = ((kk * 2 + lane / 32) ^ (lane % 8)) * 16;
+  auto read = [&](int set, const uint8_t* a, const uint8_t* w, int kk, int f) {
+    const int at = ((kk * 2 + lane / 32) ^ (lane / 2 % 8)) * 16;
+    fw[set][f] = *reinterpret_cast<const i32x4*>(w + (128 * wc + 32 * f + lane % 32) * kStepBytes + at);
+    fa[set][f] = *reinterpret_cast<const i32x4*>(a + (128 * wr + 32 * f + lane % 32) * kStepBytes + at);
+  };
+  // The products of the fragments in `set`; between them part kk of (a, w) is
+  // read into the other set and, with kHalf >= 0, half of a step is requested
+  // for (to_a, to_w): spread out, because a request holds up the wave that
+  // makes it while the other waves' are being taken.
+  auto part = [&](auto set, const uint8_t* a, const uint8_t* w, int kk, auto half, uint8_t* to_a, uint8_t* to_w,
+                  auto fresh) {
+    constexpr int kSet = decltype(set)::value, kHalf = decltype(half)::value;
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
-      fw[set ^ 1][f] = *reinterpret_cast<const i32x4*>(&s_w[buf][(128 * wc + 32 * f + lane % 32) * kStepBytes + at]);
-      fa[set ^ 1][f] = *reinterpret_cast<const i32x4*>(&s_a[buf][(128 * wr + 32 * f + lane % 32) * kStepBytes + at]);
-    }
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         i32x16 c = acc[f][g];
-        if constexpr (decltype(fresh)::value)
+        if constexpr (decltype(fresh)::value != 0)
 #pragma unroll
           for (int i = 0; i < 16; ++i) c[i] = 0;
-        acc[f][g] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[set][f], fa[set][g], c, 0, 0, 0);
+        acc[f][g] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[kSet][f], fa[kSet][g], c, 0, 0, 0);
+        if (g == 1) {
+          __builtin_amdgcn_sched_barrier(0);
+          read(kSet ^ 1, a, w, kk, f);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
-      if constexpr (decltype(fetch_too)::value) {
-        fetch(fs, buf ^ 1, f);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (kHalf >= 0) {
+        fetch(fs, to_a, to_w, 4 * kHalf + f);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
-  constexpr std::integral_constant<bool, true> yes{};
-  constexpr std::integral_constant<bool, false> no{};
+  constexpr std::integral_constant<int, -1> none{};
+  constexpr std::integral_constant<int, 0> zero{};
+  constexpr std::integral_constant<int, 1> one{};
+
+  // Step s of a tile, in the buffer (a, w); (na, nw) holds the step after it.
+  auto step = [&](int s, uint8_t* a, uint8_t* w, uint8_t* na, uint8_t* nw) {
+    if (s == 0) part(zero, a, w, 1, one, na, nw, one);
+    else part(zero, a, w, 1, one, na, nw, zero);
+    fetched();
+    part(one, a, w, 2, none, na, nw, zero);
+    part(zero, a, w, 3, none, na, nw, zero);
+    arrived(s + 1 < steps ? s + 1 : 0, nw);
+    part(one, na, nw, 0, zero, a, w, zero);
+  };
 
 #pragma unroll
-  for (int q = 0; q < 4; ++q) fetch(fs, 0, q);
+  for (int i = 0; i < 8; ++i) fetch(fs, s_a0, s_w0, i);
   fetched();
-  arrived(0, 0);
+  arrived(0, s_w0);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) fetch(fs, 1, q);
-  fetched();
-  int buf = 0;
+  for (int i = 0; i < 4; ++i) fetch(fs, s_a1, s_w1, i);
 #pragma unroll
-  for (int f = 0; f < 4; ++f) {
-    const int at = ((lane / 32) ^ (lane % 8)) * 16;
-    fw[0][f] = *reinterpret_cast<const i32x4*>(&s_w[0][(128 * wc + 32 * f + lane % 32) * kStepBytes + at]);
-    fa[0][f] = *reinterpret_cast<const i32x4*>(&s_a[0][(128 * wr + 32 * f + lane % 32) * kStepBytes + at]);
-  }
+  for (int f = 0; f < 4; ++f) read(0, s_a0, s_w0, 0, f);
+  bool odd = false;  // whether the tile's first step is in the second buffer
   do {
-    for (int s = 0; s < steps; ++s) {
-      if (s == 0) part(0, buf, 1, no, yes);
-      else part(0, buf, 1, no, no);
-      part(1, buf, 2, no, no);
-      part(0, buf, 3, no, no);
-      arrived(s + 1 < steps ? s + 1 : 0, buf ^ 1);
-      part(1, buf ^ 1, 0, yes, no);
-      fetched();
-      buf ^= 1;
+    int s = 0;
+    if (odd) step(s++, s_a1, s_w1, s_a0, s_w0);
+    for (; s + 1 < steps; s += 2) {
+      step(s, s_a0, s_w0, s_a1, s_w1);
+      step(s + 1, s_a1, s_w1, s_a0, s_w0);
     }
+    odd = s < steps;
+    if (odd) step(s, s_a0, s_w0, s_a1, s_w1);
 
     // Stores go through a buffer of the tile's rows: what a lane has for a row
     // or channel past the end gets an offset past the buffer and is dropped.
