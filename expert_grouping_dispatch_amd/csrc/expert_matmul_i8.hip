@@ -128,6 +128,8 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_
 }
 
 constexpr int kWaitLoads = 0x0F70;     // s_waitcnt vmcnt(0)
+// s_waitcnt vmcnt(n), n <= 63
+constexpr int wait_all_but(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
 constexpr int kWaitLdsScalar = 0xC07F;  // s_waitcnt lgkmcnt(0)
 
 }  // namespace
@@ -168,6 +170,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
   __shared__ __align__(16) uint8_t s_w0[kTile * kStepBytes], s_w1[kTile * kStepBytes];
   __shared__ uint32_t s_first[kMaxActive + 1];  // first tile of each active expert
   __shared__ uint32_t s_row[kMaxActive + 1];    // its first row
+  __shared__ int32_t s_expert[kMaxActive];      // its id
   __shared__ uint32_t s_scan[kTileThreads / kWave];
   const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
   constexpr int kChannels = kSwiglu ? kTile / 2 : kTile;
@@ -182,6 +185,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
     group_rows(p.starts, min(j, p.n_experts - 1), p.a_rows, lo, hi);
     if (j >= p.n_experts) lo = hi;
     s_row[j] = lo;
+    s_expert[j] = j < p.n_experts ? p.expert_ids[j] : -1;
     if (j == kMaxActive - 1) s_row[kMaxActive] = hi;
     tiles[i] = hi - lo > uint32_t(kFewRows) ? ((hi - lo + kTile - 1) / kTile) * col_tiles : 0u;
     sum += tiles[i];
@@ -217,7 +221,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
       const uint32_t in = at.tile - uniform(s_first[at.j]);
       t.row0 = lo + (in % row_tiles) * kTile;
       t.c0 = int(in / row_tiles) * kChannels;
-      t.e = p.expert_ids[at.j];
+      t.e = uniform(s_expert[at.j]);
       if (t.e < 0 || t.e >= p.n_experts || t.row0 >= hi || t.c0 >= p.n_out) continue;
       t.n_rows = int(min(hi - t.row0, uint32_t(kTile)));
       at.tile += grid;
@@ -251,10 +255,17 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
     load_to_lds(a_from, lane_off[i % 2], at, to_a + (64 * wave + 8 * i) * kStepBytes);
     load_to_lds(w_from, lane_off[i % 2], at, to_w + (64 * wave + 8 * i) * kStepBytes);
   };
-  // Waits for this wave's part of the buffer of step s; pieces past the row's
-  // end become zeros in the weights, so that they add nothing.
-  auto arrived = [&](int s, uint8_t* w) {
-    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+  // 32 channels of a fragment: a lane has four of each eight, 8*q + (lane/32)*4 + i.
+  constexpr int kOutFrags = kSwiglu ? 2 : 4, kStores = 8 * kOutFrags;
+  static_assert(kStores + 16 <= 63, "the memory operations after a tile's requests are counted");
+  // Waits for this wave's part of the buffer of step s.  In a tile's first step
+  // that was requested before the stores of the tile before it (kStores of them)
+  // and the loads of this tile's scales (20), which need not be waited for:
+  // memory operations end in order.  Pieces past the
+  // row's end become zeros in the weights, so that they add nothing.
+  auto arrived = [&](int s, uint8_t* w, bool behind) {
+    if (behind) __builtin_amdgcn_s_waitcnt(wait_all_but(kStores + 16));
+    else __builtin_amdgcn_s_waitcnt(kWaitLoads);
     asm volatile("" ::: "memory");
     if (ragged && s == steps - 1) {
 #pragma unroll
@@ -327,27 +338,53 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
   constexpr std::integral_constant<int, 0> zero{};
   constexpr std::integral_constant<int, 1> one{};
 
+  bool stored = false;  // whether a tile was stored before this one
   // Step s of a tile, in the buffer (a, w); (na, nw) holds the step after it.
   auto step = [&](int s, uint8_t* a, uint8_t* w, uint8_t* na, uint8_t* nw) {
-    if (s == 0) part(zero, a, w, 1, one, na, nw, one);
-    else part(zero, a, w, 1, one, na, nw, zero);
-    fetched();
+    if (s == 0) {
+      part(zero, a, w, 1, none, na, nw, one);
+    } else {
+      part(zero, a, w, 1, one, na, nw, zero);
+      fetched();
+    }
     part(one, a, w, 2, none, na, nw, zero);
     part(zero, a, w, 3, none, na, nw, zero);
-    arrived(s + 1 < steps ? s + 1 : 0, nw);
+    arrived(s + 1 < steps ? s + 1 : 0, nw, s == 0 && stored);
     part(one, na, nw, 0, zero, a, w, zero);
   };
 
 #pragma unroll
   for (int i = 0; i < 8; ++i) fetch(fs, s_a0, s_w0, i);
   fetched();
-  arrived(0, s_w0);
+  arrived(0, s_w0, false);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) fetch(fs, s_a1, s_w1, i);
+  for (int i = 0; i < 8; ++i) fetch(fs, s_a1, s_w1, i);
+  fetched();
 #pragma unroll
   for (int f = 0; f < 4; ++f) read(0, s_a0, s_w0, 0, f);
   bool odd = false;  // whether the tile's first step is in the second buffer
   do {
+    // The tile's scales, loaded now for the epilogue.
+    float sa[4];
+    f32x4 s0[4][4];
+    {
+      const __amdgpu_buffer_rsrc_t rows = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<float*>(p.a_scales + now.row0), 0, now.n_rows * 4, 0x00027000);
+      const __amdgpu_buffer_rsrc_t channels = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<float*>(p.w_scales + int64_t(now.e) * wide), 0, wide * 4, 0x00027000);
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        sa[g] = __uint_as_float(
+            __builtin_amdgcn_raw_buffer_load_b32(rows, (128 * wr + 32 * g + lane % 32) * 4, 0, 0));
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int c0 = now.c0 + 32 * kOutFrags * wc + 32 * (f % kOutFrags) + (f < kOutFrags ? 0 : p.n_out);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          s0[f][q] = __builtin_bit_cast(
+              f32x4, __builtin_amdgcn_raw_buffer_load_b128(channels, (c0 + 8 * q + 4 * (lane / 32)) * 4, 0, 0));
+      }
+    }
     int s = 0;
     if (odd) step(s++, s_a1, s_w1, s_a0, s_w0);
     for (; s + 1 < steps; s += 2) {
@@ -356,28 +393,23 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
     }
     odd = s < steps;
     if (odd) step(s, s_a0, s_w0, s_a1, s_w1);
+    // The second half of the request that the last step began: before the stores.
+#pragma unroll
+    for (int i = 4; i < 8; ++i) {
+      if (odd) fetch(fs, s_a0, s_w0, i);
+      else fetch(fs, s_a1, s_w1, i);
+    }
+    fetched();
 
+    stored = true;
     // Stores go through a buffer of the tile's rows: what a lane has for a row
     // or channel past the end gets an offset past the buffer and is dropped.
-    const float* sw = p.w_scales + int64_t(now.e) * wide;
     const uint32_t row_bytes = uint32_t(p.n_out) * 2, out_bytes = uint32_t(now.n_rows) * row_bytes;
     const __amdgpu_buffer_rsrc_t out =
         __builtin_amdgcn_make_buffer_rsrc(p.out + int64_t(now.row0) * p.n_out, 0, out_bytes, 0x00027000);
-    float sa[4];
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
-      sa[g] = p.a_scales[now.row0 + min(128 * wr + 32 * g + lane % 32, now.n_rows - 1)];
-#pragma unroll
-    for (int f = 0; f < (kSwiglu ? 2 : 4); ++f) {
-      // 32 channels; a lane has four of each eight: 8*q + (lane/32)*4 + i
-      const int c0 = now.c0 + (kSwiglu ? 64 : 128) * wc + 32 * f;
-      f32x4 s0[4], s1[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = min(c0 + 8 * q, p.n_out - 8) + 4 * (lane / 32);
-        s0[q] = *reinterpret_cast<const f32x4*>(sw + c);
-        if constexpr (kSwiglu) s1[q] = *reinterpret_cast<const f32x4*>(sw + p.n_out + c);
-      }
+    for (int f = 0; f < kOutFrags; ++f) {
+      const int c0 = now.c0 + 32 * kOutFrags * wc + 32 * f;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         // The sums stay in accumulation registers until their turn.
@@ -389,8 +421,8 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
           float x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            x[i] = scaled(acc[f][g][4 * q + i], sa[g], s0[q][i]);
-            if constexpr (kSwiglu) x[i] = silu_times(x[i], scaled(acc[f + 2][g][4 * q + i], sa[g], s1[q][i]));
+            x[i] = scaled(acc[f][g][4 * q + i], sa[g], s0[f][q][i]);
+            if constexpr (kSwiglu) x[i] = silu_times(x[i], scaled(acc[f + 2][g][4 * q + i], sa[g], s0[f + 2][q][i]));
           }
           v[q] = u32x2{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
         }
