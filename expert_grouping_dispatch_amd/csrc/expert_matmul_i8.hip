@@ -22,7 +22,10 @@ namespace {
 constexpr int kFewRows = 64;
 constexpr int kFewWaves = 4, kFewThreads = kFewWaves * kWave;
 constexpr int kTile = 256, kStepBytes = 128;  // tile edge, and values of k per step
-constexpr int kTileThreads = 256;
+constexpr int kTileThreads = 256, kStripThreads = 256;
+#ifndef MOE_STRIP_MIN
+#define MOE_STRIP_MIN 512
+#endif
 constexpr int kMaxActive = 1024;
 
 // Rows [lo, hi) of active expert j, inside the buffer whatever the starts hold.
@@ -111,7 +114,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void k_matmul_few(ExpertMatmul p) {
   else matmul_few_tile<4, kSwiglu>(p, lo, n, e, c0, s_part);
 }
 
-// ---- tiles ----------------------------------------------------------------------
+// ---- strips ---------------------------------------------------------------------
 
 namespace {
 
@@ -123,8 +126,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* base,
 }
 
 // 64 lanes x 16 bytes from `off` (per lane) + `at` to 1 KB of LDS at `dst`.
+template <bool kNonTemporal = false>
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t off, uint32_t at, uint8_t* dst) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)(dst), 16, off, at, 0, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)(dst), 16, off, at, 0,
+                                           kNonTemporal ? 2 : 0);
 }
 
 constexpr int kWaitLoads = 0x0F70;     // s_waitcnt vmcnt(0)
@@ -133,6 +138,131 @@ constexpr int wait_all_but(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14);
 constexpr int kWaitLdsScalar = 0xC07F;  // s_waitcnt lgkmcnt(0)
 
 }  // namespace
+
+// One workgroup: 256 weight rows (with SwiGLU 128 gate rows and the 128 up rows
+// of the same channels) times the n <= 32*G rows of one group.  Bound by
+// reading the weights: they go to LDS in whole cache lines, non-temporal, and
+// two workgroups a CU with two buffers of a step (128 values of k) each keep
+// about 80 KB a CU on its way.  Layout of a buffer, 16-byte pieces and their
+// order as in k_matmul_tile; each wave takes 64 weight rows (32 gate and 32 up).
+template <int G, bool kSwiglu>
+__device__ __forceinline__ void strip(const ExpertMatmul& p, uint32_t lo, int n, int e, int c0, uint8_t* a0,
+                                      uint8_t* a1, uint8_t* w0, uint8_t* w1) {
+  const int lane = threadIdx.x % kWave, wave = uniform(int(threadIdx.x / kWave));
+  const int wide = kSwiglu ? 2 * p.n_out : p.n_out;
+  const int steps = (p.depth + kStepBytes - 1) / kStepBytes;
+  const bool ragged = p.depth % kStepBytes != 0;
+  const int piece[2] = {(lane % 8) ^ (lane / 16), (lane % 8) ^ (4 + lane / 16)};
+  const uint32_t lane_off[2] = {uint32_t(lane / 8) * p.depth + piece[0] * 16,
+                                uint32_t(lane / 8) * p.depth + piece[1] * 16};
+  // This wave's weight rows: LDS rows [64*wave, +64) are channels c, c+1, .. (32 gate and 32 up with SwiGLU).
+  const int c = c0 + (kSwiglu ? 32 : 64) * wave;
+  const uint64_t a_bytes = uint64_t(p.a_rows - lo) * p.depth, w_rows = uint64_t(p.n_experts) * wide;
+  const uint64_t w_row = uint64_t(e) * wide + min(c, p.n_out);
+  const uint8_t* w = reinterpret_cast<const uint8_t*>(p.w);
+  const __amdgpu_buffer_rsrc_t a_from = buffer_of(reinterpret_cast<const uint8_t*>(p.a) + uint64_t(lo) * p.depth, a_bytes);
+  const __amdgpu_buffer_rsrc_t w_from = buffer_of(w + w_row * p.depth, (w_rows - w_row) * p.depth);
+  const uint64_t up_row = kSwiglu ? w_row + p.n_out : w_row;
+  const __amdgpu_buffer_rsrc_t up_from = buffer_of(w + up_row * p.depth, (w_rows - up_row) * p.depth);
+  auto fetch = [&](int s, uint8_t* to_a, uint8_t* to_w) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = kSwiglu ? 8 * (i % 4) : 8 * i;
+      if (c + r < p.n_out)
+        load_to_lds<true>(kSwiglu && i >= 4 ? up_from : w_from, lane_off[i % 2],
+                          uint32_t(s) * kStepBytes + uint32_t(r) * p.depth, to_w + (64 * wave + 8 * i) * kStepBytes);
+    }
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const int r = 8 * (wave + 4 * i);
+      if (r < n)
+        load_to_lds(a_from, lane_off[wave % 2], uint32_t(s) * kStepBytes + uint32_t(r) * p.depth, to_a + r * kStepBytes);
+    }
+  };
+  i32x16 acc[2][G];
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[f][g][i] = 0;
+  auto step = [&](int s, uint8_t* a, uint8_t* w, uint8_t* next_a, uint8_t* next_w) {
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    asm volatile("" ::: "memory");
+    if (ragged && s == steps - 1) {  // pieces past the row's end add nothing
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (s * kStepBytes + piece[i % 2] * 16 >= p.depth)
+          *reinterpret_cast<u32x4*>(w + (64 * wave + 8 * i) * kStepBytes + lane * 16) = u32x4{0u, 0u, 0u, 0u};
+    }
+    __builtin_amdgcn_s_waitcnt(kWaitLdsScalar);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (s + 1 < steps) fetch(s + 1, next_a, next_w);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const int at = ((kk * 2 + lane / 32) ^ (lane / 2 % 8)) * 16;
+      i32x4 fw[2], fa[G];
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+        fw[f] = *reinterpret_cast<const i32x4*>(w + (64 * wave + 32 * f + lane % 32) * kStepBytes + at);
+#pragma unroll
+      for (int g = 0; g < G; ++g) fa[g] = *reinterpret_cast<const i32x4*>(a + (32 * g + lane % 32) * kStepBytes + at);
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          acc[f][g] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[f], fa[g], acc[f][g], 0, 0, 0);
+    }
+  };
+  fetch(0, a0, w0);
+  for (int s = 0; s < steps; s += 2) {
+    step(s, a0, w0, a1, w1);
+    if (s + 1 < steps) step(s + 1, a1, w1, a0, w0);
+  }
+  const float* sw = p.w_scales + int64_t(e) * wide;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int r = 32 * g + lane % 32;
+    const float sa = p.a_scales[lo + min(r, n - 1)];
+    uint16_t* o = p.out + int64_t(lo + r) * p.n_out;
+#pragma unroll
+    for (int f = 0; f < (kSwiglu ? 1 : 2); ++f)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int ch = c + 32 * f + 8 * q + 4 * (lane / 32);
+        if (r >= n || ch >= p.n_out) continue;
+        const f32x4 s0 = *reinterpret_cast<const f32x4*>(sw + ch);
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = scaled(acc[f][g][4 * q + i], sa, s0[i]);
+        if constexpr (kSwiglu) {
+          const f32x4 s1 = *reinterpret_cast<const f32x4*>(sw + p.n_out + ch);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = silu_times(v[i], scaled(acc[1][g][4 * q + i], sa, s1[i]));
+        }
+        *reinterpret_cast<u32x2*>(o + ch) = u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      }
+  }
+}
+
+template <bool kSwiglu>
+__global__ __launch_bounds__(kStripThreads, 2) void k_matmul_strip(ExpertMatmul p) {
+  __shared__ __align__(16) uint8_t s_a0[kFewRows * kStepBytes], s_a1[kFewRows * kStepBytes];
+  __shared__ __align__(16) uint8_t s_w0[kTile * kStepBytes], s_w1[kTile * kStepBytes];
+  uint32_t lo, hi;
+  group_rows(p.starts, blockIdx.y, p.a_rows, lo, hi);
+  const uint32_t n = hi - lo;
+  if (n == 0 || n > uint32_t(kFewRows)) return;
+  const int e = p.expert_ids[blockIdx.y];
+  if (e < 0 || e >= p.n_experts) return;
+  const int c0 = blockIdx.x * (kSwiglu ? kTile / 2 : kTile);
+  if (n <= 32) strip<1, kSwiglu>(p, lo, n, e, c0, s_a0, s_a1, s_w0, s_w1);
+  else strip<2, kSwiglu>(p, lo, n, e, c0, s_a0, s_a1, s_w0, s_w1);
+}
+
+// ---- tiles ----------------------------------------------------------------------
 
 // A tile: its rows of the buffer, its first output channel, its expert.
 struct TilePlace {
@@ -448,8 +578,12 @@ namespace {
 template <bool kSwiglu>
 hipError_t go(const ExpertMatmul& p, hipStream_t s) {
   const uint32_t groups = p.a_rows < uint32_t(p.n_experts) ? p.a_rows : uint32_t(p.n_experts);
-  const int per = kSwiglu ? 16 : 32;
-  hipLaunchKernelGGL((k_matmul_few<kSwiglu>), dim3((p.n_out + per - 1) / per, groups), dim3(kFewThreads), 0, s, p);
+  const int per = kSwiglu ? 16 : 32, strip = kSwiglu ? kTile / 2 : kTile;
+  const uint32_t strips = (p.n_out + strip - 1) / strip;
+  if (strips * groups >= MOE_STRIP_MIN)
+    hipLaunchKernelGGL((k_matmul_strip<kSwiglu>), dim3(strips, groups), dim3(kStripThreads), 0, s, p);
+  else
+    hipLaunchKernelGGL((k_matmul_few<kSwiglu>), dim3((p.n_out + per - 1) / per, groups), dim3(kFewThreads), 0, s, p);
   if (const hipError_t e = hipGetLastError(); e != hipSuccess || p.a_rows <= uint32_t(kFewRows)) return e;
   hipLaunchKernelGGL((k_matmul_tile<kSwiglu>), dim3(256), dim3(kTileThreads), 0, s, p);
   return hipGetLastError();

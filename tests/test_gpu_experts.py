@@ -157,6 +157,8 @@ CASES = [
     ([0] * 40 + [90, 3] + [0] * 20, 9, 656, 1040),
     ([5] * 300, 11, 80, 64),
     ([70] * 24, 1, 2064, 320),
+    ([2, 33, 64, 17, 1, 32, 48, 0] * 26, 5, 272, 528),
+    ([1, 90, 16, 31] * 40, 0, 128, 1040),
 ]
 
 
