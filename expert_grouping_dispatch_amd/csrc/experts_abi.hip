@@ -15,6 +15,7 @@ using moe::slots_ok;
 
 constexpr int64_t kMaxRows = 0xFFFFFFFEll;
 constexpr int32_t kMaxWidth = 1 << 20;
+constexpr int32_t kMaxFewWidth = 1 << 18;  // MOE_FEW_MAX_SLOTS rows of it stay below 2^31 bytes
 
 bool width_ok(int32_t n) { return n > 0 && n <= kMaxWidth && n % 16 == 0; }
 
@@ -30,7 +31,7 @@ int layer_few(const uint16_t* x, int64_t n_rows, int32_t hidden, int32_t top_k, 
               const void* w_down, const float* down_scales, int32_t inter, uint16_t* output_tokens,
               void* workspace, size_t workspace_bytes, void* stream) {
   const size_t need = moe_layer_few_workspace_bytes(n_rows, top_k, inter);
-  if (need == 0 || !width_ok(hidden) || n_experts < 1 || n_experts > MOE_MAX_EXPERTS || tp_rank < 0)
+  if (need == 0 || !width_ok(hidden) || hidden > kMaxFewWidth || n_experts < 1 || n_experts > MOE_MAX_EXPERTS || tp_rank < 0)
     return MOE_ERR_INVALID_ARGUMENT;
   if (w_gate_up == nullptr || w_down == nullptr || (gate_up_scales == nullptr) != (down_scales == nullptr))
     return MOE_ERR_INVALID_ARGUMENT;
@@ -118,7 +119,7 @@ int moe_expert_matmul_i8(const int8_t* a_q, const float* a_scales, int64_t a_row
 
 size_t moe_layer_few_workspace_bytes(int64_t n_rows, int32_t top_k, int32_t inter) {
   if (n_rows < 0 || top_k < 1 || top_k > MOE_FEW_MAX_SLOTS || n_rows > MOE_FEW_MAX_SLOTS / top_k ||
-      !width_ok(inter))
+      !width_ok(inter) || inter > kMaxFewWidth)
     return 0;
   const size_t bytes = size_t(n_rows) * size_t(top_k) * size_t(inter) * 2;
   return bytes == 0 ? 256 : (bytes + 255) & ~size_t(255);

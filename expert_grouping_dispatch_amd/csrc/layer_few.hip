@@ -17,6 +17,7 @@
 //                are summed in ascending order, so the result does not depend on
 //                which wave came first.
 #include "experts.h"
+#include "lds_fill.h"
 #include "stream.h"
 
 namespace moe {
@@ -45,79 +46,183 @@ __device__ __forceinline__ int expert_of(const IdT* ids, int i, int n_experts) {
 
 // ---- gate, up and their product --------------------------------------------
 
-// NG groups of 16 slots, list[0 .. n), n <= 16*NG.
-template <class C, int NG, bool kScaled>
-__device__ __forceinline__ void few_up_tile(const uint8_t* x, int hidden, int top_k, const uint8_t* w,
-                                            const float* w_scales, int inter, int tile,
-                                            const uint16_t* list, int n, uint16_t* h, f32x4* s_part) {
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int64_t w_row = int64_t(hidden) * (C::kWBytes / 16);
-  const uint8_t* wp[2];
-  const uint8_t* xp[NG];
-  wp[0] = w + int64_t(tile * 16 + lane % 16) * w_row;
-  wp[1] = wp[0] + int64_t(inter) * w_row;
-#pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    const int slot = list[min(g * 16 + lane % 16, n - 1)];
-    xp[g] = x + int64_t(slot / top_k) * hidden * 2;
+constexpr int kUpChannels = 64;  // per workgroup: 64 gate and 64 up rows
+constexpr int kUpWBytes = 2 * kUpChannels * 128, kUpXBytes = 8192;
+
+// A step is 128 bytes of every weight row: 64 values of k in bf16, 128 in
+// int8, against 128 or 256 bytes of every activation row.
+struct UpBf16 {
+  static constexpr int kStep = 64, kXRow = 128, kWSize = 2;
+  // Products of the 16 bytes this lane has of a weight row, piece c of 8, with n activation rows in x.
+  static __device__ __forceinline__ f32x16 mac(const u32x4& w, const uint8_t* x, int row, int c, f32x16 acc) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(x + row * kXRow + (c ^ (row / 2 % 8)) * 16);
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, v), acc, 0,
+                                                   0, 0);
   }
-  f32x4 acc[2][NG];
+};
+struct UpI8 {
+  static constexpr int kStep = 128, kXRow = 256, kWSize = 1;
+  static __device__ __forceinline__ f32x16 mac(const u32x4& w, const uint8_t* x, int row, int c, f32x16 acc) {
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int g = 0; g < NG; ++g) acc[r][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  int begin, end;
-  step_range(hidden, wave, kUpWaves, begin, end);
-  stream_products<C, 2, NG, (NG == 1 ? 4 : NG == 2 ? 2 : 1)>(wp, xp, begin, end, hidden, acc);
-#pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int g = 0; g < NG; ++g) s_part[((wave * 2 + r) * NG + g) * kWave + lane] = acc[r][g];
-  __syncthreads();
-  for (int g = wave; g < NG; g += kUpWaves) {
-    f32x4 sum[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      sum[r] = s_part[(r * NG + g) * kWave + lane];
-#pragma unroll
-      for (int v = 1; v < kUpWaves; ++v) {
-        const f32x4 p = s_part[((v * 2 + r) * NG + g) * kWave + lane];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[r][i] += p[i];
-      }
+    for (int j = 0; j < 2; ++j) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(x + row * kXRow + ((2 * c + j) ^ (row % 16)) * 16);
+      const u32x2 lo = bf16_of_i8(w[2 * j]), hi = bf16_of_i8(w[2 * j + 1]);
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, (u32x4{lo.x, lo.y, hi.x, hi.y})),
+                                                    __builtin_bit_cast(bf16x8, v), acc, 0, 0, 0);
     }
-    const int at = g * 16 + lane % 16, c = tile * 16 + (lane / 16) * 4;
-    if (at < n) {
-      if constexpr (kScaled) {
+    return acc;
+  }
+};
+
+struct UpBuffers {
+  uint8_t *w[3], *xa[3], *xb[3];  // weights; activation rows 0..31 and 32..63
+};
+
+// One expert's gate and up rows of channels [c0, c0 + 64) times n <= 32*G of
+// its slots.  NB buffers of a step are filled straight from global memory, the
+// weights non-temporal and in whole cache lines; each wave takes 16 gate and
+// the 16 up rows of the same channels as one 32-row operand, so one lane has
+// both.  16-byte pieces lie in an order that spreads a read over all banks:
+// piece c of a 128-byte row r at c ^ (r/2 % 8), of a 256-byte row at c ^ (r % 16).
+template <class C, int G, int NB, bool kScaled>
+__device__ __forceinline__ void few_up(const uint8_t* x, int n_rows, int hidden, int top_k, const uint8_t* w,
+                                       uint64_t w_bytes, const float* w_scales, int inter, int c0,
+                                       const uint16_t* list, int n, uint16_t* h, const UpBuffers& buf) {
+  const int lane = threadIdx.x % kWave, wave = uniform(int(threadIdx.x / kWave));
+  constexpr int kXFills = C::kXRow == 128 ? G : 2 * G;  // requests of activation rows per wave and step
+  constexpr int kFills = 4 + kXFills;
+  const uint32_t w_row = uint32_t(hidden) * C::kWSize;
+  const int steps = (hidden + C::kStep - 1) / C::kStep;
+  const bool ragged = hidden % C::kStep != 0;
+  // Weights: LDS rows [32*wave, +32), eight per request: gate rows c, .., c+15, then up rows.
+  const int c = min(c0 + 16 * wave, inter - 16);
+  const uint64_t at_gate = uint64_t(c) * w_row, at_up = uint64_t(inter + c) * w_row;
+  const __amdgpu_buffer_rsrc_t gate = buffer_of(w + at_gate, w_bytes - at_gate);
+  const __amdgpu_buffer_rsrc_t up = buffer_of(w + at_up, w_bytes - at_up);
+  const int w_piece[2] = {(lane % 8) ^ (lane / 16), (lane % 8) ^ (4 + lane / 16)};
+  const uint32_t w_off[2] = {uint32_t(lane / 8) * w_row + w_piece[0] * 16, uint32_t(lane / 8) * w_row + w_piece[1] * 16};
+  // Activations: request i = wave + 4*j fills rows from i*8 (128-byte rows) or i*4.
+  const __amdgpu_buffer_rsrc_t rows = buffer_of(x, uint64_t(n_rows) * hidden * 2);
+  int x_piece[kXFills];
+  uint32_t x_off[kXFills];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sum[0][i] *= w_scales[c + i];
-          sum[1][i] *= w_scales[inter + c + i];
-        }
+  for (int j = 0; j < kXFills; ++j) {
+    const int i = wave + 4 * j;
+    int r;
+    if constexpr (C::kXRow == 128) {
+      r = 8 * i + lane / 8;
+      x_piece[j] = (lane % 8) ^ (r / 2 % 8);
+    } else {
+      r = 4 * i + lane / 16;
+      x_piece[j] = (lane % 16) ^ (r % 16);
+    }
+    x_off[j] = uint32_t(list[min(r, n - 1)] / top_k) * uint32_t(hidden * 2) + x_piece[j] * 16;
+  }
+  // Where request j of the activations goes: 4 KB a half in bf16, 8 KB in int8.
+  constexpr int kHalf = 32 * C::kXRow, kPerHalf = kHalf / 1024;
+  auto x_place = [&](int j, uint8_t* xa, uint8_t* xb) {
+    const int i = wave + 4 * j;
+    return j * 4 < kPerHalf ? xa + i * 1024 : xb + (i - kPerHalf) * 1024;
+  };
+  auto fetch = [&](int s, uint8_t* to_w, uint8_t* xa, uint8_t* xb) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      load_to_lds<true>(i < 2 ? gate : up, w_off[i % 2], uint32_t(s) * 128 + uint32_t(8 * (i % 2)) * w_row,
+                        to_w + (32 * wave + 8 * i) * 128);
+#pragma unroll
+    for (int j = 0; j < kXFills; ++j) load_to_lds(rows, x_off[j], uint32_t(s) * C::kXRow, x_place(j, xa, xb));
+  };
+  f32x16 acc[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[g][i] = 0.0f;
+  auto step = [&](int s, uint8_t* w, uint8_t* xa, uint8_t* xb, uint8_t* next_w, uint8_t* next_xa, uint8_t* next_xb) {
+    if (NB == 3 && s + 1 < steps) __builtin_amdgcn_s_waitcnt(wait_all_but(NB == 3 ? kFills : 0));
+    else __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    asm volatile("" ::: "memory");
+    if (ragged && s == steps - 1) {  // pieces past the rows' end: zeros in both, so that they add nothing
+      const u32x4 zero{0u, 0u, 0u, 0u};
+      const int left = (hidden - s * C::kStep) * C::kWSize, x_left = (hidden - s * C::kStep) * 2;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (w_piece[i % 2] * 16 >= left) *reinterpret_cast<u32x4*>(w + (32 * wave + 8 * i) * 128 + lane * 16) = zero;
+#pragma unroll
+      for (int j = 0; j < kXFills; ++j)
+        if (x_piece[j] * 16 >= x_left) *reinterpret_cast<u32x4*>(x_place(j, xa, xb) + lane * 16) = zero;
+    }
+    __builtin_amdgcn_s_waitcnt(kWaitLdsScalar);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (s + NB - 1 < steps) fetch(s + NB - 1, next_w, next_xa, next_xb);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const int c = 2 * kk + lane / 32, r = 32 * wave + lane % 32;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(w + r * 128 + (c ^ (r / 2 % 8)) * 16);
+#pragma unroll
+      for (int g = 0; g < G; ++g) acc[g] = C::mac(v, g == 0 ? xa : xb, lane % 32, c, acc[g]);
+    }
+  };
+  fetch(0, buf.w[0], buf.xa[0], buf.xb[0]);
+  if (NB == 3 && steps > 1) fetch(1, buf.w[1], buf.xa[1], buf.xb[1]);
+  if constexpr (NB == 3) {
+    for (int s = 0; s < steps; s += 3) {
+      step(s, buf.w[0], buf.xa[0], buf.xb[0], buf.w[2], buf.xa[2], buf.xb[2]);
+      if (s + 1 < steps) step(s + 1, buf.w[1], buf.xa[1], buf.xb[1], buf.w[0], buf.xa[0], buf.xb[0]);
+      if (s + 2 < steps) step(s + 2, buf.w[2], buf.xa[2], buf.xb[2], buf.w[1], buf.xa[1], buf.xb[1]);
+    }
+  } else {
+    for (int s = 0; s < steps; s += 2) {
+      step(s, buf.w[0], buf.xa[0], buf.xb[0], buf.w[1], buf.xa[1], buf.xb[1]);
+      if (s + 1 < steps) step(s + 1, buf.w[1], buf.xa[1], buf.xb[1], buf.w[0], buf.xa[0], buf.xb[0]);
+    }
+  }
+  // This lane's channels: 8*q + 4*(lane/32) + i of the wave's 16, gate in acc[8*.. of q 0, 1], up in q 2, 3.
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int at = 32 * g + lane % 32;
+    if (at >= n) continue;
+    uint16_t* row = h + int64_t(list[at]) * inter;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int ch = c + 8 * q + 4 * (lane / 32);
+      f32x4 sg{1.0f, 1.0f, 1.0f, 1.0f}, su = sg;
+      if constexpr (kScaled) {
+        sg = *reinterpret_cast<const f32x4*>(w_scales + ch);
+        su = *reinterpret_cast<const f32x4*>(w_scales + inter + ch);
       }
       float v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = silu_times(sum[0][i], sum[1][i]);
-      *reinterpret_cast<u32x2*>(h + int64_t(list[at]) * inter + c) =
-          u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      for (int i = 0; i < 4; ++i) {
+        float a = acc[g][4 * q + i], b = acc[g][8 + 4 * q + i];
+        if constexpr (kScaled) {
+          a *= sg[i];
+          b *= su[i];
+        }
+        v[i] = silu_times(a, b);
+      }
+      *reinterpret_cast<u32x2*>(row + ch) = u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
     }
   }
-  __syncthreads();  // s_part is rewritten for the next slots
+  __syncthreads();  // the buffers are filled again for the next slots
 }
 
-// blockIdx.x: tile of 16 channels.  blockIdx.y: the expert, or, when there
-// are fewer slots than experts, a slot, which stands for its expert if it is
-// the first slot on it.
+// blockIdx.x: 64 channels.  blockIdx.y: the expert, or, when there are fewer
+// slots than experts, a slot, which stands for its expert if it is the first
+// slot on it.
 template <class C, bool kScaled, typename IdT>
-__global__ __launch_bounds__(kUpThreads, 4) void k_few_up(const uint8_t* __restrict__ x, int n_rows, int hidden,
-                                                       int top_k, const IdT* __restrict__ ids, PadMask pad,
-                                                       int n_experts, bool by_slot,
-                                                       const uint8_t* __restrict__ w,
-                                                       const float* __restrict__ w_scales, int inter,
-                                                       uint16_t* __restrict__ h) {
+__global__ __launch_bounds__(kUpThreads, 2) void k_few_up(const uint8_t* __restrict__ x, int n_rows, int hidden,
+                                                          int top_k, const IdT* __restrict__ ids, PadMask pad,
+                                                          int n_experts, bool by_slot,
+                                                          const uint8_t* __restrict__ w,
+                                                          const float* __restrict__ w_scales, int inter,
+                                                          uint16_t* __restrict__ h) {
+  // Named apart, so that the compiler sees that filling one does not touch the others.
+  __shared__ __align__(16) uint8_t s_w0[kUpWBytes], s_w1[kUpWBytes], s_w2[kUpWBytes];
+  __shared__ __align__(16) uint8_t s_x0[kUpXBytes], s_x1[kUpXBytes], s_x2[kUpXBytes];
   __shared__ uint16_t s_list[kFewMaxSlots];
   __shared__ int s_n, s_earlier;
-  __shared__ f32x4 s_part[kUpWaves * 2 * kMaxGroups * kWave];
   const int tid = threadIdx.x;
   const int slots = real_slots(pad, n_rows, top_k);
   if (tid == 0) s_n = s_earlier = 0;
@@ -136,17 +241,26 @@ __global__ __launch_bounds__(kUpThreads, 4) void k_few_up(const uint8_t* __restr
   }
   __syncthreads();
   if (s_earlier != 0) return;
-  const int n = s_n;
-  const uint8_t* we = w + int64_t(e) * 2 * inter * hidden * (C::kWBytes / 16);
+  const int total = uniform(s_n);
+  const uint64_t each = uint64_t(2) * inter * hidden * C::kWSize;
+  const uint8_t* we = w + e * each;
   const float* se = kScaled ? w_scales + int64_t(e) * 2 * inter : nullptr;
-  for (int c0 = 0; c0 < n; c0 += 16 * kMaxGroups) {
-    const int m = min(n - c0, 16 * kMaxGroups);
-    if (m <= 16)
-      few_up_tile<C, 1, kScaled>(x, hidden, top_k, we, se, inter, blockIdx.x, s_list + c0, m, h, s_part);
-    else if (m <= 32)
-      few_up_tile<C, 2, kScaled>(x, hidden, top_k, we, se, inter, blockIdx.x, s_list + c0, m, h, s_part);
-    else
-      few_up_tile<C, 4, kScaled>(x, hidden, top_k, we, se, inter, blockIdx.x, s_list + c0, m, h, s_part);
+  const uint64_t w_bytes = (n_experts - e) * each;
+  const int c0 = blockIdx.x * kUpChannels;
+  for (int i = 0; i < total;) {
+    const int n = total - i;
+    if (n <= 32) {
+      const UpBuffers buf{{s_w0, s_w1, s_w2}, {s_x0, s_x1, s_x2}, {s_x0, s_x1, s_x2}};
+      few_up<C, 1, 3, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, n, h, buf);
+    } else if constexpr (C::kXRow == 128) {
+      const UpBuffers buf{{s_w0, s_w1, s_w2}, {s_x0, s_x1, s_x2}, {s_x0 + 4096, s_x1 + 4096, s_x2 + 4096}};
+      few_up<C, 2, 3, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h, buf);
+    } else {
+      // 64 rows of 256 bytes: the third weight buffer and two activation buffers hold them, two steps deep
+      const UpBuffers buf{{s_w0, s_w1, nullptr}, {s_w2, s_x0, nullptr}, {s_w2 + 8192, s_x1, nullptr}};
+      few_up<C, 2, 2, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h, buf);
+    }
+    i += 64;
   }
 }
 
@@ -272,11 +386,12 @@ __global__ __launch_bounds__(kDownThreads, 4) void k_few_down(
 
 namespace {
 
-template <class C, bool kScaled, typename IdT>
+template <class Up, class C, bool kScaled, typename IdT>
 hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
   const int slots = p.n_rows * p.top_k;
   const bool by_slot = slots < p.n_experts;
-  hipLaunchKernelGGL((k_few_up<C, kScaled, IdT>), dim3(p.inter / 16, by_slot ? slots : p.n_experts),
+  hipLaunchKernelGGL((k_few_up<Up, kScaled, IdT>),
+                     dim3((p.inter + kUpChannels - 1) / kUpChannels, by_slot ? slots : p.n_experts),
                      dim3(kUpThreads), 0, s, reinterpret_cast<const uint8_t*>(p.x), p.n_rows, p.hidden, p.top_k,
                      p.ids, p.pad, p.n_experts, by_slot, static_cast<const uint8_t*>(p.w_gate_up),
                      p.gate_up_scales, p.inter, p.h);
@@ -297,7 +412,7 @@ hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
 template <typename IdT>
 hipError_t launch_layer_few(const FewLayer<IdT>& p, hipStream_t s) {
   if (p.n_rows == 0) return hipSuccess;
-  return p.gate_up_scales != nullptr ? go<CoreI8Bf16, true, IdT>(p, s) : go<CoreBf16, false, IdT>(p, s);
+  return p.gate_up_scales != nullptr ? go<UpI8, CoreI8Bf16, true, IdT>(p, s) : go<UpBf16, CoreBf16, false, IdT>(p, s);
 }
 
 template hipError_t launch_layer_few<int32_t>(const FewLayer<int32_t>&, hipStream_t);
