@@ -118,7 +118,7 @@ int moe_expert_matmul_i8(const int8_t* a_q, const float* a_scales, int64_t a_row
 }
 
 size_t moe_layer_few_workspace_bytes(int64_t n_rows, int32_t top_k, int32_t inter) {
-  if (n_rows < 0 || top_k < 1 || top_k > MOE_FEW_MAX_SLOTS || n_rows > MOE_FEW_MAX_SLOTS / top_k ||
+  if (n_rows < 0 || top_k < 1 || top_k > MOE_MAX_TOP_K || n_rows > MOE_FEW_MAX_SLOTS / top_k ||
       !width_ok(inter) || inter > kMaxFewWidth)
     return 0;
   const size_t bytes = size_t(n_rows) * size_t(top_k) * size_t(inter) * 2;

@@ -124,7 +124,7 @@ size_t moe_layer_few_workspace_bytes(int64_t n_rows, int32_t top_k, int32_t inte
  * with fp32 sums.  Tokens without a routed choice are written as +0.
  *
  *   x              [device] bf16 [n_rows, hidden], 16-byte aligned.
- *   n_rows, top_k  n_rows*top_k <= MOE_FEW_MAX_SLOTS, top_k >= 1.
+ *   n_rows, top_k  n_rows*top_k <= MOE_FEW_MAX_SLOTS, 1 <= top_k <= MOE_MAX_TOP_K.
  *   hidden, inter  > 0, multiples of 16, at most 262144.
  *   topk_ids       [device] int32 [n_rows, top_k]; ids outside [0, n_experts)
  *                  are unrouted.  Not modified.
