@@ -75,9 +75,25 @@ struct UpI8 {
   }
 };
 
+#ifndef MOE_UP_DEEP_MAX
+#define MOE_UP_DEEP_MAX 256
+#endif
+constexpr int kUpMost = 6;  // buffers
 struct UpBuffers {
-  uint8_t *w[3], *xa[3], *xb[3];  // weights; activation rows 0..31 and 32..63
+  uint8_t *w[kUpMost], *xa[kUpMost], *xb[kUpMost];  // weights; activation rows 0..31 and 32..63
 };
+
+// Waits until all but the last n groups of kFills requests have arrived, n <= 4.
+template <int kFills>
+__device__ __forceinline__ void wait_fills(int n) {
+  switch (n) {
+    case 0: __builtin_amdgcn_s_waitcnt(wait_all_but(0)); break;
+    case 1: __builtin_amdgcn_s_waitcnt(wait_all_but(kFills)); break;
+    case 2: __builtin_amdgcn_s_waitcnt(wait_all_but(2 * kFills)); break;
+    case 3: __builtin_amdgcn_s_waitcnt(wait_all_but(3 * kFills)); break;
+    default: __builtin_amdgcn_s_waitcnt(wait_all_but(4 * kFills)); break;
+  }
+}
 
 // One expert's gate and up rows of channels [c0, c0 + 64) times n <= 32*G of
 // its slots.  NB buffers of a step are filled straight from global memory, the
@@ -139,8 +155,7 @@ __device__ __forceinline__ void few_up(const uint8_t* x, int n_rows, int hidden,
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[g][i] = 0.0f;
   auto step = [&](int s, uint8_t* w, uint8_t* xa, uint8_t* xb, uint8_t* next_w, uint8_t* next_xa, uint8_t* next_xb) {
-    if (NB == 3 && s + 1 < steps) __builtin_amdgcn_s_waitcnt(wait_all_but(NB == 3 ? kFills : 0));
-    else __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    wait_fills<kFills>(min(NB - 2, steps - 1 - s));
     asm volatile("" ::: "memory");
     if (ragged && s == steps - 1) {  // pieces past the rows' end: zeros in both, so that they add nothing
       const u32x4 zero{0u, 0u, 0u, 0u};
@@ -165,18 +180,16 @@ __device__ __forceinline__ void few_up(const uint8_t* x, int n_rows, int hidden,
       for (int g = 0; g < G; ++g) acc[g] = C::mac(v, g == 0 ? xa : xb, lane % 32, c, acc[g]);
     }
   };
-  fetch(0, buf.w[0], buf.xa[0], buf.xb[0]);
-  if (NB == 3 && steps > 1) fetch(1, buf.w[1], buf.xa[1], buf.xb[1]);
-  if constexpr (NB == 3) {
-    for (int s = 0; s < steps; s += 3) {
-      step(s, buf.w[0], buf.xa[0], buf.xb[0], buf.w[2], buf.xa[2], buf.xb[2]);
-      if (s + 1 < steps) step(s + 1, buf.w[1], buf.xa[1], buf.xb[1], buf.w[0], buf.xa[0], buf.xb[0]);
-      if (s + 2 < steps) step(s + 2, buf.w[2], buf.xa[2], buf.xb[2], buf.w[1], buf.xa[1], buf.xb[1]);
-    }
-  } else {
-    for (int s = 0; s < steps; s += 2) {
-      step(s, buf.w[0], buf.xa[0], buf.xb[0], buf.w[1], buf.xa[1], buf.xb[1]);
-      if (s + 1 < steps) step(s + 1, buf.w[1], buf.xa[1], buf.xb[1], buf.w[0], buf.xa[0], buf.xb[0]);
+#pragma unroll
+  for (int b = 0; b < NB - 1; ++b)
+    if (b < steps) fetch(b, buf.w[b], buf.xa[b], buf.xb[b]);
+  for (int s = 0; s < steps; s += NB) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      constexpr int kBack = NB - 1;
+      const int next = (b + kBack) % NB;
+      if (s + b < steps)
+        step(s + b, buf.w[b], buf.xa[b], buf.xb[b], buf.w[next], buf.xa[next], buf.xb[next]);
     }
   }
   // This lane's channels: 8*q + 4*(lane/32) + i of the wave's 16, gate in acc[8*.. of q 0, 1], up in q 2, 3.
@@ -209,11 +222,14 @@ __device__ __forceinline__ void few_up(const uint8_t* x, int n_rows, int hidden,
   __syncthreads();  // the buffers are filled again for the next slots
 }
 
+// kDeep: six buffers and one workgroup a CU instead of three and two, for
+// grids that do not fill the CUs, which are bound by how long a step takes to
+// arrive (MEASURE_DEEP).
 // blockIdx.x: 64 channels.  blockIdx.y: the expert, or, when there are fewer
 // slots than experts, a slot, which stands for its expert if it is the first
 // slot on it.
-template <class C, bool kScaled, typename IdT>
-__global__ __launch_bounds__(kUpThreads, 2) void k_few_up(const uint8_t* __restrict__ x, int n_rows, int hidden,
+template <class C, bool kDeep, bool kScaled, typename IdT>
+__global__ __launch_bounds__(kUpThreads, (kDeep ? 1 : 2)) void k_few_up(const uint8_t* __restrict__ x, int n_rows, int hidden,
                                                           int top_k, const IdT* __restrict__ ids, PadMask pad,
                                                           int n_experts, bool by_slot,
                                                           const uint8_t* __restrict__ w,
@@ -222,6 +238,10 @@ __global__ __launch_bounds__(kUpThreads, 2) void k_few_up(const uint8_t* __restr
   // Named apart, so that the compiler sees that filling one does not touch the others.
   __shared__ __align__(16) uint8_t s_w0[kUpWBytes], s_w1[kUpWBytes], s_w2[kUpWBytes];
   __shared__ __align__(16) uint8_t s_x0[kUpXBytes], s_x1[kUpXBytes], s_x2[kUpXBytes];
+  constexpr int kMoreW = kDeep ? kUpWBytes : 16, kMoreX = kDeep ? kUpXBytes : 16;
+  __shared__ __align__(16) uint8_t s_w3[kMoreW], s_w4[kMoreW], s_w5[kMoreW];
+  __shared__ __align__(16) uint8_t s_x3[kMoreX], s_x4[kMoreX], s_x5[kMoreX];
+  constexpr int NB = kDeep ? 6 : 3;
   __shared__ uint16_t s_list[kFewMaxSlots];
   __shared__ int s_n, s_earlier;
   const int tid = threadIdx.x;
@@ -250,16 +270,21 @@ __global__ __launch_bounds__(kUpThreads, 2) void k_few_up(const uint8_t* __restr
   const int c0 = blockIdx.x * kUpChannels;
   for (int i = 0; i < total;) {
     const int n = total - i;
+    UpBuffers buf{{s_w0, s_w1, s_w2, s_w3, s_w4, s_w5}, {s_x0, s_x1, s_x2, s_x3, s_x4, s_x5},
+                  {s_x0, s_x1, s_x2, s_x3, s_x4, s_x5}};
     if (n <= 32) {
-      const UpBuffers buf{{s_w0, s_w1, s_w2}, {s_x0, s_x1, s_x2}, {s_x0, s_x1, s_x2}};
-      few_up<C, 1, 3, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, n, h, buf);
+      few_up<C, 1, NB, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, n, h, buf);
     } else if constexpr (C::kXRow == 128) {
-      const UpBuffers buf{{s_w0, s_w1, s_w2}, {s_x0, s_x1, s_x2}, {s_x0 + 4096, s_x1 + 4096, s_x2 + 4096}};
-      few_up<C, 2, 3, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h, buf);
+#pragma unroll
+      for (int b = 0; b < kUpMost; ++b) buf.xb[b] = buf.xa[b] + kUpXBytes / 2;
+      few_up<C, 2, NB, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h, buf);
+    } else if constexpr (kDeep) {
+      // 64 rows of 256 bytes take two activation buffers, or a weight buffer: four steps deep
+      const UpBuffers wide{{s_w0, s_w1, s_w2, s_w3}, {s_x0, s_x2, s_x4, s_w4}, {s_x1, s_x3, s_x5, s_w4 + kUpXBytes}};
+      few_up<C, 2, 4, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h, wide);
     } else {
-      // 64 rows of 256 bytes: the third weight buffer and two activation buffers hold them, two steps deep
-      const UpBuffers buf{{s_w0, s_w1, nullptr}, {s_w2, s_x0, nullptr}, {s_w2 + 8192, s_x1, nullptr}};
-      few_up<C, 2, 2, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h, buf);
+      const UpBuffers wide{{s_w0, s_w1}, {s_w2, s_x0}, {s_w2 + kUpXBytes, s_x1}};
+      few_up<C, 2, 2, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h, wide);
     }
     i += 64;
   }
@@ -503,11 +528,15 @@ template <class Up, class C, bool kScaled, typename IdT>
 hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
   const int slots = p.n_rows * p.top_k;
   const bool by_slot = slots < p.n_experts;
-  hipLaunchKernelGGL((k_few_up<Up, kScaled, IdT>),
-                     dim3((p.inter + kUpChannels - 1) / kUpChannels, by_slot ? slots : p.n_experts),
-                     dim3(kUpThreads), 0, s, reinterpret_cast<const uint8_t*>(p.x), p.n_rows, p.hidden, p.top_k,
-                     p.ids, p.pad, p.n_experts, by_slot, static_cast<const uint8_t*>(p.w_gate_up),
-                     p.gate_up_scales, p.inter, p.h);
+  const dim3 grid((p.inter + kUpChannels - 1) / kUpChannels, by_slot ? slots : p.n_experts);
+#define MOE_GO(DEEP)                                                                                             \
+  hipLaunchKernelGGL((k_few_up<Up, DEEP, kScaled, IdT>), grid, dim3(kUpThreads), 0, s,                           \
+                     reinterpret_cast<const uint8_t*>(p.x), p.n_rows, p.hidden, p.top_k, p.ids, p.pad,           \
+                     p.n_experts, by_slot, static_cast<const uint8_t*>(p.w_gate_up), p.gate_up_scales, p.inter, \
+                     p.h)
+  if (int64_t(grid.x) * grid.y <= MOE_UP_DEEP_MAX) MOE_GO(true);
+  else MOE_GO(false);
+#undef MOE_GO
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   // Room for the results of the slots of a chunk, and for several parts of k while that stays within 512 slots' room.
   const int chunk = slots <= kDownSlots ? slots : kDownSlots / p.top_k * p.top_k;
