@@ -26,9 +26,7 @@ namespace {
 
 constexpr int kFewMaxSlots = 2048;
 constexpr int kUpWaves = 4, kUpThreads = kUpWaves * kWave;
-constexpr int kDownWaves = 8, kDownThreads = kDownWaves * kWave;
 constexpr int kDownSlots = 1024;  // slots at a time in k_few_down: 64 KB of results, two workgroups a CU
-constexpr int kMaxGroups = 4;  // 16 slots each, per pass over the weights
 
 // Slots at or past the boundary row are unrouted.
 __device__ __forceinline__ int real_slots(const PadMask& pad, int n_rows, int top_k) {
@@ -77,6 +75,9 @@ struct UpI8 {
 
 #ifndef MOE_UP_DEEP_MAX
 #define MOE_UP_DEEP_MAX 256
+#endif
+#ifndef MOE_DOWN_WIDE_MIN
+#define MOE_DOWN_WIDE_MIN 6144
 #endif
 constexpr int kUpMost = 6;  // buffers
 struct UpBuffers {
@@ -292,28 +293,34 @@ __global__ __launch_bounds__(kUpThreads, (kDeep ? 1 : 2)) void k_few_up(const ui
 
 // ---- down and the weighted sum ------------------------------------------------
 
-template <class C, int NG>
-__device__ __forceinline__ void few_down_tile(const uint8_t* h, int inter, const uint8_t* w, const uint16_t* list, int n, int begin, int end, int base,
+template <class C, int RT, int NG>
+__device__ __forceinline__ void few_down_tile(const uint8_t* h, int inter, const uint8_t* w, int w_rows,
+                                              const uint16_t* list, int n, int begin, int end, int base,
                                               f32x4* s_y) {
   const int lane = threadIdx.x % kWave;
-  const uint8_t* wp[1] = {w + int64_t(lane % 16) * inter * (C::kWBytes / 16)};
+  const uint8_t* wp[RT];
   const uint8_t* hp[NG];
-  f32x4 acc[1][NG];
+  f32x4 acc[RT][NG];
 #pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    hp[g] = h + int64_t(list[min(g * 16 + lane % 16, n - 1)]) * inter * 2;
-    acc[0][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int r = 0; r < RT; ++r) {
+    wp[r] = w + int64_t(min(16 * r, w_rows - 16) + lane % 16) * inter * (C::kWBytes / 16);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) acc[r][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  stream_products<C, 1, NG, (NG == 2 ? 2 : 1)>(wp, hp, begin, end, inter, acc);
+#pragma unroll
+  for (int g = 0; g < NG; ++g) hp[g] = h + int64_t(list[min(g * 16 + lane % 16, n - 1)]) * inter * 2;
+  stream_products<C, RT, NG, 1>(wp, hp, begin, end, inter, acc);
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     const int at = g * 16 + lane % 16;
-    if (at < n) s_y[(int(list[at]) - base) * 4 + lane / 16] = acc[0][g];
+    if (at < n)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) s_y[((int(list[at]) - base) * RT + r) * 4 + lane / 16] = acc[r][g];
   }
 }
 
 // The results of experts with 16 or fewer slots.  `find(item)` gives an item's
-// rows and range of steps; items first, first + kDownWaves, .. below `items`
+// rows and range of steps; items first, first + NW, .. below `items`
 // are taken, those with more slots passed over.  Two batches of U steps are in
 // registers or on their way, weights and activations together (loads end in
 // order, so activations requested later would wait for the next weights); the
@@ -321,14 +328,14 @@ __device__ __forceinline__ void few_down_tile(const uint8_t* h, int inter, const
 // stream of weights does not stop at an expert's end.  Past the last item, and
 // in columns without a slot, requests point past their buffer and read nothing.
 struct DownItem {
-  const uint8_t* w;      // the expert's 16 rows of weights
+  const uint8_t* w;      // the expert's rows of weights, 16 for each of RT
   const uint16_t* list;  // its slots
   f32x4* y;              // where the results of this part of k go
   int n, begin, end;
 };
-template <class C, int U, class Find>
-__device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_bytes, int inter, int base, int first,
-                                                int items, Find find) {
+template <class C, int RT, int NW, int U, class Find>
+__device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_bytes, int inter, int w_rows, int base,
+                                                int first, int items, Find find) {
   const int lane = threadIdx.x % kWave, group = lane / 16;
   constexpr int WV = C::kWBytes / 16, XV = C::kXBytes / 16;
   const uint32_t w_row = uint32_t(inter) * WV, nowhere = 0x80000000u;
@@ -338,30 +345,34 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
     int at, s;
   };
   auto turn = [&](Walk& k) {  // to the next item; at >= items when there is none
-    do k.at += kDownWaves;
+    do k.at += NW;
     while (k.at < items && !find(k.at, k.i));
     k.s = k.i.begin;
   };
   Walk ask, form;
-  ask.at = first - kDownWaves;
+  ask.at = first - NW;
   turn(ask);
   if (ask.at >= items) return;
   form = ask;
-  const uint32_t w_lane = uint32_t(lane % 16) * w_row + group * C::kWBytes;
+  uint32_t w_lane[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) w_lane[r] = uint32_t(16 * r + lane % 16) * w_row + group * C::kWBytes;
   auto row_of = [&](const DownItem& i) {
     return lane % 16 < i.n ? uint32_t(i.list[lane % 16]) * uint32_t(inter * 2) + group * C::kXBytes : nowhere;
   };
   uint32_t x_lane = row_of(ask.i);
-  auto request = [&](typename C::W(&w)[U], typename C::X(&x)[U]) {
+  auto request = [&](typename C::W(&w)[U][RT], typename C::X(&x)[U]) {
     const bool live = ask.at < items;
-    const __amdgpu_buffer_rsrc_t from = buffer_of(ask.i.w, uint64_t(16) * w_row);
+    const __amdgpu_buffer_rsrc_t from = buffer_of(ask.i.w, uint64_t(w_rows) * w_row);
     if (live && ask.s + U <= ask.i.end && (ask.s + U) * kStreamStep <= inter) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int v = 0; v < WV; ++v)
-          w[u].v[v] = __builtin_amdgcn_raw_buffer_load_b128(from, w_lane + 4 * C::kWBytes * u + 16 * v,
-                                                            ask.s * 4 * C::kWBytes, 0);
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int v = 0; v < WV; ++v)
+            w[u][r].v[v] = __builtin_amdgcn_raw_buffer_load_b128(from, w_lane[r] + 4 * C::kWBytes * u + 16 * v,
+                                                                 ask.s * 4 * C::kWBytes, 0);
 #pragma unroll
         for (int v = 0; v < XV; ++v)
           x[u].v[v] = __builtin_amdgcn_raw_buffer_load_b128(rows, x_lane + 4 * C::kXBytes * u + 16 * v,
@@ -373,9 +384,11 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
         const int s = ask.s + u;
         const bool some = live && s < ask.i.end && s * kStreamStep + group * 16 < inter;
 #pragma unroll
-        for (int v = 0; v < WV; ++v)
-          w[u].v[v] = __builtin_amdgcn_raw_buffer_load_b128(
-              from, some ? w_lane + uint32_t(s) * 4 * C::kWBytes + 16 * v : nowhere, 0, 0);
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int v = 0; v < WV; ++v)
+            w[u][r].v[v] = __builtin_amdgcn_raw_buffer_load_b128(
+                from, some ? w_lane[r] + uint32_t(s) * 4 * C::kWBytes + 16 * v : nowhere, 0, 0);
 #pragma unroll
         for (int v = 0; v < XV; ++v)
           x[u].v[v] = __builtin_amdgcn_raw_buffer_load_b128(
@@ -388,18 +401,28 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
       if (ask.at < items) x_lane = row_of(ask.i);
     }
   };
-  f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
-  auto products = [&](const typename C::W(&w)[U], const typename C::X(&x)[U]) {
+  f32x4 acc[RT];
+  auto clear = [&] {
 #pragma unroll
-    for (int u = 0; u < U; ++u) acc = C::mac(w[u], x[u], acc);
+    for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  clear();
+  auto products = [&](const typename C::W(&w)[U][RT], const typename C::X(&x)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[r] = C::mac(w[u][r], x[u], acc[r]);
     form.s += U;
     if (form.s >= form.i.end) {
-      if (lane % 16 < form.i.n) form.i.y[(int(form.i.list[lane % 16]) - base) * 4 + group] = acc;
-      acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (lane % 16 < form.i.n)
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          form.i.y[((int(form.i.list[lane % 16]) - base) * RT + r) * 4 + group] = acc[r];
+      clear();
       turn(form);
     }
   };
-  typename C::W w0[U], w1[U];
+  typename C::W w0[U][RT], w1[U][RT];
   typename C::X x0[U], x1[U];
   request(w0, x0);
   request(w1, x1);
@@ -412,11 +435,11 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
   }
 }
 
-// s_y (dynamic LDS): parts x chunk slots x 16 channels of fp32.  Slots are
+// s_y (dynamic LDS): parts x chunk slots x 16*RT channels of fp32.  Slots are
 // taken `chunk` at a time, a whole number of tokens; with more than one chunk
 // an expert's weights are read for each that has a slot on it.
-template <class C, bool kScaled, typename IdT>
-__global__ __launch_bounds__(kDownThreads, 4) void k_few_down(
+template <class C, int RT, int NW, bool kScaled, typename IdT>
+__global__ __launch_bounds__(NW * kWave, 4) void k_few_down(
     const uint8_t* __restrict__ h, int n_rows, int hidden, int top_k, const IdT* __restrict__ ids,
     const float* __restrict__ router_weights, PadMask pad, int n_experts, const uint8_t* __restrict__ w,
     const float* __restrict__ w_scales, int inter, int chunk, int max_parts, uint16_t* __restrict__ out) {
@@ -424,41 +447,44 @@ __global__ __launch_bounds__(kDownThreads, 4) void k_few_down(
   __shared__ uint32_t s_count[1024];  // slots per expert, then their first place in s_list
   __shared__ uint16_t s_list[kDownSlots];
   __shared__ uint16_t s_expert[1024], s_start[1025];  // active experts
-  __shared__ uint32_t s_scan[kDownWaves];
+  __shared__ uint32_t s_scan[NW];
+  constexpr int kThreads = NW * kWave, kQuads = 4 * RT;
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int all = n_rows * top_k, routed_end = real_slots(pad, n_rows, top_k);
+  const int c0 = blockIdx.x * 16 * RT, w_rows = min(16 * RT, hidden - c0);
+  constexpr int kBatch = 64 / (C::kWBytes * RT);  // steps: 4 KB of weights a wave
   for (int base = 0; base < all; base += chunk) {
     const int end = min(base + chunk, all), slots = min(end, routed_end);
-    constexpr int kOwn = kDownSlots / kDownThreads;
-    for (int e = tid; e < n_experts; e += kDownThreads) s_count[e] = 0;
+    constexpr int kOwn = kDownSlots / kThreads;
+    for (int e = tid; e < n_experts; e += kThreads) s_count[e] = 0;
     __syncthreads();
     int own_e[kOwn];
     uint32_t own_rank[kOwn];
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-      const int slot = base + tid + i * kDownThreads;
+      const int slot = base + tid + i * kThreads;
       own_e[i] = slot < slots ? expert_of(ids, slot, n_experts) : -1;
       if (own_e[i] >= 0) own_rank[i] = atomicAdd(&s_count[own_e[i]], 1u);
     }
     __syncthreads();
     // Each lane scans two experts: slots in the low half, active experts in the high.
-    const uint32_t c0 = 2 * tid < n_experts ? s_count[2 * tid] : 0u;
-    const uint32_t c1 = 2 * tid + 1 < n_experts ? s_count[2 * tid + 1] : 0u;
-    const uint32_t v0 = c0 | (c0 != 0 ? 0x10000u : 0u), v1 = c1 | (c1 != 0 ? 0x10000u : 0u);
+    const uint32_t n0 = 2 * tid < n_experts ? s_count[2 * tid] : 0u;
+    const uint32_t n1 = 2 * tid + 1 < n_experts ? s_count[2 * tid + 1] : 0u;
+    const uint32_t v0 = n0 | (n0 != 0 ? 0x10000u : 0u), v1 = n1 | (n1 != 0 ? 0x10000u : 0u);
     const uint32_t sum = wave_inclusive_sum(v0 + v1);
     if (lane == kWave - 1) s_scan[wave] = sum;
     __syncthreads();
     uint32_t before = sum - v0 - v1, total = 0;
-    for (int i = 0; i < kDownWaves; ++i) {
+    for (int i = 0; i < NW; ++i) {
       if (i < wave) before += s_scan[i];
       total += s_scan[i];
     }
     const int active = uniform(int(total >> 16)), routed = int(total & 0xFFFFu);
-    if (c0 != 0) {
+    if (n0 != 0) {
       s_expert[before >> 16] = uint16_t(2 * tid);
       s_start[before >> 16] = uint16_t(before);
     }
-    if (c1 != 0) {
+    if (n1 != 0) {
       s_expert[(before + v0) >> 16] = uint16_t(2 * tid + 1);
       s_start[(before + v0) >> 16] = uint16_t(before + v0);
     }
@@ -468,44 +494,45 @@ __global__ __launch_bounds__(kDownThreads, 4) void k_few_down(
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kOwn; ++i)
-      if (own_e[i] >= 0) s_list[s_count[own_e[i]] + own_rank[i]] = uint16_t(base + tid + i * kDownThreads);
+      if (own_e[i] >= 0) s_list[s_count[own_e[i]] + own_rank[i]] = uint16_t(base + tid + i * kThreads);
     __syncthreads();
 
     // With fewer experts than waves, k is split so that every wave has work; every part has a step.
     int parts = 1;
-    while (parts * 2 <= max_parts && parts * 2 * kStreamStep <= inter && parts * active < 2 * kDownWaves) parts *= 2;
+    while (parts * 2 <= max_parts && parts * 2 * kStreamStep <= inter && parts * active < 2 * NW) parts *= 2;
     auto find = [&](int item, DownItem& i) {
       const int a = item / parts, p = item - a * parts;
       const int first = uniform(s_start[a]);
       i.n = uniform(s_start[a + 1]) - first;
       i.list = s_list + first;
-      i.w = w + (int64_t(uniform(s_expert[a])) * hidden + blockIdx.x * 16) * inter * (C::kWBytes / 16);
-      i.y = s_y + p * chunk * 4;
+      i.w = w + (int64_t(uniform(s_expert[a])) * hidden + c0) * inter * (C::kWBytes / 16);
+      i.y = s_y + p * chunk * kQuads;
       step_range(inter, p, parts, i.begin, i.end);
       return i.n <= 16;
     };
-    few_down_stream<C, 64 / C::kWBytes>(h, uint64_t(all) * inter * 2, inter, base, uniform(wave), active * parts, find);
-    for (int item = uniform(wave); item < active * parts; item += kDownWaves) {  // more than 16 slots
+    few_down_stream<C, RT, NW, kBatch>(h, uint64_t(all) * inter * 2, inter, w_rows, base, uniform(wave),
+                                       active * parts, find);
+    for (int item = uniform(wave); item < active * parts; item += NW) {  // more than 16 slots
       DownItem i;
       if (find(item, i)) continue;
-      for (int j = 0; j < i.n; j += 16 * kMaxGroups) {
-        const int m = min(i.n - j, 16 * kMaxGroups);
-        if (m <= 32) few_down_tile<C, 2>(h, inter, i.w, i.list + j, m, i.begin, i.end, base, i.y);
-        else few_down_tile<C, 4>(h, inter, i.w, i.list + j, m, i.begin, i.end, base, i.y);
-      }
+      constexpr int kGroups = 4 / RT;  // 16 slots each, per pass over the weights
+      for (int j = 0; j < i.n; j += 16 * kGroups)
+        few_down_tile<C, RT, kGroups>(h, inter, i.w, w_rows, i.list + j, min(i.n - j, 16 * kGroups), i.begin, i.end,
+                                      base, i.y);
     }
     __syncthreads();
 
-    for (int i = tid; i < (end - base) / top_k * 4; i += kDownThreads) {
-      const int t = base / top_k + i / 4, quad = i % 4, c = blockIdx.x * 16 + quad * 4;
+    for (int i = tid; i < (end - base) / top_k * kQuads; i += kThreads) {
+      const int t = base / top_k + i / kQuads, quad = i % kQuads, c = c0 + quad * 4;
+      if (c >= hidden) continue;
       float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int j = 0; j < top_k; ++j) {
         const int slot = t * top_k + j;
         const int e = slot < slots ? expert_of(ids, slot, n_experts) : -1;
         if (e < 0) continue;
-        f32x4 y = s_y[(slot - base) * 4 + quad];
+        f32x4 y = s_y[(slot - base) * kQuads + quad];
         for (int p = 1; p < parts; ++p) {
-          const f32x4 v = s_y[(p * chunk + slot - base) * 4 + quad];
+          const f32x4 v = s_y[(p * chunk + slot - base) * kQuads + quad];
 #pragma unroll
           for (int q = 0; q < 4; ++q) y[q] += v[q];
         }
@@ -541,12 +568,16 @@ hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
   // Room for the results of the slots of a chunk, and for several parts of k while that stays within 512 slots' room.
   const int chunk = slots <= kDownSlots ? slots : kDownSlots / p.top_k * p.top_k;
   int max_parts = 1;
-  while (max_parts < kDownWaves && max_parts * 2 * chunk <= 512) max_parts *= 2;
+  while (max_parts < 8 && max_parts * 2 * chunk <= 512) max_parts *= 2;
   const size_t lds = size_t(max_parts) * chunk * 16 * sizeof(float);
-  hipLaunchKernelGGL((k_few_down<C, kScaled, IdT>), dim3(p.hidden / 16), dim3(kDownThreads), lds, s,
-                     reinterpret_cast<const uint8_t*>(p.h), p.n_rows, p.hidden, p.top_k, p.ids, p.router_weights,
-                     p.pad, p.n_experts, static_cast<const uint8_t*>(p.w_down), p.down_scales, p.inter, chunk,
-                     max_parts, p.out);
+#define MOE_GO(RT, NW)                                                                                              \
+  hipLaunchKernelGGL((k_few_down<C, RT, NW, kScaled, IdT>), dim3((p.hidden + 16 * RT - 1) / (16 * RT)),             \
+                     dim3(NW * kWave), lds * RT, s, reinterpret_cast<const uint8_t*>(p.h), p.n_rows, p.hidden,      \
+                     p.top_k, p.ids, p.router_weights, p.pad, p.n_experts, static_cast<const uint8_t*>(p.w_down),   \
+                     p.down_scales, p.inter, chunk, max_parts, p.out)
+  if (p.hidden >= MOE_DOWN_WIDE_MIN) MOE_GO(2, 16);
+  else MOE_GO(1, 8);
+#undef MOE_GO
   return hipGetLastError();
 }
 

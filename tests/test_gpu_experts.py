@@ -262,6 +262,9 @@ LAYERS = [
     (3, 6, 1024, 32, 16, "mixed"),
     (2048, 1, 2, 16, 32, "mixed"),
     (5, 2, 40, 2064, 1040, "distinct"),
+    (12, 3, 10, 6160, 80, "mixed"),
+    (400, 3, 6, 6160, 48, "mixed"),
+    (130, 8, 300, 6144, 16, "distinct"),
 ]
 
 
