@@ -320,7 +320,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
   const uint32_t first = xcd * per + min(xcd, rest) + blockIdx.x / 8;
 
   // The walk's next tile with work; false when there is none left.
-  auto advance = [&](Walk& at, TilePlace& t) {
+  auto advance = [&](Walk& at, TilePlace& t) __attribute__((always_inline)) {
     for (; at.tile < total; at.tile += grid) {
       while (at.j + 1 < kMaxActive && uniform(s_first[at.j + 1]) <= at.tile) ++at.j;
       const uint32_t lo = uniform(s_row[at.j]), hi = max(min(uniform(s_row[at.j + 1]), p.a_rows), lo);
@@ -341,38 +341,58 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
   const int wide = kSwiglu ? 2 * p.n_out : p.n_out;
   const int steps = (p.depth + kStepBytes - 1) / kStepBytes;
   const bool ragged = p.depth % kStepBytes != 0;
-  const uint64_t a_bytes = uint64_t(p.a_rows) * p.depth, w_bytes = uint64_t(p.n_experts) * wide * p.depth;
+  const uint64_t w_bytes = uint64_t(p.n_experts) * wide * p.depth;
   // This wave fills LDS rows [64*wave, +64) of both operands, eight rows an
-  // instruction.  Rows past the tile's end are whatever follows it, or nothing
-  // past the buffer's end: what they give is not stored.
+  // instruction.  Rows past the tile's end lie past its buffer and are not
+  // read; weight rows past the expert's end are the next one's, or nothing: what
+  // they give is not stored.
   // of an instruction of even and of odd number: the piece this lane fills
   const int piece[2] = {(lane % 8) ^ (lane / 16), (lane % 8) ^ (4 + lane / 16)};
   const uint32_t lane_off[2] = {uint32_t(lane / 8) * p.depth + piece[0] * 16,
                                 uint32_t(lane / 8) * p.depth + piece[1] * 16};
   __amdgpu_buffer_rsrc_t a_from, w_from;
-  auto aim = [&](const TilePlace& t) {
-    const uint64_t a0 = (uint64_t(t.row0) + 64 * wave) * p.depth;
+  auto aim = [&](const TilePlace& t) __attribute__((always_inline)) {
+    const int rows = max(t.n_rows - 64 * wave, 0);
+    const uint64_t a0 = (uint64_t(t.row0) + (rows > 0 ? 64 * wave : 0)) * p.depth;
     const int first_w = t.c0 + (kSwiglu ? 64 * (wave / 2) + (wave % 2) * p.n_out : 64 * wave);
     const uint64_t w0 = (uint64_t(t.e) * wide + first_w) * p.depth;
-    a_from = buffer_of(reinterpret_cast<const uint8_t*>(p.a) + min(a0, a_bytes), a0 < a_bytes ? a_bytes - a0 : 0);
+    a_from = buffer_of(reinterpret_cast<const uint8_t*>(p.a) + a0, uint64_t(rows) * p.depth);
     w_from = buffer_of(reinterpret_cast<const uint8_t*>(p.w) + min(w0, w_bytes), w0 < w_bytes ? w_bytes - w0 : 0);
   };
+  // `ahead` is the tile being fetched, up to two steps in front of `now`, the
+  // tile being formed; each walks the tiles on its own.  Past the last tile
+  // its steps are fetched again, for nothing.
+  TilePlace now, ahead;
+  Walk at_now{first, 0}, at_ahead{first, 0};
+  if (!advance(at_now, now)) return;
+  advance(at_ahead, ahead);
+  aim(ahead);
+  int fs = 0;  // the next step of `ahead` to fetch
+  auto fetched = [&]() __attribute__((always_inline)) {
+    if (++fs == steps) {
+      fs = 0;
+      if (advance(at_ahead, ahead)) aim(ahead);
+      __builtin_amdgcn_s_waitcnt(kWaitLdsScalar);
+    }
+  };
+
   // Eight of this wave's 64 rows of both operands, for a step.
-  auto fetch = [&](int s, uint8_t* to_a, uint8_t* to_w, int i) {
+  auto fetch = [&](int s, uint8_t* to_a, uint8_t* to_w, int i) __attribute__((always_inline)) {
     const uint32_t at = uint32_t(s) * kStepBytes + uint32_t(8 * i) * p.depth;
     load_to_lds(a_from, lane_off[i % 2], at, to_a + (64 * wave + 8 * i) * kStepBytes);
     load_to_lds(w_from, lane_off[i % 2], at, to_w + (64 * wave + 8 * i) * kStepBytes);
   };
-  // 32 channels of a fragment: a lane has four of each eight, 8*q + (lane/32)*4 + i.
-  constexpr int kOutFrags = kSwiglu ? 2 : 4, kStores = 8 * kOutFrags;
-  static_assert(kStores + 16 <= 63, "the memory operations after a tile's requests are counted");
   // Waits for this wave's part of the buffer of step s.  In a tile's first step
-  // that was requested before the stores of the tile before it (kStores of them)
-  // and the loads of this tile's scales (20), which need not be waited for:
-  // memory operations end in order.  Pieces past the
-  // row's end become zeros in the weights, so that they add nothing.
-  auto arrived = [&](int s, uint8_t* w, bool behind) {
-    if (behind) __builtin_amdgcn_s_waitcnt(wait_all_but(kStores + 16));
+  // that was requested before the stores of the tile before it (`stored` of
+  // them) and the loads of this tile's scales (18 or 20), which need not be
+  // waited for: memory operations end in order.  Pieces past the row's end
+  // become zeros in the weights, so that they add nothing.
+  // Fragments of 32 channels for each wave; a lane has four of each eight, 8*q + (lane/32)*4 + i.
+  constexpr int kOutFrags = kSwiglu ? 2 : 4;
+  static_assert(8 * kOutFrags + 16 <= 63, "s_waitcnt counts to 63");
+  auto arrived = [&](int s, uint8_t* w, int stored) __attribute__((always_inline)) {
+    if (stored == 8 * kOutFrags) __builtin_amdgcn_s_waitcnt(wait_all_but(8 * kOutFrags + 16));
+    else if (stored == 4 * kOutFrags) __builtin_amdgcn_s_waitcnt(wait_all_but(4 * kOutFrags + 16));
     else __builtin_amdgcn_s_waitcnt(kWaitLoads);
     asm volatile("" ::: "memory");
     if (ragged && s == steps - 1) {
@@ -388,92 +408,26 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
     asm volatile("" ::: "memory");
   };
 
-  // `ahead` is the tile being fetched, up to two steps in front of `now`, the
-  // tile being formed; each walks the tiles on its own.  Past the last tile
-  // its steps are fetched again, for nothing.
-  TilePlace now, ahead;
-  Walk at_now{first, 0}, at_ahead{first, 0};
-  if (!advance(at_now, now)) return;
-  advance(at_ahead, ahead);
-  aim(ahead);
-  int fs = 0;  // the next step of `ahead` to fetch
-  auto fetched = [&] {
-    if (++fs == steps) {
-      fs = 0;
-      if (advance(at_ahead, ahead)) aim(ahead);
-      __builtin_amdgcn_s_waitcnt(kWaitLdsScalar);
-    }
-  };
-
   const int wr = wave / 2, wc = wave % 2;
-  i32x4 fw[2][4], fa[2][4];
-  i32x16 acc[4][4];
-  auto read = [&](int set, const uint8_t* a, const uint8_t* w, int kk, int f) {
-    const int at = ((kk * 2 + lane / 32) ^ (lane / 2 % 8)) * 16;
-    fw[set][f] = *reinterpret_cast<const i32x4*>(w + (128 * wc + 32 * f + lane % 32) * kStepBytes + at);
-    fa[set][f] = *reinterpret_cast<const i32x4*>(a + (128 * wr + 32 * f + lane % 32) * kStepBytes + at);
-  };
-  // The products of the fragments in `set`; between them part kk of (a, w) is
-  // read into the other set and, with kHalf >= 0, half of a step is requested
-  // for (to_a, to_w): spread out, because a request holds up the wave that
-  // makes it while the other waves' are being taken.
-  auto part = [&](auto set, const uint8_t* a, const uint8_t* w, int kk, auto half, uint8_t* to_a, uint8_t* to_w,
-                  auto fresh) {
-    constexpr int kSet = decltype(set)::value, kHalf = decltype(half)::value;
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        i32x16 c = acc[f][g];
-        if constexpr (decltype(fresh)::value != 0)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) c[i] = 0;
-        acc[f][g] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[kSet][f], fa[kSet][g], c, 0, 0, 0);
-        if (g == 1) {
-          __builtin_amdgcn_sched_barrier(0);
-          read(kSet ^ 1, a, w, kk, f);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (kHalf >= 0) {
-        fetch(fs, to_a, to_w, 4 * kHalf + f);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-  };
   constexpr std::integral_constant<int, -1> none{};
   constexpr std::integral_constant<int, 0> zero{};
   constexpr std::integral_constant<int, 1> one{};
 
-  bool stored = false;  // whether a tile was stored before this one
-  // Step s of a tile, in the buffer (a, w); (na, nw) holds the step after it.
-  auto step = [&](int s, uint8_t* a, uint8_t* w, uint8_t* na, uint8_t* nw) {
-    if (s == 0) {
-      part(zero, a, w, 1, none, na, nw, one);
-    } else {
-      part(zero, a, w, 1, one, na, nw, zero);
-      fetched();
-    }
-    part(one, a, w, 2, none, na, nw, zero);
-    part(zero, a, w, 3, none, na, nw, zero);
-    arrived(s + 1 < steps ? s + 1 : 0, nw, s == 0 && stored);
-    part(one, na, nw, 0, zero, a, w, zero);
-  };
-
 #pragma unroll
   for (int i = 0; i < 8; ++i) fetch(fs, s_a0, s_w0, i);
   fetched();
-  arrived(0, s_w0, false);
+  arrived(0, s_w0, 0);
 #pragma unroll
   for (int i = 0; i < 8; ++i) fetch(fs, s_a1, s_w1, i);
   fetched();
-#pragma unroll
-  for (int f = 0; f < 4; ++f) read(0, s_a0, s_w0, 0, f);
   bool odd = false;  // whether the tile's first step is in the second buffer
-  do {
+  int stored = 0;    // the stores of the tile before this one, of each wave
+
+  // A tile of up to 64*G rows, 32*G for each wave.
+  auto form = [&](auto frags) __attribute__((always_inline)) {
+    constexpr int G = decltype(frags)::value;
     // The tile's scales, loaded now for the epilogue.
-    float sa[4];
+    float sa[G];
     f32x4 s0[4][4];
     {
       const __amdgpu_buffer_rsrc_t rows = __builtin_amdgcn_make_buffer_rsrc(
@@ -481,9 +435,9 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
       const __amdgpu_buffer_rsrc_t channels = __builtin_amdgcn_make_buffer_rsrc(
           const_cast<float*>(p.w_scales + int64_t(now.e) * wide), 0, wide * 4, 0x00027000);
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
+      for (int g = 0; g < G; ++g)
         sa[g] = __uint_as_float(
-            __builtin_amdgcn_raw_buffer_load_b32(rows, (128 * wr + 32 * g + lane % 32) * 4, 0, 0));
+            __builtin_amdgcn_raw_buffer_load_b32(rows, (32 * G * wr + 32 * g + lane % 32) * 4, 0, 0));
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
         const int c0 = now.c0 + 32 * kOutFrags * wc + 32 * (f % kOutFrags) + (f < kOutFrags ? 0 : p.n_out);
@@ -493,8 +447,64 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
               f32x4, __builtin_amdgcn_raw_buffer_load_b128(channels, (c0 + 8 * q + 4 * (lane / 32)) * 4, 0, 0));
       }
     }
+    i32x4 fw[2][4], fa[2][G];
+    i32x16 acc[4][G];
+    auto read = [&](int set, const uint8_t* a, const uint8_t* w, int kk, int f) __attribute__((always_inline)) {
+      const int at = ((kk * 2 + lane / 32) ^ (lane / 2 % 8)) * 16;
+      fw[set][f] = *reinterpret_cast<const i32x4*>(w + (128 * wc + 32 * f + lane % 32) * kStepBytes + at);
+      if (f < G) fa[set][f] = *reinterpret_cast<const i32x4*>(a + (32 * G * wr + 32 * f + lane % 32) * kStepBytes + at);
+    };
+    // The products of the fragments in `set`; between them part kk of (a, w) is
+    // read into the other set and, with kHalf >= 0, half of a step is requested
+    // for (to_a, to_w): spread out, because a request holds up the wave that
+    // makes it while the other waves' are being taken.
+    auto part = [&](auto set, const uint8_t* a, const uint8_t* w, int kk, auto half, uint8_t* to_a, uint8_t* to_w,
+                    auto fresh) __attribute__((always_inline)) {
+      constexpr int kSet = decltype(set)::value, kHalf = decltype(half)::value;
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          i32x16 c = acc[f][g];
+          if constexpr (decltype(fresh)::value != 0)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) c[i] = 0;
+          acc[f][g] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[kSet][f], fa[kSet][g], c, 0, 0, 0);
+          if (g == G / 2 - 1) {
+            __builtin_amdgcn_sched_barrier(0);
+            read(kSet ^ 1, a, w, kk, f);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (kHalf >= 0) {
+          fetch(fs, to_a, to_w, 4 * kHalf + f);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    };
+    // Step s of the tile, in the buffer (a, w); (na, nw) holds the step after it.
+    auto step = [&](int s, uint8_t* a, uint8_t* w, uint8_t* na, uint8_t* nw) __attribute__((always_inline)) {
+      if (s == 0) {
+        part(zero, a, w, 1, none, na, nw, one);
+      } else {
+        part(zero, a, w, 1, one, na, nw, zero);
+        fetched();
+      }
+      part(one, a, w, 2, none, na, nw, zero);
+      part(zero, a, w, 3, none, na, nw, zero);
+      arrived(s + 1 < steps ? s + 1 : 0, nw, s == 0 ? stored : 0);
+      part(one, na, nw, 0, zero, a, w, zero);
+    };
     int s = 0;
-    if (odd) step(s++, s_a1, s_w1, s_a0, s_w0);
+    if (odd) {
+#pragma unroll
+      for (int f = 0; f < 4; ++f) read(0, s_a1, s_w1, 0, f);
+      step(s++, s_a1, s_w1, s_a0, s_w0);
+    } else {
+#pragma unroll
+      for (int f = 0; f < 4; ++f) read(0, s_a0, s_w0, 0, f);
+    }
     for (; s + 1 < steps; s += 2) {
       step(s, s_a0, s_w0, s_a1, s_w1);
       step(s + 1, s_a1, s_w1, s_a0, s_w0);
@@ -509,7 +519,6 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
     }
     fetched();
 
-    stored = true;
     // Stores go through a buffer of the tile's rows: what a lane has for a row
     // or channel past the end gets an offset past the buffer and is dropped.
     const uint32_t row_bytes = uint32_t(p.n_out) * 2, out_bytes = uint32_t(now.n_rows) * row_bytes;
@@ -519,7 +528,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
     for (int f = 0; f < kOutFrags; ++f) {
       const int c0 = now.c0 + 32 * kOutFrags * wc + 32 * f;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
+      for (int g = 0; g < G; ++g) {
         // The sums stay in accumulation registers until their turn.
         asm volatile("" : "+a"(acc[f][g]));
         if constexpr (kSwiglu) asm volatile("" : "+a"(acc[f + 2][g]));
@@ -536,7 +545,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
         }
         // Lanes l and l+32 hold the two halves of each eight channels of one
         // row: the lower one takes all of the even q, the upper of the odd.
-        const int r = 128 * wr + 32 * g + lane % 32;
+        const int r = 32 * G * wr + 32 * g + lane % 32;
         const uint32_t at = uint32_t(r) * row_bytes + uint32_t(c0 + 8 * (lane / 32)) * 2;
 #pragma unroll
         for (int q = 0; q < 4; q += 2) {
@@ -547,6 +556,11 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
         __builtin_amdgcn_sched_barrier(0);  // one fragment at a time, or the registers do not suffice
       }
     }
+    stored = 2 * kOutFrags * G;
+  };
+  do {
+    if (now.n_rows > kTile / 2) form(std::integral_constant<int, 4>{});
+    else form(std::integral_constant<int, 2>{});
   } while (advance(at_now, now));
   __builtin_amdgcn_s_waitcnt(kWaitLoads);  // nothing may still be on its way to LDS
 }
