@@ -24,6 +24,7 @@ constexpr int kFewRows = 64;
 constexpr int kFewWaves = 4, kFewThreads = kFewWaves * kWave;
 constexpr int kTile = 256, kStepBytes = 128;  // tile edge, and values of k per step
 constexpr int kTileThreads = 256, kStripThreads = 256;
+constexpr int kStripFrags = 2;  // of 32 weight rows, for each wave
 #ifndef MOE_STRIP_MIN
 #define MOE_STRIP_MIN 512
 #endif
@@ -117,15 +118,16 @@ __global__ __launch_bounds__(kFewThreads, 4) void k_matmul_few(ExpertMatmul p) {
 
 // ---- strips ---------------------------------------------------------------------
 
-// One workgroup: 256 weight rows (with SwiGLU 128 gate rows and the 128 up rows
-// of the same channels) times the n <= 32*G rows of one group.  Bound by
-// reading the weights: they go to LDS in whole cache lines, non-temporal, and
-// two workgroups a CU with two buffers of a step (128 values of k) each keep
-// about 80 KB a CU on its way.  Layout of a buffer, 16-byte pieces and their
-// order as in k_matmul_tile; each wave takes 64 weight rows (32 gate and 32 up).
+// One workgroup: 128*F weight rows (with SwiGLU half of them gate rows, half
+// the up rows of the same channels) times the n <= 32*G rows of one group.
+// Bound by reading the weights: they go to LDS in whole cache lines,
+// non-temporal, in two buffers of a step (128 values of k).  Layout of a
+// buffer, 16-byte pieces and their order as in k_matmul_tile; each wave takes
+// 32*F weight rows, with SwiGLU first its gate and then its up rows.
 template <int G, bool kSwiglu>
 __device__ __forceinline__ void strip(const ExpertMatmul& p, uint32_t lo, int n, int e, int c0, uint8_t* a0,
                                       uint8_t* a1, uint8_t* w0, uint8_t* w1) {
+  constexpr int F = kStripFrags;
   const int lane = threadIdx.x % kWave, wave = uniform(int(threadIdx.x / kWave));
   const int wide = kSwiglu ? 2 * p.n_out : p.n_out;
   const int steps = (p.depth + kStepBytes - 1) / kStepBytes;
@@ -133,8 +135,9 @@ __device__ __forceinline__ void strip(const ExpertMatmul& p, uint32_t lo, int n,
   const int piece[2] = {(lane % 8) ^ (lane / 16), (lane % 8) ^ (4 + lane / 16)};
   const uint32_t lane_off[2] = {uint32_t(lane / 8) * p.depth + piece[0] * 16,
                                 uint32_t(lane / 8) * p.depth + piece[1] * 16};
-  // This wave's weight rows: LDS rows [64*wave, +64) are channels c, c+1, .. (32 gate and 32 up with SwiGLU).
-  const int c = c0 + (kSwiglu ? 32 : 64) * wave;
+  // This wave's weight rows, LDS rows [32*F*wave, +32*F): channels c, c+1, ..
+  constexpr int kWaveChannels = kSwiglu ? 16 * F : 32 * F;
+  const int c = c0 + kWaveChannels * wave;
   const uint64_t a_bytes = uint64_t(p.a_rows - lo) * p.depth, w_rows = uint64_t(p.n_experts) * wide;
   const uint64_t w_row = uint64_t(e) * wide + min(c, p.n_out);
   const uint8_t* w = reinterpret_cast<const uint8_t*>(p.w);
@@ -142,13 +145,13 @@ __device__ __forceinline__ void strip(const ExpertMatmul& p, uint32_t lo, int n,
   const __amdgpu_buffer_rsrc_t w_from = buffer_of(w + w_row * p.depth, (w_rows - w_row) * p.depth);
   const uint64_t up_row = kSwiglu ? w_row + p.n_out : w_row;
   const __amdgpu_buffer_rsrc_t up_from = buffer_of(w + up_row * p.depth, (w_rows - up_row) * p.depth);
-  auto fetch = [&](int s, uint8_t* to_a, uint8_t* to_w) {
+  auto fetch = [&](int s, uint8_t* to_a, uint8_t* to_w) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = kSwiglu ? 8 * (i % 4) : 8 * i;
+    for (int i = 0; i < 4 * F; ++i) {
+      const int r = kSwiglu ? 8 * (i % (2 * F)) : 8 * i;
       if (c + r < p.n_out)
-        load_to_lds<true>(kSwiglu && i >= 4 ? up_from : w_from, lane_off[i % 2],
-                          uint32_t(s) * kStepBytes + uint32_t(r) * p.depth, to_w + (64 * wave + 8 * i) * kStepBytes);
+        load_to_lds<true>(kSwiglu && i >= 2 * F ? up_from : w_from, lane_off[i % 2],
+                          uint32_t(s) * kStepBytes + uint32_t(r) * p.depth, to_w + (32 * F * wave + 8 * i) * kStepBytes);
     }
 #pragma unroll
     for (int i = 0; i < G; ++i) {
@@ -157,21 +160,21 @@ __device__ __forceinline__ void strip(const ExpertMatmul& p, uint32_t lo, int n,
         load_to_lds(a_from, lane_off[wave % 2], uint32_t(s) * kStepBytes + uint32_t(r) * p.depth, to_a + r * kStepBytes);
     }
   };
-  i32x16 acc[2][G];
+  i32x16 acc[F][G];
 #pragma unroll
-  for (int f = 0; f < 2; ++f)
+  for (int f = 0; f < F; ++f)
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[f][g][i] = 0;
-  auto step = [&](int s, uint8_t* a, uint8_t* w, uint8_t* next_a, uint8_t* next_w) {
+  auto step = [&](int s, uint8_t* a, uint8_t* w, uint8_t* next_a, uint8_t* next_w) __attribute__((always_inline)) {
     __builtin_amdgcn_s_waitcnt(kWaitLoads);
     asm volatile("" ::: "memory");
     if (ragged && s == steps - 1) {  // pieces past the row's end add nothing
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 4 * F; ++i)
         if (s * kStepBytes + piece[i % 2] * 16 >= p.depth)
-          *reinterpret_cast<u32x4*>(w + (64 * wave + 8 * i) * kStepBytes + lane * 16) = u32x4{0u, 0u, 0u, 0u};
+          *reinterpret_cast<u32x4*>(w + (32 * F * wave + 8 * i) * kStepBytes + lane * 16) = u32x4{0u, 0u, 0u, 0u};
     }
     __builtin_amdgcn_s_waitcnt(kWaitLdsScalar);
     asm volatile("" ::: "memory");
@@ -181,14 +184,14 @@ __device__ __forceinline__ void strip(const ExpertMatmul& p, uint32_t lo, int n,
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       const int at = ((kk * 2 + lane / 32) ^ (lane / 2 % 8)) * 16;
-      i32x4 fw[2], fa[G];
+      i32x4 fw[F], fa[G];
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
-        fw[f] = *reinterpret_cast<const i32x4*>(w + (64 * wave + 32 * f + lane % 32) * kStepBytes + at);
+      for (int f = 0; f < F; ++f)
+        fw[f] = *reinterpret_cast<const i32x4*>(w + (32 * F * wave + 32 * f + lane % 32) * kStepBytes + at);
 #pragma unroll
       for (int g = 0; g < G; ++g) fa[g] = *reinterpret_cast<const i32x4*>(a + (32 * g + lane % 32) * kStepBytes + at);
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
+      for (int f = 0; f < F; ++f)
 #pragma unroll
         for (int g = 0; g < G; ++g)
           acc[f][g] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[f], fa[g], acc[f][g], 0, 0, 0);
@@ -199,6 +202,8 @@ __device__ __forceinline__ void strip(const ExpertMatmul& p, uint32_t lo, int n,
     step(s, a0, w0, a1, w1);
     if (s + 1 < steps) step(s + 1, a1, w1, a0, w0);
   }
+  // A lane's weight rows: 8*q + 4*(lane/32) + i of each 32.  With SwiGLU the
+  // second half of the wave's rows are the up rows of the first half's channels.
   const float* sw = p.w_scales + int64_t(e) * wide;
 #pragma unroll
   for (int g = 0; g < G; ++g) {
@@ -206,36 +211,36 @@ __device__ __forceinline__ void strip(const ExpertMatmul& p, uint32_t lo, int n,
     const float sa = p.a_scales[lo + min(r, n - 1)];
     uint16_t* o = p.out + int64_t(lo + r) * p.n_out;
 #pragma unroll
-    for (int f = 0; f < (kSwiglu ? 1 : 2); ++f)
+    for (int k = 0; k < kWaveChannels / 8; ++k) {  // eight channels, four of them this lane's
+      constexpr int kUp = kSwiglu ? 2 * F : 0;     // eights from a gate row to its up row
+      const int ch = c + 8 * k + 4 * (lane / 32);
+      if (r >= n || ch >= p.n_out) continue;
+      const f32x4 s0 = *reinterpret_cast<const f32x4*>(sw + ch);
+      float v[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int ch = c + 32 * f + 8 * q + 4 * (lane / 32);
-        if (r >= n || ch >= p.n_out) continue;
-        const f32x4 s0 = *reinterpret_cast<const f32x4*>(sw + ch);
-        float v[4];
+      for (int i = 0; i < 4; ++i) v[i] = scaled(acc[k / 4][g][4 * (k % 4) + i], sa, s0[i]);
+      if constexpr (kSwiglu) {
+        const f32x4 s1 = *reinterpret_cast<const f32x4*>(sw + p.n_out + ch);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = scaled(acc[f][g][4 * q + i], sa, s0[i]);
-        if constexpr (kSwiglu) {
-          const f32x4 s1 = *reinterpret_cast<const f32x4*>(sw + p.n_out + ch);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = silu_times(v[i], scaled(acc[1][g][4 * q + i], sa, s1[i]));
-        }
-        *reinterpret_cast<u32x2*>(o + ch) = u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+        for (int i = 0; i < 4; ++i)
+          v[i] = silu_times(v[i], scaled(acc[(k + kUp) / 4][g][4 * ((k + kUp) % 4) + i], sa, s1[i]));
       }
+      *reinterpret_cast<u32x2*>(o + ch) = u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+    }
   }
 }
 
 template <bool kSwiglu>
 __global__ __launch_bounds__(kStripThreads, 2) void k_matmul_strip(ExpertMatmul p) {
   __shared__ __align__(16) uint8_t s_a0[kFewRows * kStepBytes], s_a1[kFewRows * kStepBytes];
-  __shared__ __align__(16) uint8_t s_w0[kTile * kStepBytes], s_w1[kTile * kStepBytes];
+  __shared__ __align__(16) uint8_t s_w0[128 * kStripFrags * kStepBytes], s_w1[128 * kStripFrags * kStepBytes];
   uint32_t lo, hi;
   group_rows(p.starts, blockIdx.y, p.a_rows, lo, hi);
   const uint32_t n = hi - lo;
   if (n == 0 || n > uint32_t(kFewRows)) return;
   const int e = p.expert_ids[blockIdx.y];
   if (e < 0 || e >= p.n_experts) return;
-  const int c0 = blockIdx.x * (kSwiglu ? kTile / 2 : kTile);
+  const int c0 = blockIdx.x * (kSwiglu ? 64 * kStripFrags : 128 * kStripFrags);
   if (n <= 32) strip<1, kSwiglu>(p, lo, n, e, c0, s_a0, s_a1, s_w0, s_w1);
   else strip<2, kSwiglu>(p, lo, n, e, c0, s_a0, s_a1, s_w0, s_w1);
 }
@@ -570,7 +575,7 @@ namespace {
 template <bool kSwiglu>
 hipError_t go(const ExpertMatmul& p, hipStream_t s) {
   const uint32_t groups = p.a_rows < uint32_t(p.n_experts) ? p.a_rows : uint32_t(p.n_experts);
-  const int per = kSwiglu ? 16 : 32, strip = kSwiglu ? kTile / 2 : kTile;
+  const int per = kSwiglu ? 16 : 32, strip = (kSwiglu ? 64 : 128) * kStripFrags;
   const uint32_t strips = (p.n_out + strip - 1) / strip;
   if (strips * groups >= MOE_STRIP_MIN)
     hipLaunchKernelGGL((k_matmul_strip<kSwiglu>), dim3(strips, groups), dim3(kStripThreads), 0, s, p);
