@@ -51,7 +51,7 @@ struct FewLayer {
   const float* down_scales;
   int inter;
   uint16_t* out;
-  uint16_t* h;  // [n_rows*top_k, inter], the workspace
+  uint16_t* h;  // two [n_rows*top_k, inter], the workspace
 };
 template <typename IdT>
 hipError_t launch_layer_few(const FewLayer<IdT>& p, hipStream_t s);

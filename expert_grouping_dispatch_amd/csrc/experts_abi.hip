@@ -15,7 +15,7 @@ using moe::slots_ok;
 
 constexpr int64_t kMaxRows = 0xFFFFFFFEll;
 constexpr int32_t kMaxWidth = 1 << 20;
-constexpr int32_t kMaxFewWidth = 1 << 18;  // MOE_FEW_MAX_SLOTS rows of it stay below 2^31 bytes
+constexpr int32_t kMaxFewWidth = 1 << 17;  // 4 bytes each of MOE_FEW_MAX_SLOTS rows stay below 2^31
 
 bool width_ok(int32_t n) { return n > 0 && n <= kMaxWidth && n % 16 == 0; }
 
@@ -121,7 +121,7 @@ size_t moe_layer_few_workspace_bytes(int64_t n_rows, int32_t top_k, int32_t inte
   if (n_rows < 0 || top_k < 1 || top_k > MOE_MAX_TOP_K || n_rows > MOE_FEW_MAX_SLOTS / top_k ||
       !width_ok(inter) || inter > kMaxFewWidth)
     return 0;
-  const size_t bytes = size_t(n_rows) * size_t(top_k) * size_t(inter) * 2;
+  const size_t bytes = size_t(n_rows) * size_t(top_k) * size_t(inter) * 4;
   return bytes == 0 ? 256 : (bytes + 255) & ~size_t(255);
 }
 

@@ -6,16 +6,18 @@
 // They go straight to registers (stream.h); grouping costs each workgroup one
 // pass over the few ids instead of a kernel of its own.
 //
-//   k_few_up     one workgroup per (expert, 16 intermediate channels): lists the
-//                expert's slots, forms gate and up for up to 64 slots at a time
-//                with k split over the waves, joins the parts in LDS and writes
-//                h = silu(gate)*up as bf16, the type the second product's
-//                matrix instruction takes.
-//   k_few_down   one workgroup per 16 output channels: groups all slots, its
-//                waves take (expert, part of k) items, every slot's result goes
-//                to its own place in LDS in fp32, and then each token's choices
-//                are summed in ascending order, so the result does not depend on
-//                which wave came first.
+//   k_few_up     one workgroup per (expert, 64 intermediate channels): lists the
+//                expert's slots and forms gate, up and h = silu(gate)*up for up to
+//                64 of them at a time.  h goes out in bf16, the type of the second
+//                product's matrix instruction, with what bf16 leaves of it beside.
+//   k_few_down   one workgroup per 16 or 32 output channels: groups the slots, its
+//                waves take (expert, part of k) items, every slot's result goes to
+//                its own place in LDS in fp32, and then each token's choices are
+//                summed in ascending order, so the result does not depend on which
+//                wave came first.  The instruction has 16 columns; an expert with
+//                up to eight slots uses the others for what bf16 left of h, which
+//                costs nothing and halves the error of the whole layer; with more
+//                slots h is what bf16 holds.
 #include "experts.h"
 #include "lds_fill.h"
 #include "stream.h"
@@ -73,13 +75,22 @@ struct UpI8 {
   }
 };
 
-#ifndef MOE_UP_DEEP_MAX
-#define MOE_UP_DEEP_MAX 256
-#endif
-#ifndef MOE_DOWN_WIDE_MIN
-#define MOE_DOWN_WIDE_MIN 6144
-#endif
+// Grids of k_few_up up to this many workgroups have six buffers and a CU each.
+constexpr int kUpDeepMax = 256;
+// Layers of at least this many output channels take 32 a workgroup in
+// k_few_down, which loads the activations half as often: 7168 channels, 256
+// experts in int8, 776 slots: 1733 us for the layer against 1939 us with 16.
+// Narrower ones would leave CUs idle: 4096 channels, one token in bf16: 142 us
+// against 124 us.
+constexpr int kDownWideMin = 6144;
 constexpr int kUpMost = 6;  // buffers
+// What bf16 leaves of two values whose bf16 forms are `hi`, in bf16; nothing
+// where that is infinite or NaN.
+__device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t hi) {
+  const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xFFFF0000u);
+  return bf16_pair(fabsf(ra) < INFINITY ? ra : 0.0f, fabsf(rb) < INFINITY ? rb : 0.0f);
+}
+
 struct UpBuffers {
   uint8_t *w[kUpMost], *xa[kUpMost], *xb[kUpMost];  // weights; activation rows 0..31 and 32..63
 };
@@ -105,7 +116,7 @@ __device__ __forceinline__ void wait_fills(int n) {
 template <class C, int G, int NB, bool kScaled>
 __device__ __forceinline__ void few_up(const uint8_t* x, int n_rows, int hidden, int top_k, const uint8_t* w,
                                        uint64_t w_bytes, const float* w_scales, int inter, int c0,
-                                       const uint16_t* list, int n, uint16_t* h, const UpBuffers& buf) {
+                                       const uint16_t* list, int n, uint16_t* h, int64_t h_rest, const UpBuffers& buf) {
   const int lane = threadIdx.x % kWave, wave = uniform(int(threadIdx.x / kWave));
   constexpr int kXFills = C::kXRow == 128 ? G : 2 * G;  // requests of activation rows per wave and step
   constexpr int kFills = 4 + kXFills;
@@ -217,7 +228,9 @@ __device__ __forceinline__ void few_up(const uint8_t* x, int n_rows, int hidden,
         }
         v[i] = silu_times(a, b);
       }
-      *reinterpret_cast<u32x2*>(row + ch) = u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      const u32x2 hi{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      *reinterpret_cast<u32x2*>(row + ch) = hi;
+      *reinterpret_cast<u32x2*>(row + h_rest + ch) = u32x2{rest_pair(v[0], v[1], hi.x), rest_pair(v[2], v[3], hi.y)};
     }
   }
   __syncthreads();  // the buffers are filled again for the next slots
@@ -264,6 +277,7 @@ __global__ __launch_bounds__(kUpThreads, (kDeep ? 1 : 2)) void k_few_up(const ui
   __syncthreads();
   if (s_earlier != 0) return;
   const int total = uniform(s_n);
+  const int64_t h_rest = int64_t(n_rows) * top_k * inter;
   const uint64_t each = uint64_t(2) * inter * hidden * C::kWSize;
   const uint8_t* we = w + e * each;
   const float* se = kScaled ? w_scales + int64_t(e) * 2 * inter : nullptr;
@@ -274,18 +288,21 @@ __global__ __launch_bounds__(kUpThreads, (kDeep ? 1 : 2)) void k_few_up(const ui
     UpBuffers buf{{s_w0, s_w1, s_w2, s_w3, s_w4, s_w5}, {s_x0, s_x1, s_x2, s_x3, s_x4, s_x5},
                   {s_x0, s_x1, s_x2, s_x3, s_x4, s_x5}};
     if (n <= 32) {
-      few_up<C, 1, NB, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, n, h, buf);
+      few_up<C, 1, NB, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, n, h, h_rest, buf);
     } else if constexpr (C::kXRow == 128) {
 #pragma unroll
       for (int b = 0; b < kUpMost; ++b) buf.xb[b] = buf.xa[b] + kUpXBytes / 2;
-      few_up<C, 2, NB, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h, buf);
+      few_up<C, 2, NB, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h,
+                                  h_rest, buf);
     } else if constexpr (kDeep) {
       // 64 rows of 256 bytes take two activation buffers, or a weight buffer: four steps deep
       const UpBuffers wide{{s_w0, s_w1, s_w2, s_w3}, {s_x0, s_x2, s_x4, s_w4}, {s_x1, s_x3, s_x5, s_w4 + kUpXBytes}};
-      few_up<C, 2, 4, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h, wide);
+      few_up<C, 2, 4, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h,
+                                 h_rest, wide);
     } else {
       const UpBuffers wide{{s_w0, s_w1}, {s_w2, s_x0}, {s_w2 + kUpXBytes, s_x1}};
-      few_up<C, 2, 2, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h, wide);
+      few_up<C, 2, 2, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h,
+                                 h_rest, wide);
     }
     i += 64;
   }
@@ -319,26 +336,29 @@ __device__ __forceinline__ void few_down_tile(const uint8_t* h, int inter, const
   }
 }
 
-// The results of experts with 16 or fewer slots.  `find(item)` gives an item's
+// The results of experts with 16 or fewer slots.  Up to eight slots have two
+// of the 16 columns each, their h in bf16 and, h_bytes/2 further, what bf16 left
+// of it; the columns' sums are added at the end.  `find(item)` gives an item's
 // rows and range of steps; items first, first + NW, .. below `items`
 // are taken, those with more slots passed over.  Two batches of U steps are in
 // registers or on their way, weights and activations together (loads end in
 // order, so activations requested later would wait for the next weights); the
 // requests walk on from expert to expert ahead of the products, so that the
 // stream of weights does not stop at an expert's end.  Past the last item, and
-// in columns without a slot, requests point past their buffer and read nothing.
+// in columns without one, requests point past their buffer and read nothing.
 struct DownItem {
   const uint8_t* w;      // the expert's rows of weights, 16 for each of RT
   const uint16_t* list;  // its slots
   f32x4* y;              // where the results of this part of k go
   int n, begin, end;
 };
+constexpr int kDppRowShl8 = 0x108;  // lane l of 16 reads lane l + 8, the upper eight read 0
 template <class C, int RT, int NW, int U, class Find>
 __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_bytes, int inter, int w_rows, int base,
                                                 int first, int items, Find find) {
   const int lane = threadIdx.x % kWave, group = lane / 16;
   constexpr int WV = C::kWBytes / 16, XV = C::kXBytes / 16;
-  const uint32_t w_row = uint32_t(inter) * WV, nowhere = 0x80000000u;
+  const uint32_t w_row = uint32_t(inter) * WV, nowhere = 0x80000000u, rest = uint32_t(h_bytes / 2);
   const __amdgpu_buffer_rsrc_t rows = buffer_of(h, h_bytes);
   struct Walk {
     DownItem i;
@@ -357,8 +377,11 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
   uint32_t w_lane[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) w_lane[r] = uint32_t(16 * r + lane % 16) * w_row + group * C::kWBytes;
+  const int column = lane % 16;
   auto row_of = [&](const DownItem& i) {
-    return lane % 16 < i.n ? uint32_t(i.list[lane % 16]) * uint32_t(inter * 2) + group * C::kXBytes : nowhere;
+    const int at = i.n <= 8 ? column % 8 : column;
+    if (at >= i.n) return nowhere;
+    return uint32_t(i.list[at]) * uint32_t(inter * 2) + (at < column ? rest : 0u) + group * C::kXBytes;
   };
   uint32_t x_lane = row_of(ask.i);
   auto request = [&](typename C::W(&w)[U][RT], typename C::X(&x)[U]) {
@@ -414,10 +437,15 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
       for (int r = 0; r < RT; ++r) acc[r] = C::mac(w[u][r], x[u], acc[r]);
     form.s += U;
     if (form.s >= form.i.end) {
-      if (lane % 16 < form.i.n)
+      if (form.i.n <= 8) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
-          form.i.y[((int(form.i.list[lane % 16]) - base) * RT + r) * 4 + group] = acc[r];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[r][q] += __uint_as_float(dpp<kDppRowShl8, 0xF>(__float_as_uint(acc[r][q])));
+      }
+      if (column < form.i.n)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) form.i.y[((int(form.i.list[column]) - base) * RT + r) * 4 + group] = acc[r];
       clear();
       turn(form);
     }
@@ -510,7 +538,7 @@ __global__ __launch_bounds__(NW * kWave, 4) void k_few_down(
       step_range(inter, p, parts, i.begin, i.end);
       return i.n <= 16;
     };
-    few_down_stream<C, RT, NW, kBatch>(h, uint64_t(all) * inter * 2, inter, w_rows, base, uniform(wave),
+    few_down_stream<C, RT, NW, kBatch>(h, uint64_t(all) * inter * 4, inter, w_rows, base, uniform(wave),
                                        active * parts, find);
     for (int item = uniform(wave); item < active * parts; item += NW) {  // more than 16 slots
       DownItem i;
@@ -561,7 +589,7 @@ hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
                      reinterpret_cast<const uint8_t*>(p.x), p.n_rows, p.hidden, p.top_k, p.ids, p.pad,           \
                      p.n_experts, by_slot, static_cast<const uint8_t*>(p.w_gate_up), p.gate_up_scales, p.inter, \
                      p.h)
-  if (int64_t(grid.x) * grid.y <= MOE_UP_DEEP_MAX) MOE_GO(true);
+  if (int64_t(grid.x) * grid.y <= kUpDeepMax) MOE_GO(true);
   else MOE_GO(false);
 #undef MOE_GO
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
@@ -575,7 +603,7 @@ hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
                      dim3(NW * kWave), lds * RT, s, reinterpret_cast<const uint8_t*>(p.h), p.n_rows, p.hidden,      \
                      p.top_k, p.ids, p.router_weights, p.pad, p.n_experts, static_cast<const uint8_t*>(p.w_down),   \
                      p.down_scales, p.inter, chunk, max_parts, p.out)
-  if (p.hidden >= MOE_DOWN_WIDE_MIN) MOE_GO(2, 16);
+  if (p.hidden >= kDownWideMin) MOE_GO(2, 16);
   else MOE_GO(1, 8);
 #undef MOE_GO
   return hipGetLastError();

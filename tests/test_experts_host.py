@@ -85,7 +85,7 @@ def test_layer_refusals():
 
 def test_workspace_size():
     f = mod.moe_layer_few_workspace_bytes
-    assert f(0, 1, 16) == 256 and f(4, 2, 48) == 768 and f(256, 8, 2048) == 256 * 8 * 2048 * 2
+    assert f(0, 1, 16) == 256 and f(4, 2, 48) == 1536 and f(256, 8, 2048) == 256 * 8 * 2048 * 4
     assert f(-1, 1, 16) == f(1, 0, 16) == f(257, 8, 16) == f(1, 2049, 16) == f(1, 1, 24) == f(2 ** 40, 1, 16) == 0
     for n, k, i in ((1, 1, 16), (3, 5, 1040), (256, 8, 7168)):
         assert f(n, k, i) <= 4 * n * k * i + 256 and f(n, k, i) % 256 == 0

@@ -356,6 +356,25 @@ def test_layer_reads_the_real_count(count, tp_rank, real):
     assert not u16(out)[real:].any()
 
 
+@pytest.mark.parametrize("weights", ["bf16", "int8"])
+def test_layer_with_an_infinite_activation_between_the_products(weights):
+    """h beyond bf16's range, one expert with few slots and one with many: infinite results keep their sign."""
+    h, i = 32, 16
+    ids = np.array([[0]] * 3 + [[1]] * 12, np.int32)
+    x = torch.ones((15, h), dtype=torch.bfloat16, device=DEV)
+    one = torch.bfloat16 if weights == "bf16" else torch.int8
+    wgu, wd = torch.ones((2, 2 * i, h), dtype=one, device=DEV), torch.ones((2, h, i), dtype=one, device=DEV)
+    wd[:, 1::2] = -1
+    big = 3e36 if weights == "bf16" else 1.0
+    sg = sd = None
+    if weights == "bf16":
+        wgu[:, :i] *= big                                   # gate 9.6e37, up 32: h overflows fp32
+    else:
+        sg, sd = torch.full((2, 2 * i), 3e36, device=DEV), torch.ones((2, h), device=DEV)
+    out = _layer_call(x, ids, np.ones((15, 1), np.float32), wgu, wd, sg, sd)
+    assert (out[:, 0::2] == float("inf")).all() and (out[:, 1::2] == float("-inf")).all()
+
+
 def test_layer_without_rows_does_nothing():
     z = torch.empty((0, 32), dtype=torch.bfloat16, device=DEV)
     w = torch.zeros((2, 32, 32), dtype=torch.bfloat16, device=DEV)
