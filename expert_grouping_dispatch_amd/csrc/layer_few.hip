@@ -75,15 +75,22 @@ struct UpI8 {
   }
 };
 
-// Grids of k_few_up up to this many workgroups have six buffers and a CU each.
-constexpr int kUpDeepMax = 256;
+// Grids of k_few_up of at least this many workgroups of 64 channels; smaller
+// ones leave CUs idle and take 16 channels a workgroup (k_few_up_split).  The
+// layer in us, 64 channels against 16: 32 workgroups (1 token, 1 of 8 experts,
+// 8192 x 2048, bf16) 83 and 33, 128 workgroups (4 tokens, 2 of 8, 4096 x 1024)
+// 54 and 39, 256 workgroups (1 token, 8 of 64, 7168 x 2048) 124 and 155.
+constexpr int kUpStripsMin = 256;
 // Layers of at least this many output channels take 32 a workgroup in
 // k_few_down, which loads the activations half as often: 7168 channels, 256
 // experts in int8, 776 slots: 1733 us for the layer against 1939 us with 16.
 // Narrower ones would leave CUs idle: 4096 channels, one token in bf16: 142 us
 // against 124 us.
 constexpr int kDownWideMin = 6144;
-constexpr int kUpMost = 6;  // buffers
+#ifndef MOE_TURN
+#define MOE_TURN 1
+#endif
+constexpr int kUpMost = 3;  // buffers
 // What bf16 leaves of two values whose bf16 forms are `hi`, in bf16; nothing
 // where that is infinite or NaN.
 __device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t hi) {
@@ -91,21 +98,19 @@ __device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t hi) {
   return bf16_pair(fabsf(ra) < INFINITY ? ra : 0.0f, fabsf(rb) < INFINITY ? rb : 0.0f);
 }
 
+// h of four channels of a slot, at `to`, and what bf16 leaves of it.
+__device__ __forceinline__ void store_h(uint16_t* to, int64_t h_rest, const f32x4& gate, const f32x4& up) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = silu_times(gate[i], up[i]);
+  const u32x2 hi{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+  *reinterpret_cast<u32x2*>(to) = hi;
+  *reinterpret_cast<u32x2*>(to + h_rest) = u32x2{rest_pair(v[0], v[1], hi.x), rest_pair(v[2], v[3], hi.y)};
+}
+
 struct UpBuffers {
   uint8_t *w[kUpMost], *xa[kUpMost], *xb[kUpMost];  // weights; activation rows 0..31 and 32..63
 };
-
-// Waits until all but the last n groups of kFills requests have arrived, n <= 4.
-template <int kFills>
-__device__ __forceinline__ void wait_fills(int n) {
-  switch (n) {
-    case 0: __builtin_amdgcn_s_waitcnt(wait_all_but(0)); break;
-    case 1: __builtin_amdgcn_s_waitcnt(wait_all_but(kFills)); break;
-    case 2: __builtin_amdgcn_s_waitcnt(wait_all_but(2 * kFills)); break;
-    case 3: __builtin_amdgcn_s_waitcnt(wait_all_but(3 * kFills)); break;
-    default: __builtin_amdgcn_s_waitcnt(wait_all_but(4 * kFills)); break;
-  }
-}
 
 // One expert's gate and up rows of channels [c0, c0 + 64) times n <= 32*G of
 // its slots.  NB buffers of a step are filled straight from global memory, the
@@ -153,7 +158,9 @@ __device__ __forceinline__ void few_up(const uint8_t* x, int n_rows, int hidden,
     const int i = wave + 4 * j;
     return j * 4 < kPerHalf ? xa + i * 1024 : xb + (i - kPerHalf) * 1024;
   };
-  auto fetch = [&](int s, uint8_t* to_w, uint8_t* xa, uint8_t* xb) {
+  const int turn = ragged ? 0 : int((blockIdx.x * 5 + blockIdx.y * 3) % uint32_t(steps)) * MOE_TURN;
+  auto fetch = [&](int nth, uint8_t* to_w, uint8_t* xa, uint8_t* xb) {
+    const int s = nth + turn < steps ? nth + turn : nth + turn - steps;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       load_to_lds<true>(i < 2 ? gate : up, w_off[i % 2], uint32_t(s) * 128 + uint32_t(8 * (i % 2)) * w_row,
@@ -167,7 +174,8 @@ __device__ __forceinline__ void few_up(const uint8_t* x, int n_rows, int hidden,
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[g][i] = 0.0f;
   auto step = [&](int s, uint8_t* w, uint8_t* xa, uint8_t* xb, uint8_t* next_w, uint8_t* next_xa, uint8_t* next_xb) {
-    wait_fills<kFills>(min(NB - 2, steps - 1 - s));
+    if (NB == 3 && s + 1 < steps) __builtin_amdgcn_s_waitcnt(wait_all_but(NB == 3 ? kFills : 0));
+    else __builtin_amdgcn_s_waitcnt(kWaitLoads);
     asm volatile("" ::: "memory");
     if (ragged && s == steps - 1) {  // pieces past the rows' end: zeros in both, so that they add nothing
       const u32x4 zero{0u, 0u, 0u, 0u};
@@ -218,32 +226,51 @@ __device__ __forceinline__ void few_up(const uint8_t* x, int n_rows, int hidden,
         sg = *reinterpret_cast<const f32x4*>(w_scales + ch);
         su = *reinterpret_cast<const f32x4*>(w_scales + inter + ch);
       }
-      float v[4];
+      f32x4 a, b;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float a = acc[g][4 * q + i], b = acc[g][8 + 4 * q + i];
+        a[i] = acc[g][4 * q + i];
+        b[i] = acc[g][8 + 4 * q + i];
         if constexpr (kScaled) {
-          a *= sg[i];
-          b *= su[i];
+          a[i] *= sg[i];
+          b[i] *= su[i];
         }
-        v[i] = silu_times(a, b);
       }
-      const u32x2 hi{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-      *reinterpret_cast<u32x2*>(row + ch) = hi;
-      *reinterpret_cast<u32x2*>(row + h_rest + ch) = u32x2{rest_pair(v[0], v[1], hi.x), rest_pair(v[2], v[3], hi.y)};
+      store_h(row + ch, h_rest, a, b);
     }
   }
   __syncthreads();  // the buffers are filled again for the next slots
 }
 
-// kDeep: six buffers and one workgroup a CU instead of three and two, for
-// grids that do not fill the CUs, which are bound by how long a step takes to
-// arrive (MEASURE_DEEP).
-// blockIdx.x: 64 channels.  blockIdx.y: the expert, or, when there are fewer
-// slots than experts, a slot, which stands for its expert if it is the first
-// slot on it.
-template <class C, bool kDeep, bool kScaled, typename IdT>
-__global__ __launch_bounds__(kUpThreads, (kDeep ? 1 : 2)) void k_few_up(const uint8_t* __restrict__ x, int n_rows, int hidden,
+// blockIdx.y: the expert, or, when there are fewer slots than experts, a slot,
+// which stands for its expert if it is the first slot on it.  Lists the slots
+// of the expert and returns their number, 0 where there is nothing to do.
+template <typename IdT>
+__device__ __forceinline__ int list_slots(const IdT* ids, int slots, int n_experts, bool by_slot, uint16_t* s_list,
+                                          int* s_n, int& e) {
+  const int tid = threadIdx.x;
+  if (tid == 0) s_n[0] = s_n[1] = 0;
+  e = blockIdx.y;
+  if (by_slot) {
+    if (e >= slots) return 0;
+    e = expert_of(ids, e, n_experts);
+    if (e < 0) return 0;
+  }
+  __syncthreads();
+  for (int i = tid; i < slots; i += kUpThreads) {
+    if (expert_of(ids, i, n_experts) == e) {
+      if (by_slot && i < int(blockIdx.y)) s_n[1] = 1;
+      s_list[atomicAdd(&s_n[0], 1)] = uint16_t(i);  // any order: a slot's result does not depend on its column
+    }
+  }
+  __syncthreads();
+  e = uniform(e);
+  return uniform(s_n[1] != 0 ? 0 : s_n[0]);
+}
+
+// blockIdx.x: 64 channels.
+template <class C, bool kScaled, typename IdT>
+__global__ __launch_bounds__(kUpThreads, 2) void k_few_up(const uint8_t* __restrict__ x, int n_rows, int hidden,
                                                           int top_k, const IdT* __restrict__ ids, PadMask pad,
                                                           int n_experts, bool by_slot,
                                                           const uint8_t* __restrict__ w,
@@ -252,59 +279,115 @@ __global__ __launch_bounds__(kUpThreads, (kDeep ? 1 : 2)) void k_few_up(const ui
   // Named apart, so that the compiler sees that filling one does not touch the others.
   __shared__ __align__(16) uint8_t s_w0[kUpWBytes], s_w1[kUpWBytes], s_w2[kUpWBytes];
   __shared__ __align__(16) uint8_t s_x0[kUpXBytes], s_x1[kUpXBytes], s_x2[kUpXBytes];
-  constexpr int kMoreW = kDeep ? kUpWBytes : 16, kMoreX = kDeep ? kUpXBytes : 16;
-  __shared__ __align__(16) uint8_t s_w3[kMoreW], s_w4[kMoreW], s_w5[kMoreW];
-  __shared__ __align__(16) uint8_t s_x3[kMoreX], s_x4[kMoreX], s_x5[kMoreX];
-  constexpr int NB = kDeep ? 6 : 3;
   __shared__ uint16_t s_list[kFewMaxSlots];
-  __shared__ int s_n, s_earlier;
-  const int tid = threadIdx.x;
-  const int slots = real_slots(pad, n_rows, top_k);
-  if (tid == 0) s_n = s_earlier = 0;
-  int e = blockIdx.y;
-  if (by_slot) {
-    if (e >= slots) return;
-    e = expert_of(ids, e, n_experts);
-    if (e < 0) return;
-  }
-  __syncthreads();
-  for (int i = tid; i < slots; i += kUpThreads) {
-    if (expert_of(ids, i, n_experts) == e) {
-      if (by_slot && i < int(blockIdx.y)) s_earlier = 1;
-      s_list[atomicAdd(&s_n, 1)] = uint16_t(i);  // any order: a slot's result does not depend on its column
-    }
-  }
-  __syncthreads();
-  if (s_earlier != 0) return;
-  const int total = uniform(s_n);
+  __shared__ int s_n[2];
+  int e;
+  const int total = list_slots(ids, real_slots(pad, n_rows, top_k), n_experts, by_slot, s_list, s_n, e);
   const int64_t h_rest = int64_t(n_rows) * top_k * inter;
   const uint64_t each = uint64_t(2) * inter * hidden * C::kWSize;
   const uint8_t* we = w + e * each;
   const float* se = kScaled ? w_scales + int64_t(e) * 2 * inter : nullptr;
   const uint64_t w_bytes = (n_experts - e) * each;
   const int c0 = blockIdx.x * kUpChannels;
-  for (int i = 0; i < total;) {
+  for (int i = 0; i < total; i += 64) {
     const int n = total - i;
-    UpBuffers buf{{s_w0, s_w1, s_w2, s_w3, s_w4, s_w5}, {s_x0, s_x1, s_x2, s_x3, s_x4, s_x5},
-                  {s_x0, s_x1, s_x2, s_x3, s_x4, s_x5}};
+    UpBuffers buf{{s_w0, s_w1, s_w2}, {s_x0, s_x1, s_x2}, {s_x0, s_x1, s_x2}};
     if (n <= 32) {
-      few_up<C, 1, NB, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, n, h, h_rest, buf);
+      few_up<C, 1, 3, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, n, h, h_rest, buf);
     } else if constexpr (C::kXRow == 128) {
 #pragma unroll
       for (int b = 0; b < kUpMost; ++b) buf.xb[b] = buf.xa[b] + kUpXBytes / 2;
-      few_up<C, 2, NB, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h,
-                                  h_rest, buf);
-    } else if constexpr (kDeep) {
-      // 64 rows of 256 bytes take two activation buffers, or a weight buffer: four steps deep
-      const UpBuffers wide{{s_w0, s_w1, s_w2, s_w3}, {s_x0, s_x2, s_x4, s_w4}, {s_x1, s_x3, s_x5, s_w4 + kUpXBytes}};
-      few_up<C, 2, 4, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h,
-                                 h_rest, wide);
+      few_up<C, 2, 3, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h,
+                               h_rest, buf);
     } else {
+      // 64 rows of 256 bytes take the third weight buffer and two activation buffers: two steps deep
       const UpBuffers wide{{s_w0, s_w1}, {s_w2, s_x0}, {s_w2 + kUpXBytes, s_x1}};
       few_up<C, 2, 2, kScaled>(x, n_rows, hidden, top_k, we, w_bytes, se, inter, c0, s_list + i, min(n, 64), h,
-                                 h_rest, wide);
+                               h_rest, wide);
     }
-    i += 64;
+  }
+}
+
+// The same for small grids: 16 channels a workgroup, k split over its waves,
+// weights straight to registers (stream.h), the parts joined in LDS.
+// list[0 .. n), n <= 16*NG.
+template <class C, int NG, bool kScaled>
+__device__ __forceinline__ void few_up_split(const uint8_t* x, int hidden, int top_k, const uint8_t* w,
+                                             const float* w_scales, int inter, int tile, const uint16_t* list, int n,
+                                             uint16_t* h, int64_t h_rest, f32x4* s_part) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int64_t w_row = int64_t(hidden) * (C::kWBytes / 16);
+  const uint8_t* wp[2];
+  const uint8_t* xp[NG];
+  wp[0] = w + int64_t(tile * 16 + lane % 16) * w_row;
+  wp[1] = wp[0] + int64_t(inter) * w_row;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const int slot = list[min(g * 16 + lane % 16, n - 1)];
+    xp[g] = x + int64_t(slot / top_k) * hidden * 2;
+  }
+  f32x4 acc[2][NG];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) acc[r][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  int begin, end;
+  step_range(hidden, wave, kUpWaves, begin, end);
+  stream_products<C, 2, NG, (NG == 1 ? 8 : NG == 2 ? 4 : 2)>(wp, xp, begin, end, hidden, acc);
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) s_part[((wave * 2 + r) * NG + g) * kWave + lane] = acc[r][g];
+  __syncthreads();
+  for (int g = wave; g < NG; g += kUpWaves) {
+    f32x4 sum[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      sum[r] = s_part[(r * NG + g) * kWave + lane];
+#pragma unroll
+      for (int v = 1; v < kUpWaves; ++v) {
+        const f32x4 p = s_part[((v * 2 + r) * NG + g) * kWave + lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[r][i] += p[i];
+      }
+    }
+    const int at = g * 16 + lane % 16, c = tile * 16 + (lane / 16) * 4;
+    if (at < n) {
+      if constexpr (kScaled) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[0][i] *= w_scales[c + i];
+          sum[1][i] *= w_scales[inter + c + i];
+        }
+      }
+      store_h(h + int64_t(list[at]) * inter + c, h_rest, sum[0], sum[1]);
+    }
+  }
+  __syncthreads();  // s_part is rewritten for the next slots
+}
+
+// blockIdx.x: 16 channels.
+template <class C, bool kScaled, typename IdT>
+__global__ __launch_bounds__(kUpThreads, 2) void k_few_up_split(
+    const uint8_t* __restrict__ x, int n_rows, int hidden, int top_k, const IdT* __restrict__ ids, PadMask pad,
+    int n_experts, bool by_slot, const uint8_t* __restrict__ w, const float* __restrict__ w_scales, int inter,
+    uint16_t* __restrict__ h) {
+  __shared__ uint16_t s_list[kFewMaxSlots];
+  __shared__ int s_n[2];
+  __shared__ f32x4 s_part[kUpWaves * 2 * 4 * kWave];
+  int e;
+  const int total = list_slots(ids, real_slots(pad, n_rows, top_k), n_experts, by_slot, s_list, s_n, e);
+  const int64_t h_rest = int64_t(n_rows) * top_k * inter;
+  const uint8_t* we = w + int64_t(e) * 2 * inter * hidden * (C::kWBytes / 16);
+  const float* se = kScaled ? w_scales + int64_t(e) * 2 * inter : nullptr;
+  for (int i = 0; i < total; i += 64) {
+    const int n = min(total - i, 64);
+    if (n <= 16)
+      few_up_split<C, 1, kScaled>(x, hidden, top_k, we, se, inter, blockIdx.x, s_list + i, n, h, h_rest, s_part);
+    else if (n <= 32)
+      few_up_split<C, 2, kScaled>(x, hidden, top_k, we, se, inter, blockIdx.x, s_list + i, n, h, h_rest, s_part);
+    else
+      few_up_split<C, 4, kScaled>(x, hidden, top_k, we, se, inter, blockIdx.x, s_list + i, n, h, h_rest, s_part);
   }
 }
 
@@ -583,14 +666,18 @@ template <class Up, class C, bool kScaled, typename IdT>
 hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
   const int slots = p.n_rows * p.top_k;
   const bool by_slot = slots < p.n_experts;
-  const dim3 grid((p.inter + kUpChannels - 1) / kUpChannels, by_slot ? slots : p.n_experts);
-#define MOE_GO(DEEP)                                                                                             \
-  hipLaunchKernelGGL((k_few_up<Up, DEEP, kScaled, IdT>), grid, dim3(kUpThreads), 0, s,                           \
-                     reinterpret_cast<const uint8_t*>(p.x), p.n_rows, p.hidden, p.top_k, p.ids, p.pad,           \
-                     p.n_experts, by_slot, static_cast<const uint8_t*>(p.w_gate_up), p.gate_up_scales, p.inter, \
-                     p.h)
-  if (int64_t(grid.x) * grid.y <= kUpDeepMax) MOE_GO(true);
-  else MOE_GO(false);
+  const uint32_t strips = (p.inter + kUpChannels - 1) / kUpChannels, groups = by_slot ? slots : p.n_experts;
+#define MOE_GO(KERNEL, X)                                                                                          \
+  hipLaunchKernelGGL((KERNEL<X, kScaled, IdT>), grid, dim3(kUpThreads), 0, s, reinterpret_cast<const uint8_t*>(p.x), \
+                     p.n_rows, p.hidden, p.top_k, p.ids, p.pad, p.n_experts, by_slot,                              \
+                     static_cast<const uint8_t*>(p.w_gate_up), p.gate_up_scales, p.inter, p.h)
+  if (strips * groups >= uint32_t(kUpStripsMin)) {
+    const dim3 grid(strips, groups);
+    MOE_GO(k_few_up, Up);
+  } else {
+    const dim3 grid(p.inter / 16, groups);
+    MOE_GO(k_few_up_split, C);
+  }
 #undef MOE_GO
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   // Room for the results of the slots of a chunk, and for several parts of k while that stays within 512 slots' room.
