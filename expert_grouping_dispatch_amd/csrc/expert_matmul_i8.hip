@@ -3,12 +3,19 @@
 //   c[p, n] = sum_k a[p, k] * w[e(p), n, k]  (int32, exact in any order)
 //   out = bf16(fl(fl(fl(c) * sa[p]) * sw[e, n])), or silu(gate) * up of two of them
 //
-// The rows of an expert are known on the device only.  Two kernels share the
-// groups by their size, both reading the starts themselves:
-//   k_matmul_few   groups of at most kFewRows rows, bound by reading the
-//                  weights once: they stream into registers (stream.h).
-//   k_matmul_tile  larger groups, in tiles of 256 rows by 256 weight rows,
-//                  bound by the matrix units: both operands go through LDS.
+// The rows of an expert are known on the device only.  Kernels share the
+// groups by their size, each reading the starts itself:
+//   k_matmul_strip  groups of at most kFewRows rows, bound by reading the
+//                   weights once, 256 weight rows a workgroup, through LDS.
+//                   776 rows on 247 experts, 7168 -> 2048 with SwiGLU: 1025 us,
+//                   7.0 TB/s.
+//   k_matmul_few    the same groups where that makes too few workgroups: 32
+//                   weight rows a workgroup, straight to registers (stream.h).
+//   k_matmul_tile   larger groups, in tiles of 256 rows by 256 weight rows,
+//                   bound by the matrix units and what power they are given.
+//                   14000 rows on 8 experts, 4096 -> 14336 with SwiGLU: 1.55 ms,
+//                   2.1e15 operations/s, as many as the library's product of
+//                   8192 x 8192 x 8192 reaches.
 #include <type_traits>
 
 #include "experts.h"
@@ -20,14 +27,19 @@ namespace moe {
 
 namespace {
 
+// Largest group of the first two: 256 experts with 33 or 64 rows each, 2048 ->
+// 7168, took 712 and 762 us as strips, 862 and 872 us as tiles.
 constexpr int kFewRows = 64;
 constexpr int kFewWaves = 4, kFewThreads = kFewWaves * kWave;
 constexpr int kTile = 256, kStepBytes = 128;  // tile edge, and values of k per step
 constexpr int kTileThreads = 256, kStripThreads = 256;
 constexpr int kStripFrags = 2;  // of 32 weight rows, for each wave
-#ifndef MOE_STRIP_MIN
-#define MOE_STRIP_MIN 512
-#endif
+// Grids of k_matmul_strip of at least this many workgroups; smaller ones leave
+// CUs idle and go to k_matmul_few.  Strips against k_matmul_few in us: 64
+// workgroups (8 experts, 20 rows each, 7168 -> 2048) 67 and 35, 128 (8, 20,
+// 4096 -> 4096) 44 and 39, 256 (16, 20, 4096 -> 4096) 49 and 73, 896 (32, 16,
+// 2048 -> 7168) 83 and 115.
+constexpr uint32_t kStripsMin = 256;
 constexpr int kMaxActive = 1024;
 
 // Rows [lo, hi) of active expert j, inside the buffer whatever the starts hold.
@@ -587,7 +599,7 @@ hipError_t go(const ExpertMatmul& p, hipStream_t s) {
   const uint32_t groups = p.a_rows < uint32_t(p.n_experts) ? p.a_rows : uint32_t(p.n_experts);
   const int per = kSwiglu ? 16 : 32, strip = (kSwiglu ? 64 : 128) * kStripFrags;
   const uint32_t strips = (p.n_out + strip - 1) / strip;
-  if (strips * groups >= MOE_STRIP_MIN)
+  if (strips * groups >= kStripsMin)
     hipLaunchKernelGGL((k_matmul_strip<kSwiglu>), dim3(strips, groups), dim3(kStripThreads), 0, s, p);
   else
     hipLaunchKernelGGL((k_matmul_few<kSwiglu>), dim3((p.n_out + per - 1) / per, groups), dim3(kFewThreads), 0, s, p);

@@ -21,7 +21,7 @@ bool width_ok(int32_t n) { return n > 0 && n <= kMaxWidth && n % 16 == 0; }
 
 bool overlap(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes) {
   const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
-  return a != nullptr && b != nullptr && p < q + b_bytes && q < p + a_bytes;
+  return a != nullptr && b != nullptr && a_bytes > 0 && b_bytes > 0 && p < q + b_bytes && q < p + a_bytes;
 }
 
 template <typename IdT>
@@ -43,9 +43,15 @@ int layer_few(const uint16_t* x, int64_t n_rows, int32_t hidden, int32_t top_k, 
       !aligned(w_down, 16) || !aligned(down_scales, 16) || !aligned(output_tokens, 16) ||
       !aligned(workspace, 256))
     return MOE_ERR_INVALID_ARGUMENT;
-  const uint64_t row_bytes = uint64_t(n_rows) * uint64_t(hidden) * 2;
-  if (overlap(x, row_bytes, output_tokens, row_bytes)) return MOE_ERR_INVALID_ARGUMENT;
   if (n_rows > 0 && workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const uint64_t row_bytes = uint64_t(n_rows) * uint64_t(hidden) * 2, slots = uint64_t(n_rows) * uint64_t(top_k);
+  const uint64_t w_bytes = uint64_t(n_experts) * uint64_t(hidden) * uint64_t(inter) * (gate_up_scales == nullptr ? 2 : 1);
+  const void* reads[] = {x, topk_ids, router_weights, w_gate_up, w_down};
+  const uint64_t read_bytes[] = {row_bytes, slots * sizeof(IdT), slots * 4, 2 * w_bytes, w_bytes};
+  for (int i = 0; i < 5; ++i)
+    if (overlap(reads[i], read_bytes[i], output_tokens, row_bytes) || overlap(reads[i], read_bytes[i], workspace, need))
+      return MOE_ERR_INVALID_ARGUMENT;
+  if (overlap(output_tokens, row_bytes, workspace, need)) return MOE_ERR_INVALID_ARGUMENT;
   if (const int d = check_device()) return d;
   const moe::FewLayer<IdT> p{x, int(n_rows), hidden, top_k, topk_ids, router_weights,
                              moe::PadMask{real_token_count, top_k, tp_rank}, n_experts, w_gate_up,
@@ -67,6 +73,9 @@ int moe_dispatch_i8(const uint16_t* input_tokens, int64_t n_rows, int32_t hidden
   if (out_rows > 0 && (out_q == nullptr || out_scales == nullptr)) return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned(input_tokens, 16) || !aligned(out_q, 16) || !aligned(out_scales, 4) ||
       !aligned(restore_token_order, 4))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (n_rows > 0 && overlap(input_tokens, uint64_t(n_rows) * uint64_t(hidden) * 2, out_q,
+                            uint64_t(out_rows) * uint64_t(hidden)))
     return MOE_ERR_INVALID_ARGUMENT;
   if (const int d = check_device()) return d;
   return launched(moe::launch_dispatch_i8(input_tokens, n_rows, hidden, top_k, restore_token_order,

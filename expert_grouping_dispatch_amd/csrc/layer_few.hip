@@ -87,9 +87,6 @@ constexpr int kUpStripsMin = 256;
 // Narrower ones would leave CUs idle: 4096 channels, one token in bf16: 142 us
 // against 124 us.
 constexpr int kDownWideMin = 6144;
-#ifndef MOE_TURN
-#define MOE_TURN 1
-#endif
 constexpr int kUpMost = 3;  // buffers
 // What bf16 leaves of two values whose bf16 forms are `hi`, in bf16; nothing
 // where that is infinite or NaN.
@@ -158,7 +155,9 @@ __device__ __forceinline__ void few_up(const uint8_t* x, int n_rows, int hidden,
     const int i = wave + 4 * j;
     return j * 4 < kPerHalf ? xa + i * 1024 : xb + (i - kPerHalf) * 1024;
   };
-  const int turn = ragged ? 0 : int((blockIdx.x * 5 + blockIdx.y * 3) % uint32_t(steps)) * MOE_TURN;
+  // Workgroups begin at different steps: rows whose length is a power of two
+  // would have all of them at the same few memory channels at any time.
+  const int turn = ragged ? 0 : int((blockIdx.x * 5 + blockIdx.y * 3) % uint32_t(steps));
   auto fetch = [&](int nth, uint8_t* to_w, uint8_t* xa, uint8_t* xb) {
     const int s = nth + turn < steps ? nth + turn : nth + turn - steps;
 #pragma unroll
@@ -443,14 +442,24 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
   constexpr int WV = C::kWBytes / 16, XV = C::kXBytes / 16;
   const uint32_t w_row = uint32_t(inter) * WV, nowhere = 0x80000000u, rest = uint32_t(h_bytes / 2);
   const __amdgpu_buffer_rsrc_t rows = buffer_of(h, h_bytes);
+  // A walk through the items and, in each, through its batches, which begin
+  // at another one for every workgroup: rows whose length is a multiple of a
+  // power of two would have all workgroups at the same few memory channels.
   struct Walk {
     DownItem i;
-    int at, s;
+    int at, left, s;
   };
   auto turn = [&](Walk& k) {  // to the next item; at >= items when there is none
     do k.at += NW;
     while (k.at < items && !find(k.at, k.i));
-    k.s = k.i.begin;
+    if (k.at >= items) return;
+    k.left = (k.i.end - k.i.begin + U - 1) / U;
+    k.s = k.i.begin + int((blockIdx.x * 5 + uint32_t(k.at)) % uint32_t(k.left)) * U;
+  };
+  auto next = [&](Walk& k) {  // to the next batch; true at the item's end
+    k.s += U;
+    if (k.s >= k.i.end) k.s = k.i.begin;
+    return --k.left == 0;
   };
   Walk ask, form;
   ask.at = first - NW;
@@ -501,8 +510,7 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
               rows, some ? x_lane + uint32_t(s) * 4 * C::kXBytes + 16 * v : nowhere, 0, 0);
       }
     }
-    ask.s += U;
-    if (live && ask.s >= ask.i.end) {
+    if (live && next(ask)) {
       turn(ask);
       if (ask.at < items) x_lane = row_of(ask.i);
     }
@@ -518,8 +526,7 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int r = 0; r < RT; ++r) acc[r] = C::mac(w[u][r], x[u], acc[r]);
-    form.s += U;
-    if (form.s >= form.i.end) {
+    if (next(form)) {
       if (form.i.n <= 8) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)

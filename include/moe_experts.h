@@ -45,7 +45,8 @@ extern "C" {
  *
  *   input_tokens, n_rows, top_k, restore_token_order  as moe_dispatch.
  *   hidden        > 0, a multiple of 16.
- *   out_q         [device] int8 [out_rows, hidden], 16-byte aligned.
+ *   out_q         [device] int8 [out_rows, hidden], 16-byte aligned; must not
+ *                 overlap input_tokens.
  *   out_scales    [device] fp32 [out_rows].
  * Rows no slot points to are left untouched; positions >= out_rows are
  * skipped.  Rows with nothing routed are not read.
@@ -140,8 +141,8 @@ size_t moe_layer_few_workspace_bytes(int64_t n_rows, int32_t top_k, int32_t inte
  *   w_down         [device] [n_experts, hidden, inter], of the same type.
  *   down_scales    [device] fp32 [n_experts, hidden], 16-byte aligned; NULL
  *                  exactly where gate_up_scales is.
- *   output_tokens  [device] bf16 [n_rows, hidden], 16-byte aligned; must not
- *                  overlap x.
+ *   output_tokens  [device] bf16 [n_rows, hidden], 16-byte aligned.  Neither it
+ *                  nor the workspace may overlap the inputs or the other.
  *   workspace      [device] scratch of at least
  *                  moe_layer_few_workspace_bytes(n_rows, top_k, inter) bytes,
  *                  256-byte aligned; needs no initialisation.  Calls (and

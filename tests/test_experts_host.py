@@ -34,6 +34,14 @@ def test_every_declared_symbol_is_exported():
     assert set(names) <= exported
 
 
+def test_header_is_plain_c(tmp_path):
+    src = tmp_path / "use.c"
+    src.write_text('#include "moe_experts.h"\nint main(void) { return (int)moe_layer_few_workspace_bytes(0, 1, 16); }\n')
+    r = subprocess.run(["gcc", "-std=c11", "-Wall", "-Werror", "-pedantic", "-fsyntax-only", "-I",
+                        os.path.join(ROOT, "include"), str(src)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
 def _refusals(fn, good, bad):
     """Each (index, value) in turn replaces one good argument; all must be refused with status 1."""
     for at, value in bad:
@@ -49,7 +57,7 @@ def test_dispatch_and_quantize_refusals():
     good = [F, 10, 32, 2, P(1 << 21), P(1 << 22), P(1 << 23), 20, None]
     _refusals(mod.lib.moe_dispatch_i8, good, [(0, None), (0, P(8)), (1, -1), (1, 2 ** 31), (2, 0), (2, 24), (2, -16),
                                               (2, (1 << 20) + 16), (3, 0), (3, 1025), (4, None), (4, P(2)), (5, None),
-                                              (5, P(8)), (6, None), (6, P(2)), (7, -1)])
+                                              (5, P(8)), (5, F), (6, None), (6, P(2)), (7, -1)])
     good = [F, 10, 32, None, P(1 << 22), P(1 << 23), None]
     _refusals(mod.lib.moe_quantize_i8, good, [(0, None), (0, P(8)), (1, -1), (1, 2 ** 32 - 1), (2, 0), (2, 40),
                                               (3, P(2)), (4, None), (4, P(8)), (4, F), (4, P((1 << 20) + 32)),
@@ -77,7 +85,8 @@ def test_layer_refusals():
                   [(0, None), (0, P(8)), (1, -1), (1, 1025), (2, 0), (2, 40), (3, 0), (3, 513), (4, None), (4, P(2)),
                    (5, None), (5, P(2)), (6, P(2)), (7, -1), (8, 0), (8, 1025), (9, None), (9, P(8)),
                    (10, P(8 << 20)), (12, P(8 << 20)), (11, None), (11, P(8)), (13, 0), (13, 24), (14, None),
-                   (14, P(8)), (14, LAYER[0]), (15, None), (15, P(128))])
+                   (14, P(8)), (14, LAYER[0]), (14, LAYER[11]), (14, LAYER[15]), (15, None), (15, P(128)),
+                   (15, LAYER[0]), (15, LAYER[4]), (15, LAYER[9])])
         small = list(LAYER)
         small[16] = mod.moe_layer_few_workspace_bytes(4, 2, 48) - 1
         assert fn(*small) == 2
