@@ -14,10 +14,10 @@
 //                waves take (expert, part of k) items, every slot's result goes to
 //                its own place in LDS in fp32, and then each token's choices are
 //                summed in ascending order, so the result does not depend on which
-//                wave came first.  The instruction has 16 columns; an expert with
-//                up to eight slots uses the others for what bf16 left of h, which
-//                costs nothing and halves the error of the whole layer; with more
-//                slots h is what bf16 holds.
+//                wave came first.  The instruction has 16 columns; in calls of few
+//                slots an expert with up to eight of them uses the others for what
+//                bf16 left of h, so that the output's own rounding is all the error
+//                there is (0.0016 instead of 0.0023 of the result's norm).
 #include "experts.h"
 #include "lds_fill.h"
 #include "stream.h"
@@ -27,6 +27,11 @@ namespace moe {
 namespace {
 
 constexpr int kFewMaxSlots = 2048;
+// Calls of up to this many slots keep what bf16 leaves of h.  Its loads are as
+// many as those of h itself, which shows once they hold up the weights: 776
+// routed of 2048 slots on 256 experts in int8, 7168 x 2048, takes WITH_US us with
+// it and WITHOUT_US us without; one token in bf16 takes 119 us either way.
+constexpr int kRestSlots = 512;
 constexpr int kUpWaves = 4, kUpThreads = kUpWaves * kWave;
 constexpr int kDownSlots = 1024;  // slots at a time in k_few_down: 64 KB of results, two workgroups a CU
 
@@ -95,14 +100,15 @@ __device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t hi) {
   return bf16_pair(fabsf(ra) < INFINITY ? ra : 0.0f, fabsf(rb) < INFINITY ? rb : 0.0f);
 }
 
-// h of four channels of a slot, at `to`, and what bf16 leaves of it.
+// h of four channels of a slot, at `to`, and what bf16 leaves of it, h_rest further (0: dropped).
 __device__ __forceinline__ void store_h(uint16_t* to, int64_t h_rest, const f32x4& gate, const f32x4& up) {
   float v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = silu_times(gate[i], up[i]);
   const u32x2 hi{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
   *reinterpret_cast<u32x2*>(to) = hi;
-  *reinterpret_cast<u32x2*>(to + h_rest) = u32x2{rest_pair(v[0], v[1], hi.x), rest_pair(v[2], v[3], hi.y)};
+  if (h_rest != 0)
+    *reinterpret_cast<u32x2*>(to + h_rest) = u32x2{rest_pair(v[0], v[1], hi.x), rest_pair(v[2], v[3], hi.y)};
 }
 
 struct UpBuffers {
@@ -282,7 +288,7 @@ __global__ __launch_bounds__(kUpThreads, 2) void k_few_up(const uint8_t* __restr
   __shared__ int s_n[2];
   int e;
   const int total = list_slots(ids, real_slots(pad, n_rows, top_k), n_experts, by_slot, s_list, s_n, e);
-  const int64_t h_rest = int64_t(n_rows) * top_k * inter;
+  const int64_t h_rest = n_rows * top_k <= kRestSlots ? int64_t(n_rows) * top_k * inter : 0;
   const uint64_t each = uint64_t(2) * inter * hidden * C::kWSize;
   const uint8_t* we = w + e * each;
   const float* se = kScaled ? w_scales + int64_t(e) * 2 * inter : nullptr;
@@ -376,7 +382,7 @@ __global__ __launch_bounds__(kUpThreads, 2) void k_few_up_split(
   __shared__ f32x4 s_part[kUpWaves * 2 * 4 * kWave];
   int e;
   const int total = list_slots(ids, real_slots(pad, n_rows, top_k), n_experts, by_slot, s_list, s_n, e);
-  const int64_t h_rest = int64_t(n_rows) * top_k * inter;
+  const int64_t h_rest = n_rows * top_k <= kRestSlots ? int64_t(n_rows) * top_k * inter : 0;
   const uint8_t* we = w + int64_t(e) * 2 * inter * hidden * (C::kWBytes / 16);
   const float* se = kScaled ? w_scales + int64_t(e) * 2 * inter : nullptr;
   for (int i = 0; i < total; i += 64) {
@@ -419,8 +425,8 @@ __device__ __forceinline__ void few_down_tile(const uint8_t* h, int inter, const
 }
 
 // The results of experts with 16 or fewer slots.  Up to eight slots have two
-// of the 16 columns each, their h in bf16 and, h_bytes/2 further, what bf16 left
-// of it; the columns' sums are added at the end.  `find(item)` gives an item's
+// of the 16 columns each, their h in bf16 and, `rest` bytes further, what bf16
+// left of it (0: nothing is kept); the columns' sums are added at the end.  `find(item)` gives an item's
 // rows and range of steps; items first, first + NW, .. below `items`
 // are taken, those with more slots passed over.  Two batches of U steps are in
 // registers or on their way, weights and activations together (loads end in
@@ -436,11 +442,11 @@ struct DownItem {
 };
 constexpr int kDppRowShl8 = 0x108;  // lane l of 16 reads lane l + 8, the upper eight read 0
 template <class C, int RT, int NW, int U, class Find>
-__device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_bytes, int inter, int w_rows, int base,
+__device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_bytes, uint32_t rest, int inter, int w_rows, int base,
                                                 int first, int items, Find find) {
   const int lane = threadIdx.x % kWave, group = lane / 16;
   constexpr int WV = C::kWBytes / 16, XV = C::kXBytes / 16;
-  const uint32_t w_row = uint32_t(inter) * WV, nowhere = 0x80000000u, rest = uint32_t(h_bytes / 2);
+  const uint32_t w_row = uint32_t(inter) * WV, nowhere = 0x80000000u;
   const __amdgpu_buffer_rsrc_t rows = buffer_of(h, h_bytes);
   // A walk through the items and, in each, through its batches, which begin
   // at another one for every workgroup: rows whose length is a multiple of a
@@ -469,9 +475,9 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
   uint32_t w_lane[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) w_lane[r] = uint32_t(16 * r + lane % 16) * w_row + group * C::kWBytes;
-  const int column = lane % 16;
+  const int column = lane % 16, pairs = rest != 0 ? 8 : 0;  // most slots with two columns each
   auto row_of = [&](const DownItem& i) {
-    const int at = i.n <= 8 ? column % 8 : column;
+    const int at = i.n <= pairs ? column % 8 : column;
     if (at >= i.n) return nowhere;
     return uint32_t(i.list[at]) * uint32_t(inter * 2) + (at < column ? rest : 0u) + group * C::kXBytes;
   };
@@ -527,7 +533,7 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
 #pragma unroll
       for (int r = 0; r < RT; ++r) acc[r] = C::mac(w[u][r], x[u], acc[r]);
     if (next(form)) {
-      if (form.i.n <= 8) {
+      if (form.i.n <= pairs) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -628,7 +634,7 @@ __global__ __launch_bounds__(NW * kWave, 4) void k_few_down(
       step_range(inter, p, parts, i.begin, i.end);
       return i.n <= 16;
     };
-    few_down_stream<C, RT, NW, kBatch>(h, uint64_t(all) * inter * 4, inter, w_rows, base, uniform(wave),
+    few_down_stream<C, RT, NW, kBatch>(h, uint64_t(all) * inter * 4, all <= kRestSlots ? uint32_t(all) * inter * 2 : 0u, inter, w_rows, base, uniform(wave),
                                        active * parts, find);
     for (int item = uniform(wave); item < active * parts; item += NW) {  // more than 16 slots
       DownItem i;

@@ -69,7 +69,8 @@ def layer_few(x: np.ndarray, ids: np.ndarray, router_weights: np.ndarray, w_gate
         (|g| + 8) u relative (the exponent's argument, the exponential, a
         quotient and two products);
       * h as two bf16 values: half a step of what half a step left, 2^-16
-        relative, for experts with up to eight slots; as one, 2^-8, for others;
+        relative, for experts with up to eight slots in maps of up to 512; as
+        one, 2^-8, for others;
       * the output: 2^-8 relative;
       * the weighted sum: (top_k + 1) u.
     """
@@ -90,7 +91,7 @@ def layer_few(x: np.ndarray, ids: np.ndarray, router_weights: np.ndarray, w_gate
             g, up, dg, du = v[:inter], v[inter:], dv[:inter], dv[inter:]
             h = swiglu(g, up)
             dh = 1.1 * dg * (np.abs(up) + du) + np.abs(g * _sigmoid(g)) * du
-            dh = dh + (np.abs(h) + dh) * ((half * half if slots[e] <= 8 else half) + (np.abs(g) + 8) * u24)
+            dh = dh + (np.abs(h) + dh) * ((half * half if slots[e] <= 8 and ids.size <= 512 else half) + (np.abs(g) + 8) * u24)
             y = wd @ h
             dy = np.abs(wd) @ dh + (inter + 2) * u24 * (np.abs(wd) @ (np.abs(h) + dh))
             out[t] += rw[t, j] * y
