@@ -448,24 +448,14 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
   constexpr int WV = C::kWBytes / 16, XV = C::kXBytes / 16;
   const uint32_t w_row = uint32_t(inter) * WV, nowhere = 0x80000000u;
   const __amdgpu_buffer_rsrc_t rows = buffer_of(h, h_bytes);
-  // A walk through the items and, in each, through its batches, which begin
-  // at another one for every workgroup: rows whose length is a multiple of a
-  // power of two would have all workgroups at the same few memory channels.
   struct Walk {
     DownItem i;
-    int at, left, s;
+    int at, s;
   };
   auto turn = [&](Walk& k) {  // to the next item; at >= items when there is none
     do k.at += NW;
     while (k.at < items && !find(k.at, k.i));
-    if (k.at >= items) return;
-    k.left = (k.i.end - k.i.begin + U - 1) / U;
-    k.s = k.i.begin + int((blockIdx.x * 5 + uint32_t(k.at)) % uint32_t(k.left)) * U;
-  };
-  auto next = [&](Walk& k) {  // to the next batch; true at the item's end
-    k.s += U;
-    if (k.s >= k.i.end) k.s = k.i.begin;
-    return --k.left == 0;
+    k.s = k.i.begin;
   };
   Walk ask, form;
   ask.at = first - NW;
@@ -516,7 +506,8 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
               rows, some ? x_lane + uint32_t(s) * 4 * C::kXBytes + 16 * v : nowhere, 0, 0);
       }
     }
-    if (live && next(ask)) {
+    ask.s += U;
+    if (live && ask.s >= ask.i.end) {
       turn(ask);
       if (ask.at < items) x_lane = row_of(ask.i);
     }
@@ -532,7 +523,8 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int r = 0; r < RT; ++r) acc[r] = C::mac(w[u][r], x[u], acc[r]);
-    if (next(form)) {
+    form.s += U;
+    if (form.s >= form.i.end) {
       if (form.i.n <= pairs) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
