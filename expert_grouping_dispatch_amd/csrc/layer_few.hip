@@ -3,13 +3,19 @@
 // Both products read every active expert's weights once: 6*hidden*inter bytes
 // per expert in bf16 (half in int8) against at most a few dozen rows of
 // activations, so the layer is bound by how fast HBM delivers the weights.
-// They go straight to registers (stream.h); grouping costs each workgroup one
-// pass over the few ids instead of a kernel of its own.
+// Grouping costs each workgroup one pass over the few ids instead of a kernel
+// of its own.
 //
 //   k_few_up     one workgroup per (expert, 64 intermediate channels): lists the
 //                expert's slots and forms gate, up and h = silu(gate)*up for up to
-//                64 of them at a time.  h goes out in bf16, the type of the second
-//                product's matrix instruction, with what bf16 leaves of it beside.
+//                64 of them at a time.  Weights come in whole cache lines through
+//                LDS: 247 active experts in int8, 7168 x 2048, 776 slots, 1105 us,
+//                6.6 TB/s; two experts in bf16, 4096 x 14336, 75 us, 6.3 TB/s.  h
+//                goes out in bf16, the type of the second product's matrix
+//                instruction, with what bf16 leaves of it beside.
+//   k_few_up_split  the same for small grids: 16 channels a workgroup, its waves
+//                share k.  4 experts, 1040 x 528, 13 tokens: 12 us, the latency of
+//                two rounds of loads, the sums across waves and the launch.
 //   k_few_down   one workgroup per 16 or 32 output channels: groups the slots, its
 //                waves take (expert, part of k) items, every slot's result goes to
 //                its own place in LDS in fp32, and then each token's choices are
@@ -17,7 +23,10 @@
 //                wave came first.  The instruction has 16 columns; in calls of few
 //                slots an expert with up to eight of them uses the others for what
 //                bf16 left of h, so that the output's own rounding is all the error
-//                there is (0.0016 instead of 0.0023 of the result's norm).
+//                there is (0.0016 instead of 0.0023 of the result's norm).  Weights
+//                go straight to registers (stream.h), since LDS holds the results:
+//                670 us and 5.4 TB/s for the int8 layer above, 47 us and 5.0 TB/s
+//                for the bf16 one; 36 cycles of the address unit a load bound it.
 #include "experts.h"
 #include "lds_fill.h"
 #include "stream.h"
@@ -29,8 +38,8 @@ namespace {
 constexpr int kFewMaxSlots = 2048;
 // Calls of up to this many slots keep what bf16 leaves of h.  Its loads are as
 // many as those of h itself, which shows once they hold up the weights: 776
-// routed of 2048 slots on 256 experts in int8, 7168 x 2048, takes WITH_US us with
-// it and WITHOUT_US us without; one token in bf16 takes 119 us either way.
+// routed of 2048 slots on 256 experts in int8, 7168 x 2048, takes 1798 us with
+// it and 1741 us without; one token in bf16 takes 120 us either way.
 constexpr int kRestSlots = 512;
 constexpr int kUpWaves = 4, kUpThreads = kUpWaves * kWave;
 constexpr int kDownSlots = 1024;  // slots at a time in k_few_down: 64 KB of results, two workgroups a CU
