@@ -16,7 +16,7 @@
 //   k_few_up_split  the same for small grids: 16 channels a workgroup, its waves
 //                share k.  4 experts, 1040 x 528, 13 tokens: 12 us, the latency of
 //                two rounds of loads, the sums across waves and the launch.
-//   k_few_down   one workgroup per 16 or 32 output channels: groups the slots, its
+//   k_few_down   one workgroup per 4 to 32 output channels: groups the slots, its
 //                waves take (expert, part of k) items, every slot's result goes to
 //                its own place in LDS in fp32, and then each token's choices are
 //                summed in ascending order, so the result does not depend on which
@@ -25,8 +25,10 @@
 //                bf16 left of h, so that the output's own rounding is all the error
 //                there is (0.0016 instead of 0.0023 of the result's norm).  Weights
 //                go straight to registers (stream.h), since LDS holds the results:
-//                670 us and 5.4 TB/s for the int8 layer above, 47 us and 5.0 TB/s
+//                636 us and 5.7 TB/s for the int8 layer above, 46 us and 5.1 TB/s
 //                for the bf16 one; 36 cycles of the address unit a load bound it.
+#include <algorithm>
+
 #include "experts.h"
 #include "lds_fill.h"
 #include "stream.h"
@@ -42,7 +44,10 @@ constexpr int kFewMaxSlots = 2048;
 // it and 1741 us without; one token in bf16 takes 120 us either way.
 constexpr int kRestSlots = 512;
 constexpr int kUpWaves = 4, kUpThreads = kUpWaves * kWave;
-constexpr int kDownSlots = 1024;  // slots at a time in k_few_down: 64 KB of results, two workgroups a CU
+// Slots at a time in k_few_down with RT row tiles: 128 KB of results.  Half of
+// it read the weights of 64 experts, 1024 -> 4096, twice for 2048 slots: 323 us
+// against 232 us.
+constexpr int down_slots(int rt) { return 2048 / rt; }
 
 // Slots at or past the boundary row are unrouted.
 __device__ __forceinline__ int real_slots(const PadMask& pad, int n_rows, int top_k) {
@@ -95,12 +100,14 @@ struct UpI8 {
 // 8192 x 2048, bf16) 83 and 33, 128 workgroups (4 tokens, 2 of 8, 4096 x 1024)
 // 54 and 39, 256 workgroups (1 token, 8 of 64, 7168 x 2048) 124 and 155.
 constexpr int kUpStripsMin = 256;
-// Layers of at least this many output channels take 32 a workgroup in
-// k_few_down, which loads the activations half as often: 7168 channels, 256
-// experts in int8, 776 slots: 1733 us for the layer against 1939 us with 16.
-// Narrower ones would leave CUs idle: 4096 channels, one token in bf16: 142 us
-// against 124 us.
-constexpr int kDownWideMin = 6144;
+// Output channels a workgroup of k_few_down: what spreads them over this many
+// workgroups, in groups of four, at most 32; above 16 the workgroup has 16
+// waves of two row tiles.  Rows of a tile past the workgroup's are not read.
+// 256 experts in int8, 776 slots, 7168 channels: 636 us with 28 each, 706 us
+// with 32 on 224 workgroups (the layer 1733 us then, 1939 us with 16).  Layers
+// in bf16: 2048 channels, 32 tokens, 8 of 64 experts: 212 us with 8 each, 236
+// us with 16; 5120 channels, 1 token, 8 of 64: 96 us with 20 each, 107 with 16.
+constexpr int kDownGroups = 256;
 constexpr int kUpMost = 3;  // buffers
 // What bf16 leaves of two values whose bf16 forms are `hi`, in bf16; nothing
 // where that is infinite or NaN.
@@ -407,7 +414,10 @@ __global__ __launch_bounds__(kUpThreads, 2) void k_few_up_split(
 
 // ---- down and the weighted sum ------------------------------------------------
 
-template <class C, int RT, int NG>
+// The results of n <= 16*NG slots over steps [begin, end), U of them requested
+// at a time.  NG 2 with U 2 where it is enough: 32 slots on each of 64 experts,
+// 1024 -> 4096 in bf16: 208 us against 232 us with NG 4 and U 1.
+template <class C, int RT, int NG, int U>
 __device__ __forceinline__ void few_down_tile(const uint8_t* h, int inter, const uint8_t* w, int w_rows,
                                               const uint16_t* list, int n, int begin, int end, int base,
                                               f32x4* s_y) {
@@ -417,13 +427,13 @@ __device__ __forceinline__ void few_down_tile(const uint8_t* h, int inter, const
   f32x4 acc[RT][NG];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    wp[r] = w + int64_t(min(16 * r, w_rows - 16) + lane % 16) * inter * (C::kWBytes / 16);
+    wp[r] = w + int64_t(min(16 * r + lane % 16, w_rows - 1)) * inter * (C::kWBytes / 16);
 #pragma unroll
     for (int g = 0; g < NG; ++g) acc[r][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 #pragma unroll
   for (int g = 0; g < NG; ++g) hp[g] = h + int64_t(list[min(g * 16 + lane % 16, n - 1)]) * inter * 2;
-  stream_products<C, RT, NG, 1>(wp, hp, begin, end, inter, acc);
+  stream_products<C, RT, NG, U>(wp, hp, begin, end, inter, acc);
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     const int at = g * 16 + lane % 16;
@@ -435,14 +445,15 @@ __device__ __forceinline__ void few_down_tile(const uint8_t* h, int inter, const
 
 // The results of experts with 16 or fewer slots.  Up to eight slots have two
 // of the 16 columns each, their h in bf16 and, `rest` bytes further, what bf16
-// left of it (0: nothing is kept); the columns' sums are added at the end.  `find(item)` gives an item's
-// rows and range of steps; items first, first + NW, .. below `items`
-// are taken, those with more slots passed over.  Two batches of U steps are in
-// registers or on their way, weights and activations together (loads end in
-// order, so activations requested later would wait for the next weights); the
-// requests walk on from expert to expert ahead of the products, so that the
-// stream of weights does not stop at an expert's end.  Past the last item, and
-// in columns without one, requests point past their buffer and read nothing.
+// left of it (0: nothing is kept); the columns' sums are added at the end.
+// `find(item)` gives an item's rows and range of steps; items first, first +
+// NW, .. below `items` are taken, those with more slots passed over.  Two
+// batches of U steps are in registers or on their way, weights and activations
+// together (loads end in order, so activations requested later would wait for
+// the next weights); the requests walk on from expert to expert ahead of the
+// products, so that the stream of weights does not stop at an expert's end.
+// Past the last item, and in columns without one, requests point past their
+// buffer and read nothing.
 struct DownItem {
   const uint8_t* w;      // the expert's rows of weights, 16 for each of RT
   const uint16_t* list;  // its slots
@@ -451,8 +462,8 @@ struct DownItem {
 };
 constexpr int kDppRowShl8 = 0x108;  // lane l of 16 reads lane l + 8, the upper eight read 0
 template <class C, int RT, int NW, int U, class Find>
-__device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_bytes, uint32_t rest, int inter, int w_rows, int base,
-                                                int first, int items, Find find) {
+__device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_bytes, uint32_t rest, int inter,
+                                                int w_rows, int base, int first, int items, Find find) {
   const int lane = threadIdx.x % kWave, group = lane / 16;
   constexpr int WV = C::kWBytes / 16, XV = C::kXBytes / 16;
   const uint32_t w_row = uint32_t(inter) * WV, nowhere = 0x80000000u;
@@ -563,24 +574,28 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
 // s_y (dynamic LDS): parts x chunk slots x 16*RT channels of fp32.  Slots are
 // taken `chunk` at a time, a whole number of tokens; with more than one chunk
 // an expert's weights are read for each that has a slot on it.
+// One row tile: at most 256 workgroups of 8 waves, so a wave may have 256
+// registers (with 128 the int8 form spills: 16 tokens, 4 of 24 experts,
+// 1040 x 528: the layer in 37 us instead of 35).
 template <class C, int RT, int NW, bool kScaled, typename IdT>
-__global__ __launch_bounds__(NW * kWave, 4) void k_few_down(
+__global__ __launch_bounds__(NW * kWave, RT == 1 ? 2 : 4) void k_few_down(
     const uint8_t* __restrict__ h, int n_rows, int hidden, int top_k, const IdT* __restrict__ ids,
     const float* __restrict__ router_weights, PadMask pad, int n_experts, const uint8_t* __restrict__ w,
-    const float* __restrict__ w_scales, int inter, int chunk, int max_parts, uint16_t* __restrict__ out) {
+    const float* __restrict__ w_scales, int inter, int channels, int chunk, int max_parts,
+    uint16_t* __restrict__ out) {
   extern __shared__ f32x4 s_y[];
   __shared__ uint32_t s_count[1024];  // slots per expert, then their first place in s_list
-  __shared__ uint16_t s_list[kDownSlots];
+  __shared__ uint16_t s_list[down_slots(RT)];
   __shared__ uint16_t s_expert[1024], s_start[1025];  // active experts
   __shared__ uint32_t s_scan[NW];
   constexpr int kThreads = NW * kWave, kQuads = 4 * RT;
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int all = n_rows * top_k, routed_end = real_slots(pad, n_rows, top_k);
-  const int c0 = blockIdx.x * 16 * RT, w_rows = min(16 * RT, hidden - c0);
+  const int c0 = blockIdx.x * channels, w_rows = min(channels, hidden - c0);
   constexpr int kBatch = 64 / (C::kWBytes * RT);  // steps: 4 KB of weights a wave
   for (int base = 0; base < all; base += chunk) {
     const int end = min(base + chunk, all), slots = min(end, routed_end);
-    constexpr int kOwn = kDownSlots / kThreads;
+    constexpr int kOwn = down_slots(RT) / kThreads;
     for (int e = tid; e < n_experts; e += kThreads) s_count[e] = 0;
     __syncthreads();
     int own_e[kOwn];
@@ -635,21 +650,29 @@ __global__ __launch_bounds__(NW * kWave, 4) void k_few_down(
       step_range(inter, p, parts, i.begin, i.end);
       return i.n <= 16;
     };
-    few_down_stream<C, RT, NW, kBatch>(h, uint64_t(all) * inter * 4, all <= kRestSlots ? uint32_t(all) * inter * 2 : 0u, inter, w_rows, base, uniform(wave),
+    const uint32_t rest = all <= kRestSlots ? uint32_t(all) * inter * 2 : 0u;
+    few_down_stream<C, RT, NW, kBatch>(h, uint64_t(all) * inter * 4, rest, inter, w_rows, base, uniform(wave),
                                        active * parts, find);
     for (int item = uniform(wave); item < active * parts; item += NW) {  // more than 16 slots
       DownItem i;
       if (find(item, i)) continue;
-      constexpr int kGroups = 4 / RT;  // 16 slots each, per pass over the weights
-      for (int j = 0; j < i.n; j += 16 * kGroups)
-        few_down_tile<C, RT, kGroups>(h, inter, i.w, w_rows, i.list + j, min(i.n - j, 16 * kGroups), i.begin, i.end,
-                                      base, i.y);
+      for (int j = 0; j < i.n;) {
+        if (RT == 1 && i.n - j > 32) {
+          few_down_tile<C, RT, 4 / RT, 1>(h, inter, i.w, w_rows, i.list + j, min(i.n - j, 64), i.begin, i.end, base,
+                                          i.y);
+          j += 64;
+        } else {
+          few_down_tile<C, RT, 2, 2 / RT>(h, inter, i.w, w_rows, i.list + j, min(i.n - j, 32), i.begin, i.end, base,
+                                          i.y);
+          j += 32;
+        }
+      }
     }
     __syncthreads();
 
     for (int i = tid; i < (end - base) / top_k * kQuads; i += kThreads) {
       const int t = base / top_k + i / kQuads, quad = i % kQuads, c = c0 + quad * 4;
-      if (c >= hidden) continue;
+      if (quad * 4 >= w_rows) continue;
       float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int j = 0; j < top_k; ++j) {
         const int slot = t * top_k + j;
@@ -694,17 +717,19 @@ hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
   }
 #undef MOE_GO
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  const int channels = std::min((p.hidden / 4 + kDownGroups - 1) / kDownGroups * 4, 32);
+  const int most = down_slots(channels > 16 ? 2 : 1);
   // Room for the results of the slots of a chunk, and for several parts of k while that stays within 512 slots' room.
-  const int chunk = slots <= kDownSlots ? slots : kDownSlots / p.top_k * p.top_k;
+  const int chunk = slots <= most ? slots : most / p.top_k * p.top_k;
   int max_parts = 1;
   while (max_parts < 8 && max_parts * 2 * chunk <= 512) max_parts *= 2;
   const size_t lds = size_t(max_parts) * chunk * 16 * sizeof(float);
 #define MOE_GO(RT, NW)                                                                                              \
-  hipLaunchKernelGGL((k_few_down<C, RT, NW, kScaled, IdT>), dim3((p.hidden + 16 * RT - 1) / (16 * RT)),             \
+  hipLaunchKernelGGL((k_few_down<C, RT, NW, kScaled, IdT>), dim3((p.hidden + channels - 1) / channels),             \
                      dim3(NW * kWave), lds * RT, s, reinterpret_cast<const uint8_t*>(p.h), p.n_rows, p.hidden,      \
                      p.top_k, p.ids, p.router_weights, p.pad, p.n_experts, static_cast<const uint8_t*>(p.w_down),   \
-                     p.down_scales, p.inter, chunk, max_parts, p.out)
-  if (p.hidden >= kDownWideMin) MOE_GO(2, 16);
+                     p.down_scales, p.inter, channels, chunk, max_parts, p.out)
+  if (channels > 16) MOE_GO(2, 16);
   else MOE_GO(1, 8);
 #undef MOE_GO
   return hipGetLastError();

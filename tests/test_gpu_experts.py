@@ -265,6 +265,9 @@ LAYERS = [
     (12, 3, 10, 6160, 80, "mixed"),
     (400, 3, 6, 6160, 48, "mixed"),
     (130, 8, 300, 6144, 16, "distinct"),
+    (40, 4, 6, 4112, 48, "mixed"),
+    (300, 5, 3, 2080, 144, "mixed"),
+    (9, 2, 7, 8240, 272, "distinct"),
 ]
 
 
