@@ -335,7 +335,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
     before += tiles[i];
   }
   if (tid == 0) s_first[kMaxActive] = total;
-  total = uniform(total);
+  total = min(uniform(total), 0xFFFFFF00u);  // the walk's next tile, 256 on, stays below 2^32
   __syncthreads();
 
   // Workgroups of one XCD (blockIdx % 8) take neighbouring tiles.

@@ -3,6 +3,8 @@
 // device memory.
 #include "moe_experts.h"
 
+#include <initializer_list>
+
 #include "entry.h"
 #include "experts.h"
 
@@ -19,9 +21,25 @@ constexpr int32_t kMaxFewWidth = 1 << 17;  // 4 bytes each of MOE_FEW_MAX_SLOTS 
 
 bool width_ok(int32_t n) { return n > 0 && n <= kMaxWidth && n % 16 == 0; }
 
-bool overlap(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes) {
-  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
-  return a != nullptr && b != nullptr && a_bytes > 0 && b_bytes > 0 && p < q + b_bytes && q < p + a_bytes;
+struct Span {
+  const void* at;
+  uint64_t bytes;
+};
+
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.at), q = reinterpret_cast<uintptr_t>(b.at);
+  return a.at != nullptr && b.at != nullptr && a.bytes > 0 && b.bytes > 0 && p < q + b.bytes && q < p + a.bytes;
+}
+
+// Whether something written lies on something read or on something else written.
+bool clash(std::initializer_list<Span> reads, std::initializer_list<Span> writes) {
+  for (const Span* w = writes.begin(); w != writes.end(); ++w) {
+    for (const Span& r : reads)
+      if (overlap(r, *w)) return true;
+    for (const Span* v = writes.begin(); v != w; ++v)
+      if (overlap(*v, *w)) return true;
+  }
+  return false;
 }
 
 template <typename IdT>
@@ -31,7 +49,8 @@ int layer_few(const uint16_t* x, int64_t n_rows, int32_t hidden, int32_t top_k, 
               const void* w_down, const float* down_scales, int32_t inter, uint16_t* output_tokens,
               void* workspace, size_t workspace_bytes, void* stream) {
   const size_t need = moe_layer_few_workspace_bytes(n_rows, top_k, inter);
-  if (need == 0 || !width_ok(hidden) || hidden > kMaxFewWidth || n_experts < 1 || n_experts > MOE_MAX_EXPERTS || tp_rank < 0)
+  if (need == 0 || !width_ok(hidden) || hidden > kMaxFewWidth || n_experts < 1 || n_experts > MOE_MAX_EXPERTS ||
+      tp_rank < 0)
     return MOE_ERR_INVALID_ARGUMENT;
   if (w_gate_up == nullptr || w_down == nullptr || (gate_up_scales == nullptr) != (down_scales == nullptr))
     return MOE_ERR_INVALID_ARGUMENT;
@@ -46,12 +65,17 @@ int layer_few(const uint16_t* x, int64_t n_rows, int32_t hidden, int32_t top_k, 
   if (n_rows > 0 && workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const uint64_t row_bytes = uint64_t(n_rows) * uint64_t(hidden) * 2, slots = uint64_t(n_rows) * uint64_t(top_k);
   const uint64_t w_bytes = uint64_t(n_experts) * uint64_t(hidden) * uint64_t(inter) * (gate_up_scales == nullptr ? 2 : 1);
-  const void* reads[] = {x, topk_ids, router_weights, w_gate_up, w_down};
-  const uint64_t read_bytes[] = {row_bytes, slots * sizeof(IdT), slots * 4, 2 * w_bytes, w_bytes};
-  for (int i = 0; i < 5; ++i)
-    if (overlap(reads[i], read_bytes[i], output_tokens, row_bytes) || overlap(reads[i], read_bytes[i], workspace, need))
-      return MOE_ERR_INVALID_ARGUMENT;
-  if (overlap(output_tokens, row_bytes, workspace, need)) return MOE_ERR_INVALID_ARGUMENT;
+  const uint64_t channels = uint64_t(n_experts) * 4;
+  if (clash({{x, row_bytes},
+             {topk_ids, slots * sizeof(IdT)},
+             {router_weights, slots * 4},
+             {real_token_count, 4},
+             {w_gate_up, 2 * w_bytes},
+             {w_down, w_bytes},
+             {gate_up_scales, channels * 2 * uint64_t(inter)},
+             {down_scales, channels * uint64_t(hidden)}},
+            {{output_tokens, row_bytes}, {workspace, n_rows > 0 ? need : 0}}))
+    return MOE_ERR_INVALID_ARGUMENT;
   if (const int d = check_device()) return d;
   const moe::FewLayer<IdT> p{x, int(n_rows), hidden, top_k, topk_ids, router_weights,
                              moe::PadMask{real_token_count, top_k, tp_rank}, n_experts, w_gate_up,
@@ -74,8 +98,9 @@ int moe_dispatch_i8(const uint16_t* input_tokens, int64_t n_rows, int32_t hidden
   if (!aligned(input_tokens, 16) || !aligned(out_q, 16) || !aligned(out_scales, 4) ||
       !aligned(restore_token_order, 4))
     return MOE_ERR_INVALID_ARGUMENT;
-  if (n_rows > 0 && overlap(input_tokens, uint64_t(n_rows) * uint64_t(hidden) * 2, out_q,
-                            uint64_t(out_rows) * uint64_t(hidden)))
+  if (clash({{input_tokens, uint64_t(n_rows) * uint64_t(hidden) * 2},
+             {restore_token_order, uint64_t(n_rows) * uint64_t(top_k) * 4}},
+            {{out_q, uint64_t(out_rows) * uint64_t(hidden)}, {out_scales, uint64_t(out_rows) * 4}}))
     return MOE_ERR_INVALID_ARGUMENT;
   if (const int d = check_device()) return d;
   return launched(moe::launch_dispatch_i8(input_tokens, n_rows, hidden, top_k, restore_token_order,
@@ -91,7 +116,8 @@ int moe_quantize_i8(const uint16_t* x, int64_t n_rows, int32_t hidden, const uin
   if (!aligned(x, 16) || !aligned(out_q, 16) || !aligned(out_scales, 4) || !aligned(row_count, 4))
     return MOE_ERR_INVALID_ARGUMENT;
   const uint64_t n = uint64_t(n_rows) * uint64_t(hidden);
-  if (overlap(x, 2 * n, out_q, n)) return MOE_ERR_INVALID_ARGUMENT;
+  if (clash({{x, 2 * n}, {row_count, 4}}, {{out_q, n}, {out_scales, uint64_t(n_rows) * 4}}))
+    return MOE_ERR_INVALID_ARGUMENT;
   if (const int d = check_device()) return d;
   return launched(moe::launch_quantize_i8(x, n_rows, hidden, row_count, out_q, out_scales,
                                           static_cast<hipStream_t>(stream)));
@@ -114,11 +140,14 @@ int moe_expert_matmul_i8(const int8_t* a_q, const float* a_scales, int64_t a_row
       !aligned(expert_ids, 4) || !aligned(w_q, 16) || !aligned(w_scales, 16) || !aligned(out, 16))
     return MOE_ERR_INVALID_ARGUMENT;
   const bool swiglu = (flags & MOE_MATMUL_SWIGLU) != 0;
-  const uint64_t out_bytes = uint64_t(a_rows) * uint64_t(n_out) * 2;
-  const uint64_t wide = uint64_t(n_experts) * uint64_t(n_out) * (swiglu ? 2 : 1);
-  if (overlap(a_q, uint64_t(a_rows) * uint64_t(depth), out, out_bytes) ||
-      overlap(a_scales, uint64_t(a_rows) * 4, out, out_bytes) ||
-      overlap(w_q, wide * uint64_t(depth), out, out_bytes) || overlap(w_scales, wide * 4, out, out_bytes))
+  const uint64_t rows = uint64_t(a_rows), wide = uint64_t(n_experts) * uint64_t(n_out) * (swiglu ? 2 : 1);
+  if (clash({{a_q, rows * uint64_t(depth)},
+             {a_scales, rows * 4},
+             {expert_start_indices, uint64_t(n_experts + 1) * 4},
+             {expert_ids, uint64_t(n_experts) * 4},
+             {w_q, wide * uint64_t(depth)},
+             {w_scales, wide * 4}},
+            {{out, rows * uint64_t(n_out) * 2}}))
     return MOE_ERR_INVALID_ARGUMENT;
   if (const int d = check_device()) return d;
   const moe::ExpertMatmul p{a_q, a_scales, uint32_t(a_rows), expert_start_indices, expert_ids,

@@ -44,10 +44,10 @@ extern "C" {
  * touched by it.
  *
  *   input_tokens, n_rows, top_k, restore_token_order  as moe_dispatch.
- *   hidden        > 0, a multiple of 16.
- *   out_q         [device] int8 [out_rows, hidden], 16-byte aligned; must not
- *                 overlap input_tokens.
- *   out_scales    [device] fp32 [out_rows].
+ *   hidden        > 0, a multiple of 16, at most 1048576.
+ *   out_q         [device] int8 [out_rows, hidden], 16-byte aligned.
+ *   out_scales    [device] fp32 [out_rows].  Neither of the outputs may overlap
+ *                 an input or the other.
  * Rows no slot points to are left untouched; positions >= out_rows are
  * skipped.  Rows with nothing routed are not read.
  */
@@ -61,14 +61,15 @@ int moe_dispatch_i8(const uint16_t* input_tokens, int64_t n_rows, int32_t hidden
  * once (a weight's output channels are its rows).
  *
  *   x             [device] bf16 [n_rows, hidden], 16-byte aligned.
- *   n_rows        0 <= n_rows <= 0xFFFFFFFE; hidden > 0, a multiple of 16.
+ *   n_rows        0 <= n_rows <= 0xFFFFFFFE; hidden > 0, a multiple of 16,
+ *                 at most 1048576.
  *   row_count     [device] uint32[1] or NULL: rows [0, min(n_rows, *row_count))
  *                 are quantised (expert_start_indices + n_experts holds the
  *                 number of routed slots); the others are neither read nor
  *                 written.  NULL: all n_rows.
- *   out_q         [device] int8 [n_rows, hidden], 16-byte aligned; must not
- *                 overlap x.
- *   out_scales    [device] fp32 [n_rows].
+ *   out_q         [device] int8 [n_rows, hidden], 16-byte aligned.
+ *   out_scales    [device] fp32 [n_rows].  Neither of the outputs may overlap
+ *                 an input or the other.
  */
 int moe_quantize_i8(const uint16_t* x, int64_t n_rows, int32_t hidden, const uint32_t* row_count,
                     int8_t* out_q, float* out_scales, void* stream);
@@ -125,6 +126,8 @@ size_t moe_layer_few_workspace_bytes(int64_t n_rows, int32_t top_k, int32_t inte
  * with fp32 sums.  Between the kernels h is held as two bf16 values (16 bits of
  * mantissa), or as one where n_rows*top_k is above 512 or more than eight slots
  * share an expert.  Tokens without a routed choice are written as +0.
+ * Infinities and NaNs in a token stay in its own output; an infinite weight
+ * may give NaN where the formula gives an infinity.
  *
  *   x              [device] bf16 [n_rows, hidden], 16-byte aligned.
  *   n_rows, top_k  n_rows*top_k <= MOE_FEW_MAX_SLOTS, 1 <= top_k <= MOE_MAX_TOP_K.

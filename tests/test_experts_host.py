@@ -100,6 +100,22 @@ def test_workspace_size():
         assert f(n, k, i) <= 4 * n * k * i + 256 and f(n, k, i) % 256 == 0
 
 
+def test_outputs_on_inputs_are_refused():
+    good = [F, 10, 32, 2, P(1 << 21), P(1 << 22), P(1 << 23), 20, None]
+    _refusals(mod.lib.moe_dispatch_i8, good, [(4, good[5]), (4, P((1 << 23) + 76)), (6, F), (6, P((1 << 22) + 636)),
+                                              (6, P((1 << 22) - 76)), (5, P((1 << 21) - 624))])
+    good = [F, 10, 32, P(1 << 21), P(1 << 22), P(1 << 23), None]
+    _refusals(mod.lib.moe_quantize_i8, good, [(5, P((1 << 20) + 636)), (3, P((1 << 22) + 316)), (5, P(1 << 21)),
+                                              (5, P((1 << 22) + 316))])
+    _refusals(mod.lib.moe_expert_matmul_i8, MATMUL, [(11, MATMUL[i]) for i in (0, 1, 3, 4, 6, 7)] +
+              [(3, P((7 << 20) - 16)), (4, P((7 << 20) + 636))])
+    layer = list(LAYER)
+    layer[6], layer[10], layer[12] = P(10 << 20), P(8 << 20), P(9 << 20)
+    for fn in (mod.lib.moe_layer_few, mod.lib.moe_layer_few_i64):
+        _refusals(fn, layer, [(out, layer[i]) for out in (14, 15) for i in (0, 4, 5, 6, 9, 10, 11, 12)] +
+                  [(6, P((7 << 20) + 1532)), (15, layer[14])])
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="a HIP device is present: valid arguments would launch")
 def test_valid_arguments_reach_the_device_check():
     assert mod.lib.moe_dispatch_i8(F, 10, 32, 2, P(1 << 21), P(1 << 22), P(1 << 23), 20, None) == OK_ON_HOST
