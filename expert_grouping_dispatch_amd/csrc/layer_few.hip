@@ -586,6 +586,8 @@ __global__ __launch_bounds__(NW * kWave, RT == 1 ? 2 : 4) void k_few_down(
   extern __shared__ f32x4 s_y[];
   __shared__ uint32_t s_count[1024];  // slots per expert, then their first place in s_list
   __shared__ uint16_t s_list[down_slots(RT)];
+  __shared__ int16_t s_of[down_slots(RT)];  // a slot's expert, -1: none
+  __shared__ float s_weight[down_slots(RT)];
   __shared__ uint16_t s_expert[1024], s_start[1025];  // active experts
   __shared__ uint32_t s_scan[NW];
   constexpr int kThreads = NW * kWave, kQuads = 4 * RT;
@@ -604,6 +606,10 @@ __global__ __launch_bounds__(NW * kWave, RT == 1 ? 2 : 4) void k_few_down(
     for (int i = 0; i < kOwn; ++i) {
       const int slot = base + tid + i * kThreads;
       own_e[i] = slot < slots ? expert_of(ids, slot, n_experts) : -1;
+      if (slot < end) {
+        s_of[slot - base] = int16_t(own_e[i]);
+        s_weight[slot - base] = router_weights[slot];
+      }
       if (own_e[i] >= 0) own_rank[i] = atomicAdd(&s_count[own_e[i]], 1u);
     }
     __syncthreads();
@@ -674,21 +680,31 @@ __global__ __launch_bounds__(NW * kWave, RT == 1 ? 2 : 4) void k_few_down(
       const int t = base / top_k + i / kQuads, quad = i % kQuads, c = c0 + quad * 4;
       if (quad * 4 >= w_rows) continue;
       float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int j = 0; j < top_k; ++j) {
-        const int slot = t * top_k + j;
-        const int e = slot < slots ? expert_of(ids, slot, n_experts) : -1;
-        if (e < 0) continue;
-        f32x4 y = s_y[(slot - base) * kQuads + quad];
-        for (int p = 1; p < parts; ++p) {
-          const f32x4 v = s_y[(p * chunk + slot - base) * kQuads + quad];
+      const int from = i / kQuads * top_k;
+      constexpr int kAhead = kScaled ? 4 : 1;  // choices whose scales are requested together
+      for (int first = 0; first < top_k; first += kAhead) {
+        f32x4 scale[kAhead];
+        if constexpr (kScaled)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) y[q] += v[q];
-        }
-        const float rw = router_weights[slot];
+          for (int j = 0; j < kAhead; ++j)
+            scale[j] = *reinterpret_cast<const f32x4*>(
+                w_scales + int64_t(max(int(s_of[from + min(first + j, top_k - 1)]), 0)) * hidden + c);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if constexpr (kScaled) y[q] *= w_scales[int64_t(e) * hidden + c + q];
-          o[q] += rw * y[q];
+        for (int j = 0; j < kAhead; ++j) {
+          const int slot = from + first + j;
+          if (first + j >= top_k || s_of[slot] < 0) continue;
+          f32x4 y = s_y[slot * kQuads + quad];
+          for (int p = 1; p < parts; ++p) {
+            const f32x4 v = s_y[(p * chunk + slot) * kQuads + quad];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) y[q] += v[q];
+          }
+          const float rw = s_weight[slot];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if constexpr (kScaled) y[q] *= scale[j][q];
+            o[q] += rw * y[q];
+          }
         }
       }
       *reinterpret_cast<u32x2*>(out + int64_t(t) * hidden + c) = u32x2{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
