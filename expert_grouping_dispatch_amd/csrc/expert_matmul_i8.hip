@@ -36,9 +36,9 @@ constexpr int kTileThreads = 256, kStripThreads = 256;
 constexpr int kStripFrags = 2;  // of 32 weight rows, for each wave
 // Grids of k_matmul_strip of at least this many workgroups; smaller ones leave
 // CUs idle and go to k_matmul_few.  Strips against k_matmul_few in us: 64
-// workgroups (8 experts, 20 rows each, 7168 -> 2048) 67 and 35, 128 (8, 20,
-// 4096 -> 4096) 44 and 39, 256 (16, 20, 4096 -> 4096) 49 and 73, 896 (32, 16,
-// 2048 -> 7168) 83 and 115.
+// workgroups (8 experts, 20 rows each, 7168 -> 2048) 67 and 33, 128 (8, 20,
+// 4096 -> 4096) 45 and 36, 256 (16, 20, 4096 -> 4096) 49 and 66, 896 (32, 16,
+// 2048 -> 7168) 83 and 99.
 constexpr uint32_t kStripsMin = 256;
 constexpr int kMaxActive = 1024;
 
@@ -74,7 +74,7 @@ __device__ __forceinline__ void matmul_few_tile(const ExpertMatmul& p, uint32_t 
   }
   int begin, end;
   step_range(p.depth, wave, kFewWaves, begin, end);
-  stream_products<CoreI8, 2, NG, (NG == 1 ? 8 : NG == 2 ? 4 : 2)>(wp, ap, begin, end, p.depth, acc);
+  stream_products<CoreI8, 2, NG, (NG == 4 ? 2 : 4)>(wp, ap, begin, end, p.depth, acc);
 #pragma unroll
   for (int r = 0; r < 2; ++r)
 #pragma unroll

@@ -75,9 +75,20 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return uint32_t(__builtin_amdgcn_readfirstlane(int(v))); }
 
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return reinterpret_cast<const uint8_t*>(uint64_t(uniform(uint32_t(v >> 32))) << 32 | uniform(uint32_t(v)));
+}
+
 // The upper half of `a`'s lanes changes places with the lower half of `b`'s.
 __device__ __forceinline__ u32x2 permlane32_swap(uint32_t a, uint32_t b) {
   const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  return u32x2{r[0], r[1]};
+}
+
+// The odd rows of 16 of `a`'s lanes change places with the even rows of `b`'s.
+__device__ __forceinline__ u32x2 permlane16_swap(uint32_t a, uint32_t b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
   return u32x2{r[0], r[1]};
 }
 

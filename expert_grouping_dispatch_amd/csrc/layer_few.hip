@@ -14,19 +14,20 @@
 //                goes out in bf16, the type of the second product's matrix
 //                instruction, with what bf16 leaves of it beside.
 //   k_few_up_split  the same for small grids: 16 channels a workgroup, its waves
-//                share k.  4 experts, 1040 x 528, 13 tokens: 12 us, the latency of
+//                share k.  4 experts, 1040 x 528, 13 tokens: 11 us, the latency of
 //                two rounds of loads, the sums across waves and the launch.
 //   k_few_down   one workgroup per 4 to 32 output channels: groups the slots, its
 //                waves take (expert, part of k) items, every slot's result goes to
 //                its own place in LDS in fp32, and then each token's choices are
 //                summed in ascending order, so the result does not depend on which
-//                wave came first.  The instruction has 16 columns; in calls of few
-//                slots an expert with up to eight of them uses the others for what
-//                bf16 left of h, so that the output's own rounding is all the error
-//                there is (0.0016 instead of 0.0023 of the result's norm).  Weights
-//                go straight to registers (stream.h), since LDS holds the results:
-//                636 us and 5.7 TB/s for the int8 layer above, 46 us and 5.1 TB/s
-//                for the bf16 one; 36 cycles of the address unit a load bound it.
+//                wave came first.  Weights go straight to registers, since LDS
+//                holds the results: in whole lines for 4x4 products where an
+//                expert has a few slots and long rows, in 16x16 products else.
+//                The int8 layer above 588 us, 6.2 TB/s; the bf16 one 44 us, 5.4
+//                TB/s.  Calls of few slots keep what bf16 left of h beside it, in
+//                columns that the instruction has to spare, so that the output's
+//                own rounding is all the error there is (0.0016 instead of 0.0023
+//                of the result's norm).
 #include <algorithm>
 
 #include "experts.h"
@@ -98,16 +99,25 @@ struct UpI8 {
 // ones leave CUs idle and take 16 channels a workgroup (k_few_up_split).  The
 // layer in us, 64 channels against 16: 32 workgroups (1 token, 1 of 8 experts,
 // 8192 x 2048, bf16) 83 and 33, 128 workgroups (4 tokens, 2 of 8, 4096 x 1024)
-// 54 and 39, 256 workgroups (1 token, 8 of 64, 7168 x 2048) 124 and 155.
+// 53 and 34, 256 workgroups (1 token, 8 of 64, 7168 x 2048) 122 and 121, 512
+// workgroups (1 token, 8 of 32, 4096 x 4096) 141 and 144.
 constexpr int kUpStripsMin = 256;
 // Output channels a workgroup of k_few_down: what spreads them over this many
-// workgroups, in groups of four, at most 32; above 16 the workgroup has 16
-// waves of two row tiles.  Rows of a tile past the workgroup's are not read.
+// workgroups, in groups of four, at most 32; above 16 the workgroup has two
+// row tiles.  Rows of a tile past the workgroup's are not read.
 // 256 experts in int8, 776 slots, 7168 channels: 636 us with 28 each, 706 us
 // with 32 on 224 workgroups (the layer 1733 us then, 1939 us with 16).  Layers
 // in bf16: 2048 channels, 32 tokens, 8 of 64 experts: 212 us with 8 each, 236
 // us with 16; 5120 channels, 1 token, 8 of 64: 96 us with 20 each, 107 with 16.
 constexpr int kDownGroups = 256;
+constexpr int kDownWaves = 8;
+// Rows of w_down of at least this many values are read in whole lines
+// (few_down_lines) for experts with few slots.  The layer with and without: 97
+// tokens, 8 of 256 experts, 7168 x 2048 in int8, second product 588 and 660 us;
+// 1 token, 2 of 8, 4096 x 14336 in bf16, 116 and 120 us; 4 tokens, 8 of 64,
+// 2048 x 2048, 120 and 126 us; 32 tokens, 8 of 64, 2048 x 1408, 208 and 210 us;
+// 1 token, 8 of 64, 2048 x 1024, 27.3 and 26.3 us.
+constexpr int kLinesMin = 1280;
 constexpr int kUpMost = 3;  // buffers
 // What bf16 leaves of two values whose bf16 forms are `hi`, in bf16; nothing
 // where that is infinite or NaN.
@@ -153,7 +163,8 @@ __device__ __forceinline__ void few_up(const uint8_t* x, int n_rows, int hidden,
   const __amdgpu_buffer_rsrc_t gate = buffer_of(w + at_gate, w_bytes - at_gate);
   const __amdgpu_buffer_rsrc_t up = buffer_of(w + at_up, w_bytes - at_up);
   const int w_piece[2] = {(lane % 8) ^ (lane / 16), (lane % 8) ^ (4 + lane / 16)};
-  const uint32_t w_off[2] = {uint32_t(lane / 8) * w_row + w_piece[0] * 16, uint32_t(lane / 8) * w_row + w_piece[1] * 16};
+  const uint32_t w_off[2] = {uint32_t(lane / 8) * w_row + w_piece[0] * 16,
+                             uint32_t(lane / 8) * w_row + w_piece[1] * 16};
   // Activations: request i = wave + 4*j fills rows from i*8 (128-byte rows) or i*4.
   const __amdgpu_buffer_rsrc_t rows = buffer_of(x, uint64_t(n_rows) * hidden * 2);
   int x_piece[kXFills];
@@ -354,7 +365,8 @@ __device__ __forceinline__ void few_up_split(const uint8_t* x, int hidden, int t
     for (int g = 0; g < NG; ++g) acc[r][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   int begin, end;
   step_range(hidden, wave, kUpWaves, begin, end);
-  stream_products<C, 2, NG, (NG == 1 ? 8 : NG == 2 ? 4 : 2)>(wp, xp, begin, end, hidden, acc);
+  constexpr int U = 128 / C::kWBytes / NG;  // what the registers hold
+  stream_products<C, 2, NG, U>(wp, xp, begin, end, hidden, acc);
 #pragma unroll
   for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -415,8 +427,7 @@ __global__ __launch_bounds__(kUpThreads, 2) void k_few_up_split(
 // ---- down and the weighted sum ------------------------------------------------
 
 // The results of n <= 16*NG slots over steps [begin, end), U of them requested
-// at a time.  NG 2 with U 2 where it is enough: 32 slots on each of 64 experts,
-// 1024 -> 4096 in bf16: 208 us against 232 us with NG 4 and U 1.
+// at a time.
 template <class C, int RT, int NG, int U>
 __device__ __forceinline__ void few_down_tile(const uint8_t* h, int inter, const uint8_t* w, int w_rows,
                                               const uint16_t* list, int n, int begin, int end, int base,
@@ -443,11 +454,11 @@ __device__ __forceinline__ void few_down_tile(const uint8_t* h, int inter, const
   }
 }
 
-// The results of experts with 16 or fewer slots.  Up to eight slots have two
-// of the 16 columns each, their h in bf16 and, `rest` bytes further, what bf16
-// left of it (0: nothing is kept); the columns' sums are added at the end.
-// `find(item)` gives an item's rows and range of steps; items first, first +
-// NW, .. below `items` are taken, those with more slots passed over.  Two
+// The results of the experts that `find` takes, with 16 or fewer slots.  Up to
+// eight slots have two of the 16 columns each, their h in bf16 and, `rest`
+// bytes further, what bf16 left of it (0: nothing is kept); the columns' sums
+// are added at the end.  `find(item)` gives an item's rows and part of k, of
+// 2^bits, or false; items first, first + NW, .. below `items` are taken.  Two
 // batches of U steps are in registers or on their way, weights and activations
 // together (loads end in order, so activations requested later would wait for
 // the next weights); the requests walk on from expert to expert ahead of the
@@ -458,26 +469,28 @@ struct DownItem {
   const uint8_t* w;      // the expert's rows of weights, 16 for each of RT
   const uint16_t* list;  // its slots
   f32x4* y;              // where the results of this part of k go
-  int n, begin, end;
+  int n, part;
 };
 constexpr int kDppRowShl8 = 0x108;  // lane l of 16 reads lane l + 8, the upper eight read 0
 template <class C, int RT, int NW, int U, class Find>
 __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_bytes, uint32_t rest, int inter,
-                                                int w_rows, int base, int first, int items, Find find) {
+                                                int w_rows, int base, int first, int items, int bits, Find find) {
   const int lane = threadIdx.x % kWave, group = lane / 16;
+  const int steps = (inter + kStreamStep - 1) / kStreamStep;
   constexpr int WV = C::kWBytes / 16, XV = C::kXBytes / 16;
   const uint32_t w_row = uint32_t(inter) * WV, nowhere = 0x80000000u;
   const __amdgpu_buffer_rsrc_t rows = buffer_of(h, h_bytes);
   struct Walk {
     DownItem i;
-    int at, s;
+    int at, s, end;
   };
   auto turn = [&](Walk& k) {  // to the next item; at >= items when there is none
     do k.at += NW;
     while (k.at < items && !find(k.at, k.i));
-    k.s = k.i.begin;
+    k.s = steps * k.i.part >> bits;
+    k.end = steps * (k.i.part + 1) >> bits;
   };
-  Walk ask, form;
+  Walk ask{}, form;
   ask.at = first - NW;
   turn(ask);
   if (ask.at >= items) return;
@@ -494,40 +507,27 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
   uint32_t x_lane = row_of(ask.i);
   auto request = [&](typename C::W(&w)[U][RT], typename C::X(&x)[U]) {
     const bool live = ask.at < items;
-    const __amdgpu_buffer_rsrc_t from = buffer_of(ask.i.w, uint64_t(w_rows) * w_row);
-    if (live && ask.s + U <= ask.i.end && (ask.s + U) * kStreamStep <= inter) {
+    // Scalars, or each load becomes a loop over the lanes' values.
+    const __amdgpu_buffer_rsrc_t from = buffer_of(uniform(ask.i.w), uint64_t(w_rows) * w_row);
+    const int s0 = uniform(ask.s);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; ++u) {
+      const int s = s0 + u;
+      uint32_t out = live && s < ask.end && s * kStreamStep + group * 16 < inter ? 0u : nowhere;
+      asm("" : "+v"(out));  // or the loads go into branches, and the products wait for all of them
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+      for (int r = 0; r < RT; ++r)
 #pragma unroll
-          for (int v = 0; v < WV; ++v)
-            w[u][r].v[v] = __builtin_amdgcn_raw_buffer_load_b128(from, w_lane[r] + 4 * C::kWBytes * u + 16 * v,
-                                                                 ask.s * 4 * C::kWBytes, 0);
+        for (int v = 0; v < WV; ++v)
+          w[u][r].v[v] = __builtin_amdgcn_raw_buffer_load_b128(from, (w_lane[r] | out) + 4 * C::kWBytes * u + 16 * v,
+                                                               s0 * 4 * C::kWBytes, 0);
 #pragma unroll
-        for (int v = 0; v < XV; ++v)
-          x[u].v[v] = __builtin_amdgcn_raw_buffer_load_b128(rows, x_lane + 4 * C::kXBytes * u + 16 * v,
-                                                            ask.s * 4 * C::kXBytes, 0);
-      }
-    } else {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int s = ask.s + u;
-        const bool some = live && s < ask.i.end && s * kStreamStep + group * 16 < inter;
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-          for (int v = 0; v < WV; ++v)
-            w[u][r].v[v] = __builtin_amdgcn_raw_buffer_load_b128(
-                from, some ? w_lane[r] + uint32_t(s) * 4 * C::kWBytes + 16 * v : nowhere, 0, 0);
-#pragma unroll
-        for (int v = 0; v < XV; ++v)
-          x[u].v[v] = __builtin_amdgcn_raw_buffer_load_b128(
-              rows, some ? x_lane + uint32_t(s) * 4 * C::kXBytes + 16 * v : nowhere, 0, 0);
-      }
+      for (int v = 0; v < XV; ++v)
+        x[u].v[v] = __builtin_amdgcn_raw_buffer_load_b128(rows, (x_lane | out) + 4 * C::kXBytes * u + 16 * v,
+                                                          s0 * 4 * C::kXBytes, 0);
     }
     ask.s += U;
-    if (live && ask.s >= ask.i.end) {
+    if (live && ask.s >= ask.end) {
       turn(ask);
       if (ask.at < items) x_lane = row_of(ask.i);
     }
@@ -544,7 +544,7 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
 #pragma unroll
       for (int r = 0; r < RT; ++r) acc[r] = C::mac(w[u][r], x[u], acc[r]);
     form.s += U;
-    if (form.s >= form.i.end) {
+    if (form.at < items && form.s >= form.end) {
       if (form.i.n <= pairs) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
@@ -565,7 +565,170 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
   while (form.at < items) {
     products(w0, x0);
     request(w0, x0);
-    if (form.at >= items) break;
+    products(w1, x1);  // of zeros after the last item; a way out here would let the first products wait for both
+    request(w1, x1);
+  }
+}
+
+// Weights and activations of 4x4 products, 16 of them an instruction: lane l
+// has 16 bytes of weight row l%4 and the same k of the slot in column l%4, and
+// the 16 blocks l/4 are sixteen pieces of k whose sums are joined at an item's
+// end.  So a load takes two whole cache lines of each of four rows, 8 lines;
+// in the 16x16 instruction's layout it takes pieces of 16 lines, and the
+// address unit needs about two cycles a line.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ f32x4 mac_4x4(uint32_t w0, uint32_t w1, uint32_t x0, uint32_t x1, f32x4 acc) {
+  return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4, (u32x2{w0, w1})),
+                                                __builtin_bit_cast(s16x4, (u32x2{x0, x1})), acc, 0, 0, 0);
+}
+struct DownBf16 {  // kStep values of k are 256 bytes of a weight row
+  typedef CoreBf16 Core;
+  static constexpr int kStep = 128, kWSize = 2, kXLoads = 1;
+  struct W { u32x4 v; };
+  static __device__ __forceinline__ W weights(const u32x4& w) { return W{w}; }
+  static __device__ __forceinline__ f32x4 mac(const W& w, const u32x4 (&x)[1], f32x4 acc) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc = mac_4x4(w.v[2 * j], w.v[2 * j + 1], x[0][2 * j], x[0][2 * j + 1], acc);
+    return acc;
+  }
+};
+struct DownI8 {
+  typedef CoreI8Bf16 Core;
+  static constexpr int kStep = 256, kWSize = 1, kXLoads = 2;
+  struct W { u32x2 v[4]; };
+  static __device__ __forceinline__ W weights(const u32x4& w) {
+    return W{{bf16_of_i8(w[0]), bf16_of_i8(w[1]), bf16_of_i8(w[2]), bf16_of_i8(w[3])}};
+  }
+  static __device__ __forceinline__ f32x4 mac(const W& w, const u32x4 (&x)[2], f32x4 acc) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      acc = mac_4x4(w.v[j].x, w.v[j].y, x[j / 2][j % 2 * 2], x[j / 2][j % 2 * 2 + 1], acc);
+    return acc;
+  }
+};
+
+// The four sums over the lanes of equal l%16/4.. of a, b, c, d: lane l gets that of the (l/16)-th.
+__device__ __forceinline__ float sum_rows(float a, float b, float c, float d) {
+  const u32x2 ac = permlane32_swap(__float_as_uint(a), __float_as_uint(c));
+  const u32x2 bd = permlane32_swap(__float_as_uint(b), __float_as_uint(d));
+  const float p = __uint_as_float(ac.x) + __uint_as_float(ac.y), q = __uint_as_float(bd.x) + __uint_as_float(bd.y);
+  const u32x2 r = permlane16_swap(__float_as_uint(p), __float_as_uint(q));
+  return __uint_as_float(r.x) + __uint_as_float(r.y);
+}
+
+// The same for experts with up to eight slots, or four with `rest`, in two
+// groups of four columns: of slots 0..3 and 4..7, or of h and what bf16 left
+// of it.
+constexpr int kOnce = 2;  // non-temporal: data that no other read wants
+constexpr int kDppRowRor4 = 0x124, kDppRowRor8 = 0x128;  // lane l of 16 reads lane l - 4 or l - 8, cyclically
+template <class D, int RT, int NW, int U, class Find>
+__device__ __forceinline__ void few_down_lines(const uint8_t* h, uint64_t h_bytes, uint32_t rest, int inter,
+                                                int w_rows, int base, int first, int items, int bits, Find find) {
+  constexpr int RG = 4 * RT, XV = D::kXLoads, kStep = D::kStep;
+  const int lane = threadIdx.x % kWave, column = lane % 4, block = lane / 4;
+  const uint32_t w_row = uint32_t(inter) * D::kWSize, nowhere = 0x80000000u;
+  const __amdgpu_buffer_rsrc_t rows = buffer_of(h, h_bytes);
+  const int most = rest != 0 ? 4 : 8;  // slots of an item
+  const int steps = (inter + kStep - 1) / kStep;
+  struct Walk {
+    DownItem i;
+    int at, s, end;
+  };
+  auto turn = [&](Walk& k) {  // to the next item; at >= items when there is none
+    do k.at += NW;
+    while (k.at < items && !find(k.at, k.i));
+    k.s = steps * k.i.part >> bits;
+    k.end = steps * (k.i.part + 1) >> bits;
+  };
+  Walk ask{}, form;
+  ask.at = first - NW;
+  turn(ask);
+  if (ask.at >= items) return;
+  form = ask;
+  uint32_t w_lane[RG], x_lane[2];
+#pragma unroll
+  for (int q = 0; q < RG; ++q) w_lane[q] = uint32_t(4 * q + column) * w_row + block * 16;
+  auto columns = [&] {  // of the item asked for
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int at = column + (rest != 0 ? 0 : 4 * g);
+      x_lane[g] = nowhere;
+      if (at < ask.i.n) x_lane[g] = uint32_t(ask.i.list[at]) * uint32_t(inter * 2) + g * rest + block * (16 * XV);
+    }
+  };
+  columns();
+  auto request = [&](u32x4(&w)[U][RG], u32x4(&x)[U][2][XV]) {
+    const bool live = ask.at < items;
+    const __amdgpu_buffer_rsrc_t from = buffer_of(uniform(ask.i.w), uint64_t(w_rows) * w_row);
+    const int s0 = uniform(ask.s);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int s = s0 + u;
+      uint32_t out = live && s < ask.end && s * kStep + block * (16 / D::kWSize) < inter ? 0u : nowhere;
+      asm("" : "+v"(out));
+#pragma unroll
+      for (int q = 0; q < RG; ++q)
+        w[u][q] = __builtin_amdgcn_raw_buffer_load_b128(from, (w_lane[q] | out) + 256 * u, s0 * 256, kOnce);
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int v = 0; v < XV; ++v)
+          x[u][g][v] = __builtin_amdgcn_raw_buffer_load_b128(rows, (x_lane[g] | out) + 2 * kStep * u + 16 * v,
+                                                             s0 * 2 * kStep, 0);
+    }
+    ask.s += U;
+    if (live && ask.s >= ask.end) {
+      turn(ask);
+      if (ask.at < items) columns();
+    }
+  };
+  f32x4 acc[RG][2];
+  auto clear = [&] {
+#pragma unroll
+    for (int q = 0; q < RG; ++q) acc[q][0] = acc[q][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  clear();
+  auto products = [&](const u32x4(&w)[U][RG], const u32x4(&x)[U][2][XV]) {
+    const bool two = uniform(int(rest != 0 || form.i.n > 4)) != 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int q = 0; q < RG; ++q) {
+        const typename D::W wq = D::weights(w[u][q]);
+        acc[q][0] = D::mac(wq, x[u][0], acc[q][0]);
+        if (two) acc[q][1] = D::mac(wq, x[u][1], acc[q][1]);
+      }
+    form.s += U;
+    if (form.at < items && form.s >= form.end) {
+      const int quad = block % 4;  // the group this lane writes
+      const int at = 4 * quad + column;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float t[2];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            t[g] = sum_rows(acc[4 * r][g][i], acc[4 * r + 1][g][i], acc[4 * r + 2][g][i], acc[4 * r + 3][g][i]);
+            t[g] += __uint_as_float(dpp<kDppRowRor4, 0xF>(__float_as_uint(t[g])));
+            t[g] += __uint_as_float(dpp<kDppRowRor8, 0xF>(__float_as_uint(t[g])));
+          }
+          v[i] = rest != 0 ? t[0] + t[1] : quad == 0 ? t[0] : t[1];
+        }
+        if (4 * quad < most && at < form.i.n)
+          form.i.y[((int(form.i.list[at]) - base) * RT + r) * 4 + lane / 16] = v;
+      }
+      clear();
+      turn(form);
+    }
+  };
+  u32x4 w0[U][RG], w1[U][RG], x0[U][2][XV], x1[U][2][XV];
+  request(w0, x0);
+  request(w1, x1);
+  while (form.at < items) {
+    products(w0, x0);
+    request(w0, x0);
     products(w1, x1);
     request(w1, x1);
   }
@@ -574,11 +737,8 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
 // s_y (dynamic LDS): parts x chunk slots x 16*RT channels of fp32.  Slots are
 // taken `chunk` at a time, a whole number of tokens; with more than one chunk
 // an expert's weights are read for each that has a slot on it.
-// One row tile: at most 256 workgroups of 8 waves, so a wave may have 256
-// registers (with 128 the int8 form spills: 16 tokens, 4 of 24 experts,
-// 1040 x 528: the layer in 37 us instead of 35).
-template <class C, int RT, int NW, bool kScaled, typename IdT>
-__global__ __launch_bounds__(NW * kWave, RT == 1 ? 2 : 4) void k_few_down(
+template <class D, int RT, bool kScaled, typename IdT>
+__global__ __launch_bounds__(kDownWaves* kWave, 2) void k_few_down(
     const uint8_t* __restrict__ h, int n_rows, int hidden, int top_k, const IdT* __restrict__ ids,
     const float* __restrict__ router_weights, PadMask pad, int n_experts, const uint8_t* __restrict__ w,
     const float* __restrict__ w_scales, int inter, int channels, int chunk, int max_parts,
@@ -589,8 +749,9 @@ __global__ __launch_bounds__(NW * kWave, RT == 1 ? 2 : 4) void k_few_down(
   __shared__ int16_t s_of[down_slots(RT)];  // a slot's expert, -1: none
   __shared__ float s_weight[down_slots(RT)];
   __shared__ uint16_t s_expert[1024], s_start[1025];  // active experts
-  __shared__ uint32_t s_scan[NW];
-  constexpr int kThreads = NW * kWave, kQuads = 4 * RT;
+  __shared__ uint32_t s_scan[kDownWaves];
+  typedef typename D::Core C;
+  constexpr int NW = kDownWaves, kThreads = NW * kWave, kQuads = 4 * RT;
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int all = n_rows * top_k, routed_end = real_slots(pad, n_rows, top_k);
   const int c0 = blockIdx.x * channels, w_rows = min(channels, hidden - c0);
@@ -644,32 +805,44 @@ __global__ __launch_bounds__(NW * kWave, RT == 1 ? 2 : 4) void k_few_down(
     __syncthreads();
 
     // With fewer experts than waves, k is split so that every wave has work; every part has a step.
-    int parts = 1;
-    while (parts * 2 <= max_parts && parts * 2 * kStreamStep <= inter && parts * active < 2 * NW) parts *= 2;
-    auto find = [&](int item, DownItem& i) {
-      const int a = item / parts, p = item - a * parts;
+    int bits = 0;  // of the number of parts
+    while ((2 << bits) <= max_parts && (2 << bits) * kStreamStep <= inter && (active << bits) < 2 * NW) ++bits;
+    const int parts = 1 << bits;
+    auto item_of = [&](int item, DownItem& i) {
+      const int a = item >> bits, p = item & (parts - 1);
       const int first = uniform(s_start[a]);
       i.n = uniform(s_start[a + 1]) - first;
       i.list = s_list + first;
       i.w = w + (int64_t(uniform(s_expert[a])) * hidden + c0) * inter * (C::kWBytes / 16);
       i.y = s_y + p * chunk * kQuads;
-      step_range(inter, p, parts, i.begin, i.end);
-      return i.n <= 16;
+      i.part = p;
     };
     const uint32_t rest = all <= kRestSlots ? uint32_t(all) * inter * 2 : 0u;
-    few_down_stream<C, RT, NW, kBatch>(h, uint64_t(all) * inter * 4, rest, inter, w_rows, base, uniform(wave),
-                                       active * parts, find);
+    const uint64_t h_bytes = uint64_t(all) * inter * 4;
+    const int lines = inter < kLinesMin ? 0 : rest != 0 ? 4 : 8;  // slots of an expert up to which whole lines are read
+    if (lines > 0)
+      few_down_lines<D, RT, NW, 2 / RT>(h, h_bytes, rest, inter, w_rows, base, uniform(wave), active * parts, bits,
+                                        [&](int item, DownItem& i) {
+                                          item_of(item, i);
+                                          return i.n <= lines;
+                                        });
+    few_down_stream<C, RT, NW, kBatch>(h, h_bytes, rest, inter, w_rows, base, uniform(wave), active * parts, bits,
+                                       [&](int item, DownItem& i) {
+                                         item_of(item, i);
+                                         return i.n > lines && i.n <= 16;
+                                       });
     for (int item = uniform(wave); item < active * parts; item += NW) {  // more than 16 slots
       DownItem i;
-      if (find(item, i)) continue;
+      item_of(item, i);
+      if (i.n <= 16) continue;
+      int begin, end;
+      step_range(inter, i.part, parts, begin, end);
       for (int j = 0; j < i.n;) {
         if (RT == 1 && i.n - j > 32) {
-          few_down_tile<C, RT, 4 / RT, 1>(h, inter, i.w, w_rows, i.list + j, min(i.n - j, 64), i.begin, i.end, base,
-                                          i.y);
+          few_down_tile<C, RT, 4 / RT, 2>(h, inter, i.w, w_rows, i.list + j, min(i.n - j, 64), begin, end, base, i.y);
           j += 64;
         } else {
-          few_down_tile<C, RT, 2, 2 / RT>(h, inter, i.w, w_rows, i.list + j, min(i.n - j, 32), i.begin, i.end, base,
-                                          i.y);
+          few_down_tile<C, RT, 2, 4 / RT>(h, inter, i.w, w_rows, i.list + j, min(i.n - j, 32), begin, end, base, i.y);
           j += 32;
         }
       }
@@ -715,7 +888,7 @@ __global__ __launch_bounds__(NW * kWave, RT == 1 ? 2 : 4) void k_few_down(
 
 namespace {
 
-template <class Up, class C, bool kScaled, typename IdT>
+template <class Up, class D, bool kScaled, typename IdT>
 hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
   const int slots = p.n_rows * p.top_k;
   const bool by_slot = slots < p.n_experts;
@@ -729,7 +902,7 @@ hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
     MOE_GO(k_few_up, Up);
   } else {
     const dim3 grid(p.inter / 16, groups);
-    MOE_GO(k_few_up_split, C);
+    MOE_GO(k_few_up_split, typename D::Core);
   }
 #undef MOE_GO
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
@@ -740,13 +913,14 @@ hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
   int max_parts = 1;
   while (max_parts < 8 && max_parts * 2 * chunk <= 512) max_parts *= 2;
   const size_t lds = size_t(max_parts) * chunk * 16 * sizeof(float);
-#define MOE_GO(RT, NW)                                                                                              \
-  hipLaunchKernelGGL((k_few_down<C, RT, NW, kScaled, IdT>), dim3((p.hidden + channels - 1) / channels),             \
-                     dim3(NW * kWave), lds * RT, s, reinterpret_cast<const uint8_t*>(p.h), p.n_rows, p.hidden,      \
+#define MOE_GO(RT)                                                                                              \
+  hipLaunchKernelGGL((k_few_down<D, RT, kScaled, IdT>), dim3((p.hidden + channels - 1) / channels),             \
+                     dim3(kDownWaves * kWave), lds * RT, s, reinterpret_cast<const uint8_t*>(p.h), p.n_rows,        \
+                     p.hidden,                                                                                      \
                      p.top_k, p.ids, p.router_weights, p.pad, p.n_experts, static_cast<const uint8_t*>(p.w_down),   \
                      p.down_scales, p.inter, channels, chunk, max_parts, p.out)
-  if (channels > 16) MOE_GO(2, 16);
-  else MOE_GO(1, 8);
+  if (channels > 16) MOE_GO(2);
+  else MOE_GO(1);
 #undef MOE_GO
   return hipGetLastError();
 }
@@ -756,7 +930,7 @@ hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
 template <typename IdT>
 hipError_t launch_layer_few(const FewLayer<IdT>& p, hipStream_t s) {
   if (p.n_rows == 0) return hipSuccess;
-  return p.gate_up_scales != nullptr ? go<UpI8, CoreI8Bf16, true, IdT>(p, s) : go<UpBf16, CoreBf16, false, IdT>(p, s);
+  return p.gate_up_scales != nullptr ? go<UpI8, DownI8, true, IdT>(p, s) : go<UpBf16, DownBf16, false, IdT>(p, s);
 }
 
 template hipError_t launch_layer_few<int32_t>(const FewLayer<int32_t>&, hipStream_t);

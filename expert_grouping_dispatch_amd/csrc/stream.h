@@ -81,7 +81,9 @@ __device__ __forceinline__ u32x4 load_weight(const uint8_t* p) {
 // x[g] over steps [begin, end) of kStreamStep values of k.  w and x point at
 // this lane's row; `depth` values (a multiple of 16) are in a row, so in the
 // last step a lane group may have nothing: both operands are zero then and
-// nothing is read.  U steps of weights are requested together.
+// nothing is read.  U steps are requested together, all of them before the
+// first product: 50 rows on each of 4 experts, 4096 -> 2048 in int8: 18 us
+// against 23 us where the compiler places the loads.
 template <class C, int RT, int NG, int U>
 __device__ __forceinline__ void stream_products(const uint8_t* const (&w)[RT], const uint8_t* const (&x)[NG],
                                                 int begin, int end, int depth,
@@ -110,6 +112,7 @@ __device__ __forceinline__ void stream_products(const uint8_t* const (&w)[RT], c
           xv[u][g].v[i] =
               *reinterpret_cast<const u32x4*>(x[g] + (int64_t(s + u) * 4 + group) * C::kXBytes + 16 * i);
     }
+    __builtin_amdgcn_sched_barrier(0);  // or the loads are put between the products, to spare registers
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -143,8 +146,8 @@ __device__ __forceinline__ void stream_products(const uint8_t* const (&w)[RT], c
 // Steps [begin, end) of part p of n over a row of `depth` values.
 __device__ __forceinline__ void step_range(int depth, int p, int n, int& begin, int& end) {
   const int steps = (depth + kStreamStep - 1) / kStreamStep;
-  begin = int(int64_t(steps) * p / n);
-  end = int(int64_t(steps) * (p + 1) / n);
+  begin = steps * p / n;  // steps <= 2^15
+  end = steps * (p + 1) / n;
 }
 
 }  // namespace moe

@@ -268,6 +268,10 @@ LAYERS = [
     (40, 4, 6, 4112, 48, "mixed"),
     (300, 5, 3, 2080, 144, "mixed"),
     (9, 2, 7, 8240, 272, "distinct"),
+    (1, 2, 4, 48, 2048, "distinct"),
+    (40, 3, 8, 144, 2064, "mixed"),
+    (60, 2, 12, 4112, 2192, "mixed"),
+    (300, 2, 90, 64, 4112, "distinct"),
 ]
 
 
