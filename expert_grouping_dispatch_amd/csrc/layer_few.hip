@@ -41,8 +41,8 @@ namespace {
 constexpr int kFewMaxSlots = 2048;
 // Calls of up to this many slots keep what bf16 leaves of h.  Its loads are as
 // many as those of h itself, which shows once they hold up the weights: 776
-// routed of 2048 slots on 256 experts in int8, 7168 x 2048, takes 1798 us with
-// it and 1741 us without; one token in bf16 takes 120 us either way.
+// routed of 2048 slots on 256 experts in int8, 7168 x 2048, takes 1732 us with
+// it and 1658 us without; one token in bf16 takes 117 us either way.
 constexpr int kRestSlots = 512;
 constexpr int kUpWaves = 4, kUpThreads = kUpWaves * kWave;
 // Slots at a time in k_few_down with RT row tiles: 128 KB of results.  Half of
@@ -607,7 +607,8 @@ struct DownI8 {
   }
 };
 
-// The four sums over the lanes of equal l%16/4.. of a, b, c, d: lane l gets that of the (l/16)-th.
+// The four values that a (or b, c, d) has in lanes l%16 + 16*i, added: lane l
+// gets those of a, b, c or d by l/16.
 __device__ __forceinline__ float sum_rows(float a, float b, float c, float d) {
   const u32x2 ac = permlane32_swap(__float_as_uint(a), __float_as_uint(c));
   const u32x2 bd = permlane32_swap(__float_as_uint(b), __float_as_uint(d));
@@ -913,11 +914,10 @@ hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
   int max_parts = 1;
   while (max_parts < 8 && max_parts * 2 * chunk <= 512) max_parts *= 2;
   const size_t lds = size_t(max_parts) * chunk * 16 * sizeof(float);
-#define MOE_GO(RT)                                                                                              \
-  hipLaunchKernelGGL((k_few_down<D, RT, kScaled, IdT>), dim3((p.hidden + channels - 1) / channels),             \
+#define MOE_GO(RT)                                                                                                  \
+  hipLaunchKernelGGL((k_few_down<D, RT, kScaled, IdT>), dim3((p.hidden + channels - 1) / channels),                 \
                      dim3(kDownWaves * kWave), lds * RT, s, reinterpret_cast<const uint8_t*>(p.h), p.n_rows,        \
-                     p.hidden,                                                                                      \
-                     p.top_k, p.ids, p.router_weights, p.pad, p.n_experts, static_cast<const uint8_t*>(p.w_down),   \
+                     p.hidden, p.top_k, p.ids, p.router_weights, p.pad, p.n_experts, static_cast<const uint8_t*>(p.w_down),   \
                      p.down_scales, p.inter, channels, chunk, max_parts, p.out)
   if (channels > 16) MOE_GO(2);
   else MOE_GO(1);
