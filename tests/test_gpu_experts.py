@@ -272,6 +272,8 @@ LAYERS = [
     (40, 3, 8, 144, 2064, "mixed"),
     (60, 2, 12, 4112, 2192, "mixed"),
     (300, 2, 90, 64, 4112, "distinct"),
+    (1, 1, 2, 32, 1296, "distinct"),
+    (2, 1, 2, 32, 1264, "distinct"),
 ]
 
 
