@@ -10,9 +10,9 @@
 //                expert's slots and forms gate, up and h = silu(gate)*up for up to
 //                64 of them at a time.  Weights come in whole cache lines through
 //                LDS: 247 active experts in int8, 7168 x 2048, 776 slots, 1105 us,
-//                6.6 TB/s; two experts in bf16, 4096 x 14336, 75 us, 6.3 TB/s.  h
-//                goes out in bf16, the type of the second product's matrix
-//                instruction, with what bf16 leaves of it beside.
+//                6.6 TB/s; two experts in bf16, 4096 x 14336, 73 us, 6.4 TB/s.  h
+//                goes out as two bf16 values, the type of the second product's
+//                matrix instruction: its rounding to bf16 and what that leaves.
 //   k_few_up_split  the same for small grids: 16 channels a workgroup, its waves
 //                share k.  4 experts, 1040 x 528, 13 tokens: 11 us, the latency of
 //                two rounds of loads, the sums across waves and the launch.
@@ -22,12 +22,16 @@
 //                summed in ascending order, so the result does not depend on which
 //                wave came first.  Weights go straight to registers, since LDS
 //                holds the results: in whole lines for 4x4 products where an
-//                expert has a few slots and long rows, in 16x16 products else.
-//                The int8 layer above 588 us, 6.2 TB/s; the bf16 one 44 us, 5.4
-//                TB/s.  Calls of few slots keep what bf16 left of h beside it, in
-//                columns that the instruction has to spare, so that the output's
-//                own rounding is all the error there is (0.0016 instead of 0.0023
-//                of the result's norm).
+//                expert has up to four slots and long rows, in 16x16 products
+//                else.  The int8 layer above 671 us, 5.4 TB/s; the bf16 one 44 us,
+//                5.4 TB/s.  Both parts of h are multiplied whatever the sizes, so
+//                that a token's result does not depend on how many others there
+//                are and the output's own rounding is all the error there is
+//                (0.0017 of the result's norm; 0.0023 with h in bf16 alone).  Up to
+//                eight slots find the second part's columns unused; beyond, its
+//                loads show: 200 tokens, 8 of 256 experts in int8, 2048 x 1024,
+//                the layer 464 us, 387 with h in bf16; 256 tokens on all of 8
+//                experts, 4096 x 2048, 644 and 393.
 #include <algorithm>
 
 #include "experts.h"
@@ -39,11 +43,6 @@ namespace moe {
 namespace {
 
 constexpr int kFewMaxSlots = 2048;
-// Calls of up to this many slots keep what bf16 leaves of h.  Its loads are as
-// many as those of h itself, which shows once they hold up the weights: 776
-// routed of 2048 slots on 256 experts in int8, 7168 x 2048, takes 1732 us with
-// it and 1658 us without; one token in bf16 takes 117 us either way.
-constexpr int kRestSlots = 512;
 constexpr int kUpWaves = 4, kUpThreads = kUpWaves * kWave;
 // Slots at a time in k_few_down with RT row tiles: 128 KB of results.  Half of
 // it read the weights of 64 experts, 1024 -> 4096, twice for 2048 slots: 323 us
@@ -126,15 +125,14 @@ __device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t hi) {
   return bf16_pair(fabsf(ra) < INFINITY ? ra : 0.0f, fabsf(rb) < INFINITY ? rb : 0.0f);
 }
 
-// h of four channels of a slot, at `to`, and what bf16 leaves of it, h_rest further (0: dropped).
+// h of four channels of a slot, at `to`, and what bf16 leaves of it, h_rest further.
 __device__ __forceinline__ void store_h(uint16_t* to, int64_t h_rest, const f32x4& gate, const f32x4& up) {
   float v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = silu_times(gate[i], up[i]);
   const u32x2 hi{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
   *reinterpret_cast<u32x2*>(to) = hi;
-  if (h_rest != 0)
-    *reinterpret_cast<u32x2*>(to + h_rest) = u32x2{rest_pair(v[0], v[1], hi.x), rest_pair(v[2], v[3], hi.y)};
+  *reinterpret_cast<u32x2*>(to + h_rest) = u32x2{rest_pair(v[0], v[1], hi.x), rest_pair(v[2], v[3], hi.y)};
 }
 
 struct UpBuffers {
@@ -315,7 +313,7 @@ __global__ __launch_bounds__(kUpThreads, 2) void k_few_up(const uint8_t* __restr
   __shared__ int s_n[2];
   int e;
   const int total = list_slots(ids, real_slots(pad, n_rows, top_k), n_experts, by_slot, s_list, s_n, e);
-  const int64_t h_rest = n_rows * top_k <= kRestSlots ? int64_t(n_rows) * top_k * inter : 0;
+  const int64_t h_rest = int64_t(n_rows) * top_k * inter;
   const uint64_t each = uint64_t(2) * inter * hidden * C::kWSize;
   const uint8_t* we = w + e * each;
   const float* se = kScaled ? w_scales + int64_t(e) * 2 * inter : nullptr;
@@ -410,7 +408,7 @@ __global__ __launch_bounds__(kUpThreads, 2) void k_few_up_split(
   __shared__ f32x4 s_part[kUpWaves * 2 * 4 * kWave];
   int e;
   const int total = list_slots(ids, real_slots(pad, n_rows, top_k), n_experts, by_slot, s_list, s_n, e);
-  const int64_t h_rest = n_rows * top_k <= kRestSlots ? int64_t(n_rows) * top_k * inter : 0;
+  const int64_t h_rest = int64_t(n_rows) * top_k * inter;
   const uint8_t* we = w + int64_t(e) * 2 * inter * hidden * (C::kWBytes / 16);
   const float* se = kScaled ? w_scales + int64_t(e) * 2 * inter : nullptr;
   for (int i = 0; i < total; i += 64) {
@@ -427,37 +425,47 @@ __global__ __launch_bounds__(kUpThreads, 2) void k_few_up_split(
 // ---- down and the weighted sum ------------------------------------------------
 
 // The results of n <= 16*NG slots over steps [begin, end), U of them requested
-// at a time.
+// at a time.  Each slot has two columns: its h in bf16 and, `rest` bytes
+// further, what bf16 left of it.
 template <class C, int RT, int NG, int U>
-__device__ __forceinline__ void few_down_tile(const uint8_t* h, int inter, const uint8_t* w, int w_rows,
-                                              const uint16_t* list, int n, int begin, int end, int base,
+__device__ __forceinline__ void few_down_tile(const uint8_t* h, uint32_t rest, int inter, const uint8_t* w,
+                                              int w_rows, const uint16_t* list, int n, int begin, int end, int base,
                                               f32x4* s_y) {
   const int lane = threadIdx.x % kWave;
   const uint8_t* wp[RT];
-  const uint8_t* hp[NG];
-  f32x4 acc[RT][NG];
+  const uint8_t* hp[2 * NG];
+  f32x4 acc[RT][2 * NG];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     wp[r] = w + int64_t(min(16 * r + lane % 16, w_rows - 1)) * inter * (C::kWBytes / 16);
 #pragma unroll
-    for (int g = 0; g < NG; ++g) acc[r][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int g = 0; g < 2 * NG; ++g) acc[r][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 #pragma unroll
-  for (int g = 0; g < NG; ++g) hp[g] = h + int64_t(list[min(g * 16 + lane % 16, n - 1)]) * inter * 2;
-  stream_products<C, RT, NG, U>(wp, hp, begin, end, inter, acc);
+  for (int g = 0; g < NG; ++g) {
+    hp[g] = h + int64_t(list[min(g * 16 + lane % 16, n - 1)]) * inter * 2;
+    hp[NG + g] = hp[g] + rest;
+  }
+  stream_products<C, RT, 2 * NG, U>(wp, hp, begin, end, inter, acc);
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     const int at = g * 16 + lane % 16;
     if (at < n)
 #pragma unroll
-      for (int r = 0; r < RT; ++r) s_y[((int(list[at]) - base) * RT + r) * 4 + lane / 16] = acc[r][g];
+      for (int r = 0; r < RT; ++r) {
+        f32x4 y = acc[r][g];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[q] += acc[r][NG + g][q];
+        s_y[((int(list[at]) - base) * RT + r) * 4 + lane / 16] = y;
+      }
   }
 }
 
-// The results of the experts that `find` takes, with 16 or fewer slots.  Up to
-// eight slots have two of the 16 columns each, their h in bf16 and, `rest`
-// bytes further, what bf16 left of it (0: nothing is kept); the columns' sums
-// are added at the end.  `find(item)` gives an item's rows and part of k, of
+// The results of the experts that `find` takes, with up to eight slots, or with
+// kWide up to 16.  Of up to eight slots each has two of the 16 columns, its h
+// in bf16 and, `rest` bytes further, what bf16 left of it, whose sums are
+// added at the end; of more slots each has a column of two products, with its
+// h and with the rest.  `find(item)` gives an item's rows and part of k, of
 // 2^bits, or false; items first, first + NW, .. below `items` are taken.  Two
 // batches of U steps are in registers or on their way, weights and activations
 // together (loads end in order, so activations requested later would wait for
@@ -472,12 +480,12 @@ struct DownItem {
   int n, part;
 };
 constexpr int kDppRowShl8 = 0x108;  // lane l of 16 reads lane l + 8, the upper eight read 0
-template <class C, int RT, int NW, int U, class Find>
+template <class C, int RT, int NW, int U, bool kWide, class Find>
 __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_bytes, uint32_t rest, int inter,
                                                 int w_rows, int base, int first, int items, int bits, Find find) {
   const int lane = threadIdx.x % kWave, group = lane / 16;
   const int steps = (inter + kStreamStep - 1) / kStreamStep;
-  constexpr int WV = C::kWBytes / 16, XV = C::kXBytes / 16;
+  constexpr int WV = C::kWBytes / 16, XV = C::kXBytes / 16, NX = kWide ? 2 : 1;
   const uint32_t w_row = uint32_t(inter) * WV, nowhere = 0x80000000u;
   const __amdgpu_buffer_rsrc_t rows = buffer_of(h, h_bytes);
   struct Walk {
@@ -498,14 +506,14 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
   uint32_t w_lane[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) w_lane[r] = uint32_t(16 * r + lane % 16) * w_row + group * C::kWBytes;
-  const int column = lane % 16, pairs = rest != 0 ? 8 : 0;  // most slots with two columns each
+  const int column = lane % 16;
   auto row_of = [&](const DownItem& i) {
-    const int at = i.n <= pairs ? column % 8 : column;
+    const int at = kWide ? column : column % 8;
     if (at >= i.n) return nowhere;
     return uint32_t(i.list[at]) * uint32_t(inter * 2) + (at < column ? rest : 0u) + group * C::kXBytes;
   };
   uint32_t x_lane = row_of(ask.i);
-  auto request = [&](typename C::W(&w)[U][RT], typename C::X(&x)[U]) {
+  auto request = [&](typename C::W(&w)[U][RT], typename C::X(&x)[U][NX]) {
     const bool live = ask.at < items;
     // Scalars, or each load becomes a loop over the lanes' values.
     const __amdgpu_buffer_rsrc_t from = buffer_of(uniform(ask.i.w), uint64_t(w_rows) * w_row);
@@ -522,9 +530,11 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
           w[u][r].v[v] = __builtin_amdgcn_raw_buffer_load_b128(from, (w_lane[r] | out) + 4 * C::kWBytes * u + 16 * v,
                                                                s0 * 4 * C::kWBytes, 0);
 #pragma unroll
-      for (int v = 0; v < XV; ++v)
-        x[u].v[v] = __builtin_amdgcn_raw_buffer_load_b128(rows, (x_lane | out) + 4 * C::kXBytes * u + 16 * v,
-                                                          s0 * 4 * C::kXBytes, 0);
+      for (int b = 0; b < NX; ++b)
+#pragma unroll
+        for (int v = 0; v < XV; ++v)
+          x[u][b].v[v] = __builtin_amdgcn_raw_buffer_load_b128(
+              rows, ((x_lane + b * rest) | out) + 4 * C::kXBytes * u + 16 * v, s0 * 4 * C::kXBytes, 0);
     }
     ask.s += U;
     if (live && ask.s >= ask.end) {
@@ -538,14 +548,16 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
     for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   };
   clear();
-  auto products = [&](const typename C::W(&w)[U][RT], const typename C::X(&x)[U]) {
+  auto products = [&](const typename C::W(&w)[U][RT], const typename C::X(&x)[U][NX]) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int r = 0; r < RT; ++r) acc[r] = C::mac(w[u][r], x[u], acc[r]);
+      for (int b = 0; b < NX; ++b)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[r] = C::mac(w[u][r], x[u][b], acc[r]);
     form.s += U;
     if (form.at < items && form.s >= form.end) {
-      if (form.i.n <= pairs) {
+      if constexpr (!kWide) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -559,7 +571,7 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
     }
   };
   typename C::W w0[U][RT], w1[U][RT];
-  typename C::X x0[U], x1[U];
+  typename C::X x0[U][NX], x1[U][NX];
   request(w0, x0);
   request(w1, x1);
   while (form.at < items) {
@@ -617,9 +629,8 @@ __device__ __forceinline__ float sum_rows(float a, float b, float c, float d) {
   return __uint_as_float(r.x) + __uint_as_float(r.y);
 }
 
-// The same for experts with up to eight slots, or four with `rest`, in two
-// groups of four columns: of slots 0..3 and 4..7, or of h and what bf16 left
-// of it.
+// The same for experts with up to four slots, in two groups of four columns: of
+// h, and of what bf16 left of it.
 constexpr int kOnce = 2;  // non-temporal: data that no other read wants
 constexpr int kDppRowRor4 = 0x124, kDppRowRor8 = 0x128;  // lane l of 16 reads lane l - 4 or l - 8, cyclically
 template <class D, int RT, int NW, int U, class Find>
@@ -629,7 +640,6 @@ __device__ __forceinline__ void few_down_lines(const uint8_t* h, uint64_t h_byte
   const int lane = threadIdx.x % kWave, column = lane % 4, block = lane / 4;
   const uint32_t w_row = uint32_t(inter) * D::kWSize, nowhere = 0x80000000u;
   const __amdgpu_buffer_rsrc_t rows = buffer_of(h, h_bytes);
-  const int most = rest != 0 ? 4 : 8;  // slots of an item
   const int steps = (inter + kStep - 1) / kStep;
   struct Walk {
     DownItem i;
@@ -652,9 +662,9 @@ __device__ __forceinline__ void few_down_lines(const uint8_t* h, uint64_t h_byte
   auto columns = [&] {  // of the item asked for
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const int at = column + (rest != 0 ? 0 : 4 * g);
       x_lane[g] = nowhere;
-      if (at < ask.i.n) x_lane[g] = uint32_t(ask.i.list[at]) * uint32_t(inter * 2) + g * rest + block * (16 * XV);
+      if (column < ask.i.n)
+        x_lane[g] = uint32_t(ask.i.list[column]) * uint32_t(inter * 2) + g * rest + block * (16 * XV);
     }
   };
   columns();
@@ -690,19 +700,16 @@ __device__ __forceinline__ void few_down_lines(const uint8_t* h, uint64_t h_byte
   };
   clear();
   auto products = [&](const u32x4(&w)[U][RG], const u32x4(&x)[U][2][XV]) {
-    const bool two = uniform(int(rest != 0 || form.i.n > 4)) != 0;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int q = 0; q < RG; ++q) {
         const typename D::W wq = D::weights(w[u][q]);
         acc[q][0] = D::mac(wq, x[u][0], acc[q][0]);
-        if (two) acc[q][1] = D::mac(wq, x[u][1], acc[q][1]);
+        acc[q][1] = D::mac(wq, x[u][1], acc[q][1]);
       }
     form.s += U;
     if (form.at < items && form.s >= form.end) {
-      const int quad = block % 4;  // the group this lane writes
-      const int at = 4 * quad + column;
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         f32x4 v;
@@ -715,10 +722,10 @@ __device__ __forceinline__ void few_down_lines(const uint8_t* h, uint64_t h_byte
             t[g] += __uint_as_float(dpp<kDppRowRor4, 0xF>(__float_as_uint(t[g])));
             t[g] += __uint_as_float(dpp<kDppRowRor8, 0xF>(__float_as_uint(t[g])));
           }
-          v[i] = rest != 0 ? t[0] + t[1] : quad == 0 ? t[0] : t[1];
+          v[i] = t[0] + t[1];
         }
-        if (4 * quad < most && at < form.i.n)
-          form.i.y[((int(form.i.list[at]) - base) * RT + r) * 4 + lane / 16] = v;
+        if (block % 4 == 0 && column < form.i.n)
+          form.i.y[((int(form.i.list[column]) - base) * RT + r) * 4 + lane / 16] = v;
       }
       clear();
       turn(form);
@@ -751,6 +758,7 @@ __global__ __launch_bounds__(kDownWaves* kWave, 2) void k_few_down(
   __shared__ float s_weight[down_slots(RT)];
   __shared__ uint16_t s_expert[1024], s_start[1025];  // active experts
   __shared__ uint32_t s_scan[kDownWaves];
+  __shared__ int s_forms;  // which of the forms below have an expert
   typedef typename D::Core C;
   constexpr int NW = kDownWaves, kThreads = NW * kWave, kQuads = 4 * RT;
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
@@ -761,6 +769,7 @@ __global__ __launch_bounds__(kDownWaves* kWave, 2) void k_few_down(
     const int end = min(base + chunk, all), slots = min(end, routed_end);
     constexpr int kOwn = down_slots(RT) / kThreads;
     for (int e = tid; e < n_experts; e += kThreads) s_count[e] = 0;
+    if (tid == 0) s_forms = 0;
     __syncthreads();
     int own_e[kOwn];
     uint32_t own_rank[kOwn];
@@ -778,6 +787,9 @@ __global__ __launch_bounds__(kDownWaves* kWave, 2) void k_few_down(
     // Each lane scans two experts: slots in the low half, active experts in the high.
     const uint32_t n0 = 2 * tid < n_experts ? s_count[2 * tid] : 0u;
     const uint32_t n1 = 2 * tid + 1 < n_experts ? s_count[2 * tid + 1] : 0u;
+    const int lines = inter < kLinesMin ? 0 : 4;  // slots of an expert up to which whole lines are read
+    auto form_of = [&](int n) { return n == 0 ? 0 : n <= lines ? 1 : n <= 8 ? 2 : n <= 16 ? 4 : 8; };
+    if (const int f = form_of(n0) | form_of(n1); f != 0) atomicOr(&s_forms, f);
     const uint32_t v0 = n0 | (n0 != 0 ? 0x10000u : 0u), v1 = n1 | (n1 != 0 ? 0x10000u : 0u);
     const uint32_t sum = wave_inclusive_sum(v0 + v1);
     if (lane == kWave - 1) s_scan[wave] = sum;
@@ -818,35 +830,35 @@ __global__ __launch_bounds__(kDownWaves* kWave, 2) void k_few_down(
       i.y = s_y + p * chunk * kQuads;
       i.part = p;
     };
-    const uint32_t rest = all <= kRestSlots ? uint32_t(all) * inter * 2 : 0u;
+    const uint32_t rest = uint32_t(all) * inter * 2;
     const uint64_t h_bytes = uint64_t(all) * inter * 4;
-    const int lines = inter < kLinesMin ? 0 : rest != 0 ? 4 : 8;  // slots of an expert up to which whole lines are read
-    if (lines > 0)
+    const int forms = uniform(s_forms);
+    if (forms & 1)
       few_down_lines<D, RT, NW, 2 / RT>(h, h_bytes, rest, inter, w_rows, base, uniform(wave), active * parts, bits,
                                         [&](int item, DownItem& i) {
                                           item_of(item, i);
                                           return i.n <= lines;
                                         });
-    few_down_stream<C, RT, NW, kBatch>(h, h_bytes, rest, inter, w_rows, base, uniform(wave), active * parts, bits,
-                                       [&](int item, DownItem& i) {
-                                         item_of(item, i);
-                                         return i.n > lines && i.n <= 16;
-                                       });
-    for (int item = uniform(wave); item < active * parts; item += NW) {  // more than 16 slots
+    if (forms & 2)
+      few_down_stream<C, RT, NW, kBatch, false>(h, h_bytes, rest, inter, w_rows, base, uniform(wave), active * parts,
+                                                bits, [&](int item, DownItem& i) {
+                                                  item_of(item, i);
+                                                  return i.n > lines && i.n <= 8;
+                                                });
+    if (forms & 4)
+      few_down_stream<C, RT, NW, kBatch, true>(h, h_bytes, rest, inter, w_rows, base, uniform(wave), active * parts,
+                                               bits, [&](int item, DownItem& i) {
+                                                 item_of(item, i);
+                                                 return i.n > 8 && i.n <= 16;
+                                               });
+    for (int item = uniform(wave); (forms & 8) && item < active * parts; item += NW) {  // more than 16 slots
       DownItem i;
       item_of(item, i);
       if (i.n <= 16) continue;
       int begin, end;
       step_range(inter, i.part, parts, begin, end);
-      for (int j = 0; j < i.n;) {
-        if (RT == 1 && i.n - j > 32) {
-          few_down_tile<C, RT, 4 / RT, 2>(h, inter, i.w, w_rows, i.list + j, min(i.n - j, 64), begin, end, base, i.y);
-          j += 64;
-        } else {
-          few_down_tile<C, RT, 2, 4 / RT>(h, inter, i.w, w_rows, i.list + j, min(i.n - j, 32), begin, end, base, i.y);
-          j += 32;
-        }
-      }
+      for (int j = 0; j < i.n; j += 32)
+        few_down_tile<C, RT, 2, 2>(h, rest, inter, i.w, w_rows, i.list + j, min(i.n - j, 32), begin, end, base, i.y);
     }
     __syncthreads();
 

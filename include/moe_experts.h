@@ -123,9 +123,8 @@ size_t moe_layer_few_workspace_bytes(int64_t n_rows, int32_t top_k, int32_t inte
  *   g = w_gate_up[e][0:inter] x[t],  u = w_gate_up[e][inter:2*inter] x[t]
  *   h = silu(g) * u,                 y_j = w_down[e] h
  *   out[t] = bf16( sum_{j routed, ascending} router_weights[t, j] * y_j )
- * with fp32 sums.  Between the kernels h is held as two bf16 values (16 bits of
- * mantissa), or as one where n_rows*top_k is above 512 or more than eight slots
- * share an expert.  Tokens without a routed choice are written as +0.
+ * with fp32 sums.  Between the kernels h is held as two bf16 values, 16 bits of
+ * mantissa.  Tokens without a routed choice are written as +0.
  * Infinities and NaNs in a token stay in its own output; an infinite weight
  * may give NaN where the formula gives an infinity.
  *

@@ -69,8 +69,7 @@ def layer_few(x: np.ndarray, ids: np.ndarray, router_weights: np.ndarray, w_gate
         (|g| + 8) u relative (the exponent's argument, the exponential, a
         quotient and two products);
       * h as two bf16 values: half a step of what half a step left, 2^-16
-        relative, for experts with up to eight slots in maps of up to 512; as
-        one, 2^-8, for others;
+        relative;
       * the output: 2^-8 relative;
       * the weighted sum: (top_k + 1) u.
     """
@@ -78,7 +77,6 @@ def layer_few(x: np.ndarray, ids: np.ndarray, router_weights: np.ndarray, w_gate
     n, hidden = x.shape
     inter = w_down.shape[2]
     x, rw = x.astype(np.float64), router_weights.astype(np.float64)
-    slots = np.bincount(ids[(ids >= 0) & (ids < w_gate_up.shape[0])], minlength=w_gate_up.shape[0])
     out, bound, total = np.zeros((n, hidden)), np.zeros((n, hidden)), np.zeros((n, hidden))
     for t in range(n):
         for j in range(ids.shape[1]):
@@ -91,7 +89,7 @@ def layer_few(x: np.ndarray, ids: np.ndarray, router_weights: np.ndarray, w_gate
             g, up, dg, du = v[:inter], v[inter:], dv[:inter], dv[inter:]
             h = swiglu(g, up)
             dh = 1.1 * dg * (np.abs(up) + du) + np.abs(g * _sigmoid(g)) * du
-            dh = dh + (np.abs(h) + dh) * ((half * half if slots[e] <= 8 and ids.size <= 512 else half) + (np.abs(g) + 8) * u24)
+            dh = dh + (np.abs(h) + dh) * (half * half + (np.abs(g) + 8) * u24)
             y = wd @ h
             dy = np.abs(wd) @ dh + (inter + 2) * u24 * (np.abs(wd) @ (np.abs(h) + dh))
             out[t] += rw[t, j] * y
