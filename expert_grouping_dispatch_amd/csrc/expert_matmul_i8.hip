@@ -150,7 +150,8 @@ __device__ __forceinline__ void strip(const ExpertMatmul& p, uint32_t lo, int n,
   // This wave's weight rows, LDS rows [32*F*wave, +32*F): channels c, c+1, ..
   constexpr int kWaveChannels = kSwiglu ? 16 * F : 32 * F;
   const int c = c0 + kWaveChannels * wave;
-  const uint64_t a_bytes = uint64_t(p.a_rows - lo) * p.depth, w_rows = uint64_t(p.n_experts) * wide;
+  // The activations' buffer ends with the group: rows behind it are zeros in LDS and not read.
+  const uint64_t a_bytes = uint64_t(n) * p.depth, w_rows = uint64_t(p.n_experts) * wide;
   const uint64_t w_row = uint64_t(e) * wide + min(c, p.n_out);
   const uint8_t* w = reinterpret_cast<const uint8_t*>(p.w);
   const __amdgpu_buffer_rsrc_t a_from = buffer_of(reinterpret_cast<const uint8_t*>(p.a) + uint64_t(lo) * p.depth, a_bytes);
