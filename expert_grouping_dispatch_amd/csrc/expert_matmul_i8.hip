@@ -410,18 +410,17 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
     load_to_lds(a_from, lane_off[i % 2], at, to_a + (64 * wave + 8 * i) * kStepBytes);
     load_to_lds(w_from, lane_off[i % 2], at, to_w + (64 * wave + 8 * i) * kStepBytes);
   };
-  // Waits for this wave's part of the buffer of step s.  In a tile's first step
-  // that was requested before the stores of the tile before it (`stored` of
-  // them) and the loads of this tile's scales (18 or 20), which need not be
-  // waited for: memory operations end in order.  Pieces past the row's end
-  // become zeros in the weights, so that they add nothing.
+  // Waits for everything this wave has asked for, its part of the buffer of
+  // step s among it.  In a tile's first step that includes the stores of the
+  // tile before it and the loads of this tile's scales; a wait that leaves them
+  // out would count on how many operations the compiler makes of them, and made
+  // no difference (16 steps a tile, 491520 rows: 7.56 to 7.61 ms either way).
+  // Pieces past the row's end become zeros in the weights, so that they add
+  // nothing.
   // Fragments of 32 channels for each wave; a lane has four of each eight, 8*q + (lane/32)*4 + i.
   constexpr int kOutFrags = kSwiglu ? 2 : 4;
-  static_assert(8 * kOutFrags + 16 <= 63, "s_waitcnt counts to 63");
-  auto arrived = [&](int s, uint8_t* w, int stored) __attribute__((always_inline)) {
-    if (stored == 8 * kOutFrags) __builtin_amdgcn_s_waitcnt(wait_all_but(8 * kOutFrags + 16));
-    else if (stored == 4 * kOutFrags) __builtin_amdgcn_s_waitcnt(wait_all_but(4 * kOutFrags + 16));
-    else __builtin_amdgcn_s_waitcnt(kWaitLoads);
+  auto arrived = [&](int s, uint8_t* w) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);
     asm volatile("" ::: "memory");
     if (ragged && s == steps - 1) {
 #pragma unroll
@@ -444,12 +443,11 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
 #pragma unroll
   for (int i = 0; i < 8; ++i) fetch(fs, s_a0, s_w0, i);
   fetched();
-  arrived(0, s_w0, 0);
+  arrived(0, s_w0);
 #pragma unroll
   for (int i = 0; i < 8; ++i) fetch(fs, s_a1, s_w1, i);
   fetched();
   bool odd = false;  // whether the tile's first step is in the second buffer
-  int stored = 0;    // the stores of the tile before this one, of each wave
 
   // A tile of up to 64*G rows, 32*G for each wave.
   auto form = [&](auto frags) __attribute__((always_inline)) {
@@ -521,7 +519,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
       }
       part(one, a, w, 2, none, na, nw, zero);
       part(zero, a, w, 3, none, na, nw, zero);
-      arrived(s + 1 < steps ? s + 1 : 0, nw, s == 0 ? stored : 0);
+      arrived(s + 1 < steps ? s + 1 : 0, nw);
       part(one, na, nw, 0, zero, a, w, zero);
     };
     int s = 0;
@@ -584,7 +582,6 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_matmul_tile(ExpertMatmul p)
         __builtin_amdgcn_sched_barrier(0);  // one fragment at a time, or the registers do not suffice
       }
     }
-    stored = 2 * kOutFrags * G;
   };
   do {
     if (now.n_rows > kTile / 2) form(std::integral_constant<int, 4>{});

@@ -101,3 +101,56 @@ def test_a_tokens_result_does_not_depend_on_the_padding():
         out = _layer_call(wide_x, wide_ids, wide_rw, *args[3:], count=n)
         np.testing.assert_array_equal(u16(out[:n]), u16(want))
         assert not u16(out[n:]).any()
+
+
+def _counted(counts, k, seed):
+    """A map in which expert e has counts[e] slots (a multiple of k in all), in random order."""
+    slots = np.repeat(np.arange(len(counts)), counts)
+    return np.random.default_rng(seed).permutation(slots).reshape(-1, k).astype(np.int32)
+
+
+SHARED = [
+    # slots of each expert, top_k, hidden, inter: grids that fill the CUs, through LDS 32 or 64 slots at a time
+    ([33, 40, 50, 64], 1, 1024, 4096),
+    ([33, 40, 51, 64], 2, 1040, 4112),
+    ([65, 80, 96, 1], 1, 1024, 4096),
+    ([97, 128, 129, 20], 2, 1040, 4096),
+    ([300, 64, 32, 200], 4, 144, 4096),
+    ([64, 65, 128, 129] * 4, 2, 256, 1040),
+    ([2, 5, 8, 9, 16, 17, 32, 33] * 5, 1, 2064, 528),     # every number that changes the second product's form
+    ([1, 4, 5, 8, 9, 16, 17, 40] * 3, 2, 4112, 1296),     # with long rows and two row tiles
+    ([3, 4, 5, 8, 9, 16, 17, 70], 2, 272, 2064),          # in long rows
+    ([1024, 1024], 8, 64, 64),
+    ([31, 33, 65, 1, 70], 5, 400, 80),                    # the smallest grids: 16 channels a workgroup
+]
+
+
+@pytest.mark.parametrize("weights", ["bf16", "int8"])
+@pytest.mark.parametrize("case", range(len(SHARED)))
+def test_layer_with_many_slots_on_an_expert(case, weights):
+    counts, k, h, i = SHARED[case]
+    ids = _counted(counts, k, 400 + case)
+    check(len(ids), k, len(counts), h, i, ids, weights, 400 + case)
+
+
+@pytest.mark.parametrize("weights", ["bf16", "int8"])
+@pytest.mark.parametrize("h, i", [(2048, 4096), (4112, 1296)])
+def test_layer_with_one_real_token_in_a_large_map(h, i, weights):
+    """256 x 8 slots of which one token's are routed, by the count and by the ids."""
+    n, k, e = 256, 8, 32
+    ids = np.full((n, k), -1, np.int32)
+    ids[0] = np.random.default_rng(3).permutation(e)[:k]
+    check(n, k, e, h, i, ids, weights, 500)
+    args, want = whole_layer(n, k, e, h, i, ids, weights, 501)
+    ids[1:] = np.arange(8)
+    out = _layer_call(args[0], ids, *args[2:], count=1)
+    np.testing.assert_array_equal(u16(out), u16(want))
+
+
+@pytest.mark.parametrize("weights", ["bf16", "int8"])
+def test_layer_with_weights_beyond_2_gib(weights):
+    """Byte offsets of both weights pass 31 bits, and 32 in the first product."""
+    n, k, e, h, i = 40, 4, 68, 8192, 4096
+    ids = _ids(np.random.default_rng(8), n, k, e, "distinct")
+    ids[0, 0], ids[1] = e - 1, [e - 2, 0, e - 3, 1]
+    check(n, k, e, h, i, ids, weights, 510)
