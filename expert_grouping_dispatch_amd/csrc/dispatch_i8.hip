@@ -102,6 +102,7 @@ __device__ __forceinline__ void quantize_row(const u32x4* __restrict__ src, int 
   uint32_t amax = 0;
   float scale, inv;
   auto load = [&](int v) { return v < vecs ? load_vec<kNonTemporal>(src + v) : zero; };
+  auto first_load = [&](int v) { return v < vecs ? load_vec<false>(src + v) : zero; };  // kept for the second
   auto write = [&](int base, const u32x4& lo, const u32x4& hi) {
     const u32x4 b = pair_i8(lo, hi, inv);
     const int at = tid % 2 == 0 ? base + tid : base + lanes + tid - 1;
@@ -121,7 +122,7 @@ __device__ __forceinline__ void quantize_row(const u32x4* __restrict__ src, int 
     for (int i = 0; i < U; ++i) write(2 * lanes * i, v[i][0], v[i][1]);
   } else {
     for (int b = 0; b < vecs; b += 2 * lanes)
-      amax = max(amax, max(vec_amax(load(b + tid)), vec_amax(load(b + lanes + tid))));
+      amax = max(amax, max(vec_amax(first_load(b + tid)), vec_amax(first_load(b + lanes + tid))));
     row_scale(block_max(amax, s_part), scale, inv);
     for (int b = 0; b < vecs; b += 2 * lanes) write(b, load(b + tid), load(b + lanes + tid));
   }
