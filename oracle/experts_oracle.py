@@ -5,7 +5,8 @@ shares no code with the HIP library.
     inv = fl32(127/a), q = fl32(x*inv) to the nearest integer, ties to even.
     Quotients and products are formed in 64 bits and rounded once: the product
     of a bf16 and an fp32 value is exact in 64 bits, and a 64-bit quotient of
-    two fp32 values rounds to the fp32 quotient.  Finite inputs.
+    two fp32 values rounds to the fp32 quotient.  A row with an infinity or a
+    NaN has scale NaN; its payload is unspecified, zeros here.
   * dispatch_i8 -- row p of the output is the quantised row of token
     token_expert_order[p] // top_k.
   * expert_values -- the fp32 values v of every row and weight row: the exact
@@ -26,10 +27,13 @@ F32 = np.float32
 
 def quantize_i8(x_bits: np.ndarray):
     x = bf16_bits_to_f32(x_bits).astype(np.float64)
+    bad = ~np.isfinite(x).all(axis=1)
+    x[bad] = 0.0
     a = np.maximum(np.abs(x).max(axis=1), 2.0 ** -118)
     scale = (a / 127.0).astype(F32)
     inv = (127.0 / a).astype(F32).astype(np.float64)
     q = np.rint((x * inv[:, None]).astype(F32).astype(np.float64))
+    scale[bad] = np.nan
     return q.astype(np.int8), scale
 
 

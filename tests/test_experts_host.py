@@ -4,6 +4,7 @@ import ctypes
 import os
 import re
 import subprocess
+import warnings
 from fractions import Fraction
 
 import numpy as np
@@ -159,6 +160,16 @@ def test_quantize_pins():
     # zeros and values below the floor
     q, s = oracle.quantize_i8(_bits([[0.0] * 16, [2.0 ** -119] * 16]))
     assert s.tolist() == [np.float32(2.0 ** -118 / 127)] * 2 and not q[0].any() and (q[1] == 64).all()
+
+
+def test_quantize_of_rows_that_are_not_finite():
+    """Scale NaN, no cast of a NaN to an integer, the other rows as they are."""
+    rows = np.ones((4, 16), np.float32) * 3
+    rows[0, 5], rows[2, 0], rows[3, 15] = np.nan, np.inf, -np.inf
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        q, s = oracle.quantize_i8(_bits(rows))
+    assert np.isnan(s[[0, 2, 3]]).all() and s[1] == np.float32(3 / 127) and (q[1] == 127).all()
 
 
 def test_quantize_against_rational_arithmetic():
