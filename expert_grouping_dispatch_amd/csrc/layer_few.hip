@@ -1,10 +1,14 @@
 // The whole layer for a few tokens in two kernels.
 //
-// Both products read every active expert's weights once: 6*hidden*inter bytes
-// per expert in bf16 (half in int8) against at most a few dozen rows of
+// Both products read an active expert's weights once where few slots share it:
+// 6*hidden*inter bytes per expert in bf16 (half in int8) against a few rows of
 // activations, so the layer is bound by how fast HBM delivers the weights.
-// Grouping costs each workgroup one pass over the few ids instead of a kernel
-// of its own.
+// With more slots the first product reads them once for every 64 of them, past
+// the caches, and the second once for every 32, mostly from L2; and the second
+// fetches all of h for each workgroup's few channels, so its time grows with
+// the slots: 8 experts, 4096 x 2048 in int8, 32, 64 and 128 slots on each take
+// 114, 208 and 366 us, the grouped path 82, 154 and 117 us.  Grouping costs each
+// workgroup one pass over the few ids instead of a kernel of its own.
 //
 //   k_few_up     one workgroup per (expert, 64 intermediate channels): lists the
 //                expert's slots and forms gate, up and h = silu(gate)*up for up to
@@ -23,15 +27,15 @@
 //                wave came first.  Weights go straight to registers, since LDS
 //                holds the results: in whole lines for 4x4 products where an
 //                expert has up to four slots and long rows, in 16x16 products
-//                else.  The int8 layer above 671 us, 5.4 TB/s; the bf16 one 44 us,
-//                5.4 TB/s.  Both parts of h are multiplied whatever the sizes, so
+//                else.  The int8 layer above 650 us, 5.6 TB/s; the bf16 one 43 us,
+//                5.5 TB/s.  Both parts of h are multiplied whatever the sizes, so
 //                that a token's result does not depend on how many others there
 //                are and the output's own rounding is all the error there is
-//                (0.0017 of the result's norm; 0.0023 with h in bf16 alone).  Up to
-//                eight slots find the second part's columns unused; beyond, its
-//                loads show: 200 tokens, 8 of 256 experts in int8, 2048 x 1024,
-//                the layer 464 us, 387 with h in bf16; 256 tokens on all of 8
-//                experts, 4096 x 2048, 644 and 393.
+//                (0.0017 of the result's norm; 0.0023 with h in bf16 alone).  The
+//                second part's loads show from about five slots an expert on: 97
+//                tokens, 8 of 256 experts in int8, 7168 x 2048, the layer 1734 us,
+//                1658 with h in bf16; 200 tokens, 2048 x 1024, 466 and 388; 256
+//                tokens on all of 8 experts, 4096 x 2048, 644 and 393.
 #include <algorithm>
 
 #include "experts.h"
@@ -45,8 +49,8 @@ namespace {
 constexpr int kFewMaxSlots = 2048;
 constexpr int kUpWaves = 4, kUpThreads = kUpWaves * kWave;
 // Slots at a time in k_few_down with RT row tiles: 128 KB of results.  Half of
-// it read the weights of 64 experts, 1024 -> 4096, twice for 2048 slots: 323 us
-// against 232 us.
+// it read the weights of 64 experts, 1024 -> 4096, twice for 2048 slots: the
+// layer 565 us against 521 us in bf16, 427 against 401 us in int8.
 constexpr int down_slots(int rt) { return 2048 / rt; }
 
 // Slots at or past the boundary row are unrouted.
@@ -104,18 +108,18 @@ constexpr int kUpStripsMin = 256;
 // Output channels a workgroup of k_few_down: what spreads them over this many
 // workgroups, in groups of four, at most 32; above 16 the workgroup has two
 // row tiles.  Rows of a tile past the workgroup's are not read.
-// 256 experts in int8, 776 slots, 7168 channels: 636 us with 28 each, 706 us
-// with 32 on 224 workgroups (the layer 1733 us then, 1939 us with 16).  Layers
-// in bf16: 2048 channels, 32 tokens, 8 of 64 experts: 212 us with 8 each, 236
-// us with 16; 5120 channels, 1 token, 8 of 64: 96 us with 20 each, 107 with 16.
+// Layers, 256 experts in int8, 776 slots, 7168 channels: 1734 us with 28 each,
+// 1755 us with 32 on 224 workgroups, 1925 us with 16; in bf16, 2048 channels, 32
+// tokens, 8 of 64 experts: 210 us with 8 each, 235 us with 16; 5120 channels, 1
+// token, 8 of 64: 53 us with 20 each, 64 with 16.
 constexpr int kDownGroups = 256;
 constexpr int kDownWaves = 8;
 // Rows of w_down of at least this many values are read in whole lines
 // (few_down_lines) for experts with few slots.  The layer with and without: 97
-// tokens, 8 of 256 experts, 7168 x 2048 in int8, second product 588 and 660 us;
-// 1 token, 2 of 8, 4096 x 14336 in bf16, 116 and 120 us; 4 tokens, 8 of 64,
-// 2048 x 2048, 120 and 126 us; 32 tokens, 8 of 64, 2048 x 1408, 208 and 210 us;
-// 1 token, 8 of 64, 2048 x 1024, 27.3 and 26.3 us.
+// tokens, 8 of 256 experts, 7168 x 2048 in int8, 1734 and 1806 us; 1 token, 2 of
+// 8, 4096 x 14336 in bf16, 116 and 121 us; 4 tokens, 8 of 64, 2048 x 2048, 120
+// and 126 us; 32 tokens, 8 of 64, 2048 x 1408, 210 and 213 us; 1 token, 8 of 64,
+// 2048 x 1024, 27.3 and 26.3 us.
 constexpr int kLinesMin = 1280;
 constexpr int kUpMost = 3;  // buffers
 // What bf16 leaves of two values whose bf16 forms are `hi`, in bf16; nothing

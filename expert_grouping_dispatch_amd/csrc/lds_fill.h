@@ -5,8 +5,11 @@
 
 namespace moe {
 
-// A buffer of `bytes` bytes at `base`: reads past it give zeros, away from
-// memory.  No kernel reads further than 2^30 bytes from its base.
+// A buffer of `bytes` bytes at `base`: reads past it give zeros, in registers
+// and in LDS, away from memory.  What is compared with the size is the whole
+// offset, the per-lane and the scalar part together, also where the scalar part
+// alone is past it (seen on a buffer over the start of a larger allocation).
+// No kernel reads further than 2^30 bytes from its base.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* base, uint64_t bytes) {
   const uint32_t size = bytes < (uint64_t(1) << 31) ? uint32_t(bytes) : 0x7FFFFFF0u;
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, size, 0x00027000);

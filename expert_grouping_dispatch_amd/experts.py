@@ -28,7 +28,8 @@ for _f in (lib.moe_layer_few, lib.moe_layer_few_i64):
 
 # The smallest of these calls take a few microseconds on the GPU, so the checks
 # are kept to what they must read: a tensor's type, its device's number, its
-# layout and its address.
+# layout and its address, and the stream comes as a number, without an object
+# for it (row quantisation of 64 x 256: 6.4 us against 7.5 us a call).
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 

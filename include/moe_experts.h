@@ -124,7 +124,9 @@ size_t moe_layer_few_workspace_bytes(int64_t n_rows, int32_t top_k, int32_t inte
  *   h = silu(g) * u,                 y_j = w_down[e] h
  *   out[t] = bf16( sum_{j routed, ascending} router_weights[t, j] * y_j )
  * with fp32 sums.  Between the kernels h is held as two bf16 values, 16 bits of
- * mantissa.  Tokens without a routed choice are written as +0.
+ * mantissa.  Made for few slots on an expert: its time grows with them, and from
+ * about four on each active expert the grouped calls (moe_create_indices to
+ * moe_combine) take less time on the GPU with int8 weights.  Tokens without a routed choice are written as +0.
  * Infinities and NaNs in a token stay in its own output; an infinite weight
  * may give NaN where the formula gives an infinity.
  *
