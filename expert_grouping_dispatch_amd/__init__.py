@@ -21,6 +21,13 @@ The experts' products between dispatch and combine (``include/moe_experts.h``):
            moe_quantize_i8(x, out_q, out_scales[, row_count])
            moe_expert_matmul_i8(a_q, a_scales, expert_start_indices, expert_ids, w_q, w_scales, out[, flags])
     all -> moe_layer_few(x, topk_ids, router_weights, w_gate_up, w_down, output_tokens, workspace, ...)
+
+and in floating point (``include/moe_experts_float.h``):
+
+    out -> moe_expert_matmul(a, expert_start_indices, expert_ids, w, out[, flags])                       bf16
+           moe_dispatch_f8(input_tokens, top_k, restore_token_order, out_q, out_scales)                  e4m3
+           moe_quantize_f8(x, out_q, out_scales[, row_count])
+           moe_expert_matmul_f8(a_q, a_scales, expert_start_indices, expert_ids, w_q, w_scales, out[, flags])
 """
 from __future__ import annotations
 
@@ -38,6 +45,7 @@ __all__ = [
     "alloc_indices", "alloc_dispatch", "alloc_dispatch_mxfp4", "index_workspace_error",
     "moe_dispatch_i8", "moe_quantize_i8", "moe_expert_matmul_i8", "moe_layer_few", "moe_layer_few_workspace_bytes",
     "MATMUL_SWIGLU", "MATMUL_MAX_DEPTH", "FEW_MAX_SLOTS", "alloc_quantized", "alloc_layer_few",
+    "moe_expert_matmul", "moe_dispatch_f8", "moe_quantize_f8", "moe_expert_matmul_f8", "F8_BLOCK", "alloc_quantized_f8",
 ]
 
 SENTINEL = 0xFFFFFFFF
@@ -359,4 +367,7 @@ def moe_combine_epilogue(y: torch.Tensor, router_weights: torch.Tensor, restore_
 from .experts import (  # noqa: E402  (needs the names above)
     FEW_MAX_SLOTS, MATMUL_MAX_DEPTH, MATMUL_SWIGLU, alloc_layer_few, alloc_quantized, moe_dispatch_i8,
     moe_expert_matmul_i8, moe_layer_few, moe_layer_few_workspace_bytes, moe_quantize_i8,
+)
+from .experts_float import (  # noqa: E402
+    F8_BLOCK, alloc_quantized_f8, moe_dispatch_f8, moe_expert_matmul, moe_expert_matmul_f8, moe_quantize_f8,
 )

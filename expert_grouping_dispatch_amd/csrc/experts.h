@@ -17,22 +17,32 @@ hipError_t launch_dispatch_i8(const uint16_t* x, int64_t n_rows, int hidden, int
 hipError_t launch_quantize_i8(const uint16_t* x, int64_t n_rows, int hidden,
                               const uint32_t* row_count, int8_t* q, float* scales, hipStream_t s);
 
-// The grouped int8 product.  `wide` rows of weights per expert: n_out, or
-// 2*n_out with swiglu.
+// The grouped products.  n_out rows of weights per expert, or 2*n_out with
+// swiglu; a and w in the type of the launcher, bf16 without scales.
 struct ExpertMatmul {
-  const int8_t* a;
+  const void* a;
   const float* a_scales;
   uint32_t a_rows;
   const uint32_t* starts;
   const int32_t* expert_ids;
   int n_experts;
-  const int8_t* w;
+  const void* w;
   const float* w_scales;
   int n_out;
   int depth;
   uint16_t* out;
 };
 hipError_t launch_expert_matmul_i8(const ExpertMatmul& p, bool swiglu, hipStream_t s);
+hipError_t launch_expert_matmul_bf16(const ExpertMatmul& p, bool swiglu, hipStream_t s);
+hipError_t launch_expert_matmul_f8(const ExpertMatmul& p, bool swiglu, hipStream_t s);
+
+constexpr int kBlock = 128;  // values of a row, and weight rows, that share an e4m3 scale
+
+hipError_t launch_dispatch_f8(const uint16_t* x, int64_t n_rows, int hidden, int top_k,
+                              const uint32_t* restore, uint8_t* q, float* scales, int64_t out_rows,
+                              hipStream_t s);
+hipError_t launch_quantize_f8(const uint16_t* x, int64_t n_rows, int hidden, const uint32_t* row_count,
+                              uint8_t* q, float* scales, hipStream_t s);
 
 // The whole layer for a few tokens; pad.count == nullptr masks nothing.
 template <typename IdT>
@@ -59,6 +69,7 @@ hipError_t launch_layer_few(const FewLayer<IdT>& p, hipStream_t s);
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));

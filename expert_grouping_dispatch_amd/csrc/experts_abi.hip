@@ -3,44 +3,12 @@
 // device memory.
 #include "moe_experts.h"
 
-#include <initializer_list>
-
-#include "entry.h"
+#include "entry_experts.h"
 #include "experts.h"
 
 namespace {
 
-using moe::aligned;
-using moe::check_device;
-using moe::launched;
-using moe::slots_ok;
-
-constexpr int64_t kMaxRows = 0xFFFFFFFEll;
-constexpr int32_t kMaxWidth = 1 << 20;
-constexpr int32_t kMaxFewWidth = 1 << 17;  // 4 bytes each of MOE_FEW_MAX_SLOTS rows stay below 2^31
-
-bool width_ok(int32_t n) { return n > 0 && n <= kMaxWidth && n % 16 == 0; }
-
-struct Span {
-  const void* at;
-  uint64_t bytes;
-};
-
-bool overlap(const Span& a, const Span& b) {
-  const uintptr_t p = reinterpret_cast<uintptr_t>(a.at), q = reinterpret_cast<uintptr_t>(b.at);
-  return a.at != nullptr && b.at != nullptr && a.bytes > 0 && b.bytes > 0 && p < q + b.bytes && q < p + a.bytes;
-}
-
-// Whether something written lies on something read or on something else written.
-bool clash(std::initializer_list<Span> reads, std::initializer_list<Span> writes) {
-  for (const Span* w = writes.begin(); w != writes.end(); ++w) {
-    for (const Span& r : reads)
-      if (overlap(r, *w)) return true;
-    for (const Span* v = writes.begin(); v != w; ++v)
-      if (overlap(*v, *w)) return true;
-  }
-  return false;
-}
+using namespace moe;
 
 template <typename IdT>
 int layer_few(const uint16_t* x, int64_t n_rows, int32_t hidden, int32_t top_k, const IdT* topk_ids,

@@ -22,6 +22,11 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_
                                            kNonTemporal ? 2 : 0);
 }
 
+// 64 lanes x 4 bytes.
+__device__ __forceinline__ void load_word_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t off, uint32_t at, float* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)(dst), 4, off, at, 0, 0);
+}
+
 constexpr int kWaitLoads = 0x0F70;     // s_waitcnt vmcnt(0)
 // s_waitcnt vmcnt(n), n <= 63
 constexpr int wait_all_but(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }

@@ -143,6 +143,56 @@ __device__ __forceinline__ void stream_products(const uint8_t* const (&w)[RT], c
   }
 }
 
+// The same for e4m3 operands with a scale for each 128 values of k: a step is
+// such a block, 32 values a lane and lane group, and its sums are multiplied
+// with both scales in fp32 before they are added.  w_scales[r][s] and
+// x_scales[g][s] are those of step s, for this lane's activation row.
+template <int RT, int NG, int U>
+__device__ __forceinline__ void stream_blocks(const uint8_t* const (&w)[RT], const uint8_t* const (&x)[NG],
+                                              const float* const (&w_scales)[RT], const float* const (&x_scales)[NG],
+                                              int begin, int end, int depth, f32x4 (&acc)[RT][NG]) {
+  const int group = __lane_id() / 16;
+  const u32x4 zero{0u, 0u, 0u, 0u};
+  struct Bytes {
+    u32x4 v[2];
+  };
+  for (int s = begin; s < end; s += U) {
+    Bytes wv[U][RT], xv[U][NG];
+    float sx[U][NG];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = (s + u) * kBlock + group * 32 + 16 * i;
+        const bool some = s + u < end && at < depth;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) wv[u][r].v[i] = some ? load_weight(w[r] + at) : zero;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) xv[u][g].v[i] = some ? *reinterpret_cast<const u32x4*>(x[g] + at) : zero;
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int g = 0; g < NG; ++g) sx[u][g] = x_scales[g][min(s + u, end - 1)];
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        if (s + u >= end) continue;  // a scale that is NaN would make NaN of the zeros
+        const float sw = w_scales[r][s + u];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const f32x4 part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              __builtin_bit_cast(i32x8, wv[u][r]), __builtin_bit_cast(i32x8, xv[u][g]), f32x4{}, 0, 0, 0, 0, 0, 0);
+          const float scale = sx[u][g] * sw;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[r][g][i] = __builtin_fmaf(part[i], scale, acc[r][g][i]);
+        }
+      }
+  }
+}
+
 // Steps [begin, end) of part p of n over a row of `depth` values.
 __device__ __forceinline__ void step_range(int depth, int p, int n, int& begin, int& end) {
   const int steps = (depth + kStreamStep - 1) / kStreamStep;

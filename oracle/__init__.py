@@ -23,3 +23,11 @@ from .experts_oracle import (  # noqa: F401
     quantize_i8,
     swiglu,
 )
+from .experts_float_oracle import (  # noqa: F401
+    block_weights,
+    dispatch_f8,
+    e4m3_codes,
+    e4m3_values,
+    products,
+    quantize_f8,
+)

@@ -1,0 +1,101 @@
+"""Plain CPU oracle of the experts' products in floating point.  TEST
+INFRASTRUCTURE ONLY: it shares no code with the HIP library.
+
+  * e4m3_values -- what the 256 codes stand for: sign, four exponent bits with
+    bias 7, three mantissa bits, subnormals, no infinities, NaN at 0x7F and 0xFF.
+  * e4m3_codes -- the code next to each value, ties to the even code, values
+    above 448 that round to it saturate; the sign of zeros is kept.
+  * quantize_f8 -- for each 128 values of a row (the last block may be shorter)
+    a = max(max |x|, 2^-116), scale = fl32(a/448), inv = fl32(448/a),
+    q = e4m3(fl32(x*inv)).  Quotients and products are formed in 64 bits and
+    rounded once.  A block with an infinity or a NaN has scale NaN; its payload
+    is unspecified, zeros here.
+  * dispatch_f8 -- row p of the output is the quantised row of token
+    token_expert_order[p] // top_k.
+  * block_weights -- weights [halves * n, k] with the scales [halves * ceil(n/128),
+    ceil(k/128)] of their blocks, each half's counted from its first row, as values.
+  * products -- v = a w^T in 64 bits and a bound on how far the kernels' fp32
+    sums may be from it (see there).
+"""
+from __future__ import annotations
+
+import numpy as np
+
+from .experts_oracle import _sigmoid, swiglu
+from .moe_oracle import bf16_bits_to_f32
+
+F32 = np.float32
+BLOCK = 128
+
+
+def e4m3_values() -> np.ndarray:
+    code = np.arange(256)
+    exponent, mantissa = code >> 3 & 15, code & 7
+    v = np.where(exponent == 0, mantissa * 2.0 ** -9, (8 + mantissa) * np.exp2(exponent - 10.0))
+    v[(code & 127) == 127] = np.nan
+    return np.where(code & 128, -v, v)
+
+
+def e4m3_codes(v: np.ndarray) -> np.ndarray:
+    """v float64, |v| < 464."""
+    table = e4m3_values()[:127]  # 0 .. 448, ascending
+    m = np.minimum(np.abs(v), 448.0)
+    low = np.clip(np.searchsorted(table, m, side="right") - 1, 0, 125)
+    below, above = m - table[low], table[low + 1] - m
+    up = (above < below) | ((above == below) & (low % 2 == 1))
+    return ((low + up) | np.where(np.signbit(v), 128, 0)).astype(np.uint8)
+
+
+def quantize_f8(x_bits: np.ndarray):
+    n, h = x_bits.shape
+    blocks = -(-h // BLOCK)
+    x = np.zeros((n, blocks * BLOCK))
+    x[:, :h] = bf16_bits_to_f32(x_bits)
+    x = x.reshape(n, blocks, BLOCK)
+    bad = ~np.isfinite(x).all(axis=2)
+    x[bad] = 0.0
+    a = np.maximum(np.abs(x).max(axis=2), 2.0 ** -116)
+    scale = (a / 448.0).astype(F32)
+    inv = (448.0 / a).astype(F32).astype(np.float64)
+    q = e4m3_codes((x * inv[:, :, None]).astype(F32).astype(np.float64))
+    scale[bad] = np.nan
+    return q.reshape(n, -1)[:, :h], scale
+
+
+def dispatch_f8(x_bits: np.ndarray, token_expert_order: np.ndarray, top_k: int, n_routed: int):
+    q, s = quantize_f8(x_bits)
+    rows = token_expert_order[:n_routed].astype(np.int64) // top_k
+    return q[rows], s[rows]
+
+
+def block_weights(values: np.ndarray, scales: np.ndarray, halves: int = 1) -> np.ndarray:
+    wide, k = values.shape
+    n = wide // halves
+    per = scales.astype(np.float64).reshape(halves, -(-n // BLOCK), -1)
+    per = per[:, np.arange(n) // BLOCK][:, :, np.arange(k) // BLOCK]
+    return values * per.reshape(wide, k)
+
+
+def products(a: np.ndarray, w: np.ndarray, swiglu_halves: bool):
+    """(out, bound), both float64 [rows, n], for operands given as the values they
+    stand for, scales among them.
+
+    The bound counts, in units u = 2^-24 (half a step of fp32, relative):
+      * a sum of k products in fp32, in any order: (k + 4) u times the sum of the
+        magnitudes, plus 2 u for each block of 128: its scale's rounding and the
+        addition of its sum;
+      * silu's slope is below 1.1; its evaluation and the product with up:
+        (|g| + 8) u relative;
+      * the output: 2^-8 relative (half a step of bf16), 2^-133 below its normal numbers.
+    """
+    u24, half = 2.0 ** -24, 2.0 ** -8
+    k = a.shape[1]
+    v = a @ w.T
+    dv = (k + 4 + 2 * -(-k // BLOCK)) * u24 * (np.abs(a) @ np.abs(w).T)
+    if swiglu_halves:
+        n = w.shape[0] // 2
+        g, up, dg, du = v[:, :n], v[:, n:], dv[:, :n], dv[:, n:]
+        v = swiglu(g, up)
+        dv = 1.1 * dg * (np.abs(up) + du) + np.abs(g * _sigmoid(g)) * du
+        dv = dv + (np.abs(v) + dv) * (np.abs(g) + 8) * u24
+    return v, dv + half * (np.abs(v) + dv) + 2.0 ** -133
