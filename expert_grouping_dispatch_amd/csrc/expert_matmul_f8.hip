@@ -27,13 +27,23 @@ __device__ __forceinline__ f32x16 mac_f8(const u32x4 (&w)[2], const u32x4 (&a)[2
 
 }  // namespace
 
-// Tiles as in k_matmul_tile, with eight waves: a wave's 128 by 64 sums take 128
-// registers, the sums of the block that is being formed 32 more.
+// Tiles as in k_matmul_tile, with eight waves, 2 by 4, so that each wave's sums,
+// 128 rows by 64 weight rows, take 128 registers.  A step is a block of k: 64 KB
+// of operands and the scales of 256 rows and two blocks of weight rows, in one of
+// two buffers.
+//
+// A step goes through the wave's four fragments of rows: eight products for each,
+// whose sums the vector unit then adds while the matrix unit works for the other
+// wave of the SIMD.  Registers of a fragment are filled again as soon as the
+// products that read them have begun.  Before the last products of a step its
+// buffer is in registers: there is the step's barrier, after which the next
+// step's first fragments are read and the buffer is filled for the step after
+// that.  The stream of steps runs on across tiles.
 template <bool kSwiglu>
 __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p) {
-  __shared__ __align__(16) uint8_t s_a0[kTile * kStepBytes], s_a1[kTile * kStepBytes];
-  __shared__ __align__(16) uint8_t s_w0[kTile * kStepBytes], s_w1[kTile * kStepBytes];
-  __shared__ float s_sa0[kTile], s_sa1[kTile], s_sw0[kWave], s_sw1[kWave];
+  constexpr uint32_t kHalf = kTile * kStepBytes, kBuffer = 2 * kHalf;  // activations, then weights
+  __shared__ __align__(16) uint8_t s_buf[2 * kBuffer];
+  __shared__ float s_scale[2][kF8Threads];  // of the rows, of the two blocks of weight rows, and space that is not read
   __shared__ TileList<kF8Threads> s_tiles;
   const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
   constexpr int kChannels = kSwiglu ? kTile / 2 : kTile;
@@ -49,65 +59,81 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
 
   const int wide = kSwiglu ? 2 * p.n_out : p.n_out;
   const uint32_t row = uint32_t(p.depth);
-  const int steps = (p.depth + kBlock - 1) / kBlock, half = (p.n_out + kBlock - 1) / kBlock;
-  const bool ragged = p.depth % kBlock != 0;
+  const int blocks = (p.depth + kBlock - 1) / kBlock, half = (p.n_out + kBlock - 1) / kBlock;
+  // Two steps at least, so that the steps fetched ahead belong to this tile or to the next one: of a single block
+  // the second step is all past the row's end.
+  const int steps = max(blocks, 2);
+  const bool ragged = steps * kBlock > p.depth;
   const uint64_t w_bytes = uint64_t(p.n_experts) * wide * row;
+  // The lane's number where the compiler cannot form an address of it ahead of the
+  // loop and keep it in a register: the sums leave none for that.
+  auto lane_now = [&] {
+    uint32_t l = lane;
+    asm volatile("" : "+v"(l));
+    return l;
+  };
+  // The piece this lane fills, in an instruction of even and of odd number.
   const int piece[2] = {(lane % 8) ^ (lane / 16), (lane % 8) ^ (4 + lane / 16)};
   const uint32_t lane_off[2] = {uint32_t(lane / 8) * row + piece[0] * 16, uint32_t(lane / 8) * row + piece[1] * 16};
   // This wave fills LDS rows [32*wave, +32) of both operands; waves 0 to 3 the
-  // scales of 64 rows each, wave 4 those of the two blocks of weight rows.
-  __amdgpu_buffer_rsrc_t a_from, w_from, s_from;
-  uint32_t s_off = 0;
+  // scales of 64 rows each, wave 4 those of the two blocks of weight rows (past the
+  // last one what is read is not used), the others the same for nothing.
+  struct From {
+    u32x4 a, w, s;
+  };
   auto aim = [&](const TilePlace& t) __attribute__((always_inline)) {
+    From f;
     const int rows = max(t.n_rows - 32 * wave, 0);
     const uint64_t a0 = (uint64_t(t.row0) + (rows > 0 ? 32 * wave : 0)) * row;
     const int first_w = t.c0 + (kSwiglu ? 32 * (wave / 2) + (wave % 2) * p.n_out : 32 * wave);
     const uint64_t w0 = (uint64_t(t.e) * wide + first_w) * row;
-    a_from = buffer_of(static_cast<const uint8_t*>(p.a) + a0, uint64_t(rows) * row);
-    w_from = buffer_of(static_cast<const uint8_t*>(p.w) + min(w0, w_bytes), w0 < w_bytes ? w_bytes - w0 : 0);
+    f.a = buffer_words(static_cast<const uint8_t*>(p.a) + a0, uint64_t(rows) * row);
+    f.w = buffer_words(static_cast<const uint8_t*>(p.w) + min(w0, w_bytes), w0 < w_bytes ? w_bytes - w0 : 0);
     if (wave < 4) {
-      s_from = buffer_of(reinterpret_cast<const uint8_t*>(p.a_scales + uint64_t(t.row0) * steps),
-                         uint64_t(t.n_rows) * steps * 4);
-      s_off = uint32_t(tid) * steps * 4;
+      f.s = buffer_words(reinterpret_cast<const uint8_t*>(p.a_scales + uint64_t(t.row0) * blocks),
+                         uint64_t(t.n_rows) * blocks * 4);
     } else {
-      const uint64_t blocks = uint64_t(kSwiglu ? 2 : 1) * half * steps;
-      s_from = buffer_of(reinterpret_cast<const uint8_t*>(p.w_scales + t.e * blocks), blocks * 4);
-      const int b = t.c0 / kBlock;
-      s_off = uint32_t(lane == 0 ? b : kSwiglu ? half + b : min(b + 1, half - 1)) * steps * 4;
+      const uint64_t each = uint64_t(kSwiglu ? 2 : 1) * half, b = t.e * each + t.c0 / kBlock;
+      f.s = buffer_words(reinterpret_cast<const uint8_t*>(p.w_scales + b * blocks),
+                         (p.n_experts * each - b) * blocks * 4);
     }
+    return f;
   };
-  TilePlace now, ahead;
-  Walk at_now{first, 0}, at_ahead{first, 0};
-  if (!advance(at_now, now)) return;
-  advance(at_ahead, ahead);
-  aim(ahead);
-  int fs = 0;  // the next step of `ahead` to fetch
+  const uint32_t s_off = wave < 4 ? uint32_t(tid) * blocks * 4 : lane == 0 ? 0u : uint32_t(kSwiglu ? half : 1) * blocks * 4;
+  // The tile being formed and the one after it, whose first two steps are fetched
+  // during the last two of this one.  Past the last tile its steps are fetched
+  // again, for nothing.
+  TilePlace now, next;
+  Walk at{first, 0};
+  if (!advance(at, now)) return;
+  From from = aim(now), after;
+  uint32_t cur = 0;  // the buffer being formed, 0 or kBuffer
+  const uint32_t buf0 = lds_offset(s_buf), scale0 = lds_offset(s_scale);
+  // The XCDs begin at different steps, so that they are not all at the same memory channels.
   const int turn = ragged ? 0 : int(xcd * uint32_t(steps) / 8);
-  auto fetch = [&](uint8_t* to_a, uint8_t* to_w, float* to_sa, float* to_sw) __attribute__((always_inline)) {
-    const int s = fs + turn < steps ? fs + turn : fs + turn - steps;
+  auto fetch = [&](const From& f, int nth, uint32_t to) __attribute__((always_inline)) {
+    const int s = nth + turn < steps ? nth + turn : nth + turn - steps;
+    const uint32_t rows_at = buf0 + to + 32 * wave * kStepBytes;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t at = uint32_t(s) * kStepBytes + uint32_t(8 * i) * row;
-      load_to_lds(a_from, lane_off[i % 2], at, to_a + (32 * wave + 8 * i) * kStepBytes);
-      load_to_lds(w_from, lane_off[i % 2], at, to_w + (32 * wave + 8 * i) * kStepBytes);
+      fill_lds(f.a, lane_off[i % 2], at, rows_at + 8 * i * kStepBytes);
+      fill_lds(f.w, lane_off[i % 2], at, rows_at + kHalf + 8 * i * kStepBytes);
     }
-    if (wave <= 4) load_word_to_lds(s_from, s_off, uint32_t(s) * 4, wave < 4 ? to_sa + 64 * wave : to_sw);
-    if (++fs == steps) {
-      fs = 0;
-      if (advance(at_ahead, ahead)) aim(ahead);
-      __builtin_amdgcn_s_waitcnt(kWaitLdsScalar);
-    }
+    fill_lds_words(f.s, s_off, uint32_t(min(s, blocks - 1)) * 4, scale0 + (to ? sizeof(s_scale[0]) : 0) + 256 * wave);
   };
-  // Pieces past the row's end become zeros in both operands: what was read there instead may be a NaN.
-  auto arrived = [&](int s, uint8_t* a, uint8_t* w) __attribute__((always_inline)) {
+  // Waits until step s, in the buffer at `in`, is there for all waves.  Pieces past
+  // the row's end become zeros in both operands: what was read there instead may be a NaN.
+  auto arrived = [&](int s, uint32_t in) __attribute__((always_inline)) {
     __builtin_amdgcn_s_waitcnt(kWaitLoads);
     asm volatile("" ::: "memory");
-    if (ragged && s == steps - 1) {
+    if ((s + 1) * kBlock > p.depth) {
+      const uint32_t l = lane_now();
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (s * kStepBytes + piece[i % 2] * 16 >= p.depth) {
-          *reinterpret_cast<u32x4*>(w + (32 * wave + 8 * i) * kStepBytes + lane * 16) = u32x4{0u, 0u, 0u, 0u};
-          *reinterpret_cast<u32x4*>(a + (32 * wave + 8 * i) * kStepBytes + lane * 16) = u32x4{0u, 0u, 0u, 0u};
+        if (s * kStepBytes + int((l % 8) ^ (i % 2 * 4 + l / 16)) * 16 >= p.depth) {
+          uint8_t* at = s_buf + in + (32 * wave + 8 * i) * kStepBytes + l * 16;
+          *reinterpret_cast<u32x4*>(at) = *reinterpret_cast<u32x4*>(at + kHalf) = u32x4{0u, 0u, 0u, 0u};
         }
     }
     __builtin_amdgcn_s_waitcnt(kWaitLdsScalar);
@@ -117,9 +143,35 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
   };
 
   const int wr = wave / 4, wc = wave % 4;
+  // Where this lane's pieces of fragment 0 lie.
   const uint32_t lane_at = (lane % 32) * kStepBytes + ((lane / 32) ^ (lane / 2 % 8)) * 16;
-  fetch(s_a0, s_w0, s_sa0, s_sw0);
-  bool odd = false;  // whether the tile's first step is in the second buffer
+  u32x4 fw[2][2][2], fa[2][2];  // fragment, half of the block, piece
+  auto read_w = [&](int h) __attribute__((always_inline)) {
+    uint32_t at = lane_at + cur + kHalf + 64 * wc * kStepBytes;
+    asm volatile("" : "+v"(at));
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        fw[f][h][j] = *reinterpret_cast<const u32x4*>(s_buf + (at ^ ((2 * h + j) * 32)) + 32 * f * kStepBytes);
+  };
+  auto read_a = [&](int wave_row, int g, int h) __attribute__((always_inline)) {
+    uint32_t at = lane_at + cur + wave_row * kStepBytes;
+    asm volatile("" : "+v"(at));
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      fa[h][j] = *reinterpret_cast<const u32x4*>(s_buf + (at ^ ((2 * h + j) * 32)) + 32 * g * kStepBytes);
+  };
+  auto wave_row = [&](const TilePlace& t) { return t.n_rows > kTile / 2 ? 128 * wr : 64 * wr; };
+
+  fetch(from, 0, 0);
+  fetch(from, 1, kBuffer);
+  arrived(0, 0);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    read_w(h);
+    read_a(wave_row(now), 0, h);
+  }
 
   // A tile of up to 64*G rows, 32*G for each wave.
   auto form = [&](auto frags) __attribute__((always_inline)) {
@@ -129,60 +181,45 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
     for (int f = 0; f < 2; ++f)
 #pragma unroll
       for (int g = 0; g < G; ++g) acc[f][g] = f32x16{};
-    auto step = [&](int s, uint8_t* a, uint8_t* w, const float* sa, const float* sw, uint8_t* na, uint8_t* nw,
-                    float* nsa, float* nsw) __attribute__((always_inline)) {
-      arrived(s, a, w);
-      fetch(na, nw, nsa, nsw);
-      // Where this lane's pieces of fragment 0 lie; opaque, or the address of every fragment in every buffer is
-      // kept in a register of its own.
-      uint32_t at_a = lane_at + 32 * G * wr * kStepBytes, at_w = lane_at + 64 * wc * kStepBytes;
-      asm volatile("" : "+v"(at_a), "+v"(at_w));
-      auto piece_of = [&](const uint8_t* rows, uint32_t at, int f, int kk) __attribute__((always_inline)) {
-        return *reinterpret_cast<const u32x4*>(rows + (at ^ (kk * 32)) + 32 * f * kStepBytes);
-      };
-      u32x4 fw[2][2][2];
-#pragma unroll
-      for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) fw[f][kk / 2][kk % 2] = piece_of(w, at_w, f, kk);
-      float by[2];
-#pragma unroll
-      for (int f = 0; f < 2; ++f) by[f] = sw[kSwiglu ? f : wc / 2];
-      u32x4 fa[2][2];
-      auto read = [&](int g, int half) __attribute__((always_inline)) {
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) fa[half][kk] = piece_of(a, at_a, g, 2 * half + kk);
-      };
-      read(0, 0);
-      read(0, 1);
+    for (int s = 0; s < steps; ++s) {
+      const float* scale = s_scale[cur ? 1 : 0];
+      const float by0 = scale[kTile + (kSwiglu ? 0 : wc / 2)], by1 = scale[kTile + (kSwiglu ? 1 : wc / 2)];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float sr = sa[32 * G * wr + 32 * g + lane % 32];
+        const float sr = scale[32 * G * wr + 32 * g + (lane_now() & 31)];
         f32x16 part[2];
         __builtin_amdgcn_sched_barrier(0);
         part[0] = mac_f8(fw[0][0], fa[0], f32x16{});
         part[1] = mac_f8(fw[1][0], fa[0], f32x16{});
         __builtin_amdgcn_sched_barrier(0);
-        if (g + 1 < G) read(g + 1, 0);
+        if (g + 1 < G) {
+          read_a(32 * G * wr, g + 1, 0);
+        } else {
+          arrived(s + 1 < steps ? s + 1 : 0, cur ^ kBuffer);
+          const bool same = s + 2 < steps;
+          fetch(From{same ? from.a : after.a, same ? from.w : after.w, same ? from.s : after.s},
+                same ? s + 2 : s + 2 - steps, cur);
+          cur ^= kBuffer;
+          read_w(0);
+          read_a(s + 1 < steps ? 32 * G * wr : wave_row(next), 0, 0);
+        }
         __builtin_amdgcn_sched_barrier(0);
         part[0] = mac_f8(fw[0][1], fa[1], part[0]);
         part[1] = mac_f8(fw[1][1], fa[1], part[1]);
         __builtin_amdgcn_sched_barrier(0);
-        if (g + 1 < G) read(g + 1, 1);
+        if (g + 1 < G) {
+          read_a(32 * G * wr, g + 1, 1);
+        } else {
+          read_w(1);
+          read_a(s + 1 < steps ? 32 * G * wr : wave_row(next), 0, 1);
+        }
         __builtin_amdgcn_sched_barrier(0);
-        add_scaled(acc[0][g], part[0], sr * by[0]);
-        add_scaled(acc[1][g], part[1], sr * by[1]);
+        add_scaled(acc[0][g], part[0], sr * by0);
+        add_scaled(acc[1][g], part[1], sr * by1);
+        asm volatile("" : "+v"(acc[0][g]), "+v"(acc[1][g]));  // here, or the additions are put off while their operands pile up
         __builtin_amdgcn_sched_barrier(0);
       }
-    };
-    int s = 0;
-    if (odd) step(s++, s_a1, s_w1, s_sa1, s_sw1, s_a0, s_w0, s_sa0, s_sw0);
-    for (; s + 1 < steps; s += 2) {
-      step(s, s_a0, s_w0, s_sa0, s_sw0, s_a1, s_w1, s_sa1, s_sw1);
-      step(s + 1, s_a1, s_w1, s_sa1, s_sw1, s_a0, s_w0, s_sa0, s_sw0);
     }
-    odd = s < steps;
-    if (odd) step(s, s_a0, s_w0, s_sa0, s_sw0, s_a1, s_w1, s_sa1, s_sw1);
 
     // Stores go through a buffer of the tile's rows: what a lane has for a row
     // or channel past the end gets an offset past the buffer and is dropped.
@@ -208,21 +245,28 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
         }
         // Lanes l and l+32 hold the two halves of each eight channels of one
         // row: the lower one takes all of the even q, the upper of the odd.
-        const int r = 32 * G * wr + 32 * g + lane % 32;
-        const uint32_t at = uint32_t(r) * row_bytes + uint32_t(c0 + 8 * (lane / 32)) * 2;
+        const uint32_t l = lane_now();
+        const int r = 32 * G * wr + 32 * g + int(l % 32);
+        const uint32_t at = uint32_t(r) * row_bytes + uint32_t(c0 + 8 * (l / 32)) * 2;
 #pragma unroll
         for (int q = 0; q < 4; q += 2) {
           const u32x2 x = permlane32_swap(v[q].x, v[q + 1].x), y = permlane32_swap(v[q].y, v[q + 1].y);
           const bool some = r < now.n_rows && c0 + 8 * q < p.n_out;
           __builtin_amdgcn_raw_buffer_store_b128(u32x4{x.x, y.x, x.y, y.y}, out, some ? at + 16 * q : 0xFFFFFFF0u, 0, 0);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
-  do {
+  for (bool more = true; more;) {
+    more = advance(at, next);
+    if (!more) next = now;
+    after = aim(next);
     if (now.n_rows > kTile / 2) form(std::integral_constant<int, 4>{});
     else form(std::integral_constant<int, 2>{});
-  } while (advance(at_now, now));
+    now = next;
+    from = after;
+  }
   __builtin_amdgcn_s_waitcnt(kWaitLoads);  // nothing may still be on its way to LDS
 }
 

@@ -22,12 +22,34 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_
                                            kNonTemporal ? 2 : 0);
 }
 
+constexpr int kWaitLoads = 0x0F70;     // s_waitcnt vmcnt(0)
+// The same fills where the compiler does not see that they write LDS, and so puts
+// no wait for them before reads of it: the kernel has to wait itself, for its own
+// loads, before the barrier after which their LDS is read.  They have no output
+// register.  A buffer as four scalars; `dst` is an offset into LDS.  M0, which
+// nothing else in such a kernel uses, is set each time.
+__device__ __forceinline__ u32x4 buffer_words(const uint8_t* base, uint64_t bytes) {
+  const uint64_t at = reinterpret_cast<uint64_t>(base);
+  const uint32_t size = bytes < (uint64_t(1) << 31) ? uint32_t(bytes) : 0x7FFFFFF0u;
+  return u32x4{uniform(uint32_t(at)), uniform(uint32_t(at >> 32) & 0xFFFFu), uniform(size), 0x00027000u};
+}
+__device__ __forceinline__ void fill_lds(const u32x4& from, uint32_t off, uint32_t at, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(dst), "v"(off), "s"(from), "s"(at)
+               : "memory");
+}
 // 64 lanes x 4 bytes.
-__device__ __forceinline__ void load_word_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t off, uint32_t at, float* dst) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)(dst), 4, off, at, 0, 0);
+__device__ __forceinline__ void fill_lds_words(const u32x4& from, uint32_t off, uint32_t at, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               :
+               : "s"(dst), "v"(off), "s"(from), "s"(at)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
 }
 
-constexpr int kWaitLoads = 0x0F70;     // s_waitcnt vmcnt(0)
 // s_waitcnt vmcnt(n), n <= 63
 constexpr int wait_all_but(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
 constexpr int kWaitLdsScalar = 0xC07F;  // s_waitcnt lgkmcnt(0)
