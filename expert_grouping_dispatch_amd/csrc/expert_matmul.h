@@ -44,6 +44,10 @@ constexpr int kStripFrags = 2;  // of 32 weight rows, for each wave
 // 2048 -> 7168) 83 and 99.
 constexpr uint32_t kStripsMin = 256;
 constexpr int kMaxActive = 1024;
+// Rows of tiles that are taken column by column together: 491520 rows on 253
+// experts in e4m3, 2048 -> 7168, 8.18 ms with 8, 8.22 with 6, 8.33 with 4, 8.47
+// with all of an expert's (int8 and 1750 rows an expert do not depend on it).
+constexpr uint32_t kRowGroup = 8;
 
 // Rows [lo, hi) of active expert j, inside the buffer whatever the starts hold.
 __device__ __forceinline__ void group_rows(const uint32_t* starts, int j, uint32_t a_rows, uint32_t& lo,
@@ -420,9 +424,13 @@ struct TileList {
       const uint32_t lo = uniform(row[at.j]), hi = max(min(uniform(row[at.j + 1]), p.a_rows), lo);
       const uint32_t row_tiles = (hi - lo + kTile - 1) / kTile;
       if (row_tiles == 0) continue;
-      const uint32_t in = at.tile - uniform(first[at.j]);
-      t.row0 = lo + (in % row_tiles) * kTile;
-      t.c0 = int(in / row_tiles) * channels;
+      // Rows by kRowGroup, within them columns, within a column its rows: the tiles that an XCD's workgroups take at
+      // once then share both operands in its L2.
+      const uint32_t in = at.tile - uniform(first[at.j]), col_tiles = (uint32_t(p.n_out) + channels - 1) / channels;
+      const uint32_t group = in / (kRowGroup * col_tiles), rest = in % (kRowGroup * col_tiles);
+      const uint32_t rows = min(row_tiles - group * kRowGroup, kRowGroup);
+      t.row0 = lo + (group * kRowGroup + rest % rows) * kTile;
+      t.c0 = int(rest / rows) * channels;
       t.e = uniform(expert[at.j]);
       if (t.e < 0 || t.e >= p.n_experts || t.row0 >= hi || t.c0 >= p.n_out) continue;
       t.n_rows = int(min(hi - t.row0, uint32_t(kTile)));

@@ -25,6 +25,15 @@ __device__ __forceinline__ f32x16 mac_f8(const u32x4 (&w)[2], const u32x4 (&a)[2
                                                          0, 0);
 }
 
+__device__ __forceinline__ f32x4 mac16_f8(const u32x4 (&w)[2], const u32x4 (&a)[2]) {
+  struct Both {
+    u32x4 v[2];
+  };
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, (Both{w[0], w[1]})),
+                                                          __builtin_bit_cast(i32x8, (Both{a[0], a[1]})), f32x4{}, 0, 0,
+                                                          0, 0, 0, 0);
+}
+
 }  // namespace
 
 // Tiles as in k_matmul_tile, with eight waves, 2 by 4, so that each wave's sums,
@@ -43,7 +52,7 @@ template <bool kSwiglu>
 __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p) {
   constexpr uint32_t kHalf = kTile * kStepBytes, kBuffer = 2 * kHalf;  // activations, then weights
   __shared__ __align__(16) uint8_t s_buf[2 * kBuffer];
-  __shared__ float s_scale[2][kF8Threads];  // of the rows, of the two blocks of weight rows, and space that is not read
+  __shared__ __align__(16) f32x4 s_scale[2][kTile + kWave];  // four steps' of the rows, then of the two blocks of weight rows
   __shared__ TileList<kF8Threads> s_tiles;
   const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
   constexpr int kChannels = kSwiglu ? kTile / 2 : kTile;
@@ -77,7 +86,8 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
   const uint32_t lane_off[2] = {uint32_t(lane / 8) * row + piece[0] * 16, uint32_t(lane / 8) * row + piece[1] * 16};
   // This wave fills LDS rows [32*wave, +32) of both operands; waves 0 to 3 the
   // scales of 64 rows each, wave 4 those of the two blocks of weight rows (past the
-  // last one what is read is not used), the others the same for nothing.
+  // last one what is read is not used), for four steps at a time: one by one they
+  // cost as many cache lines as the operands' bytes do (217 us of 1963).
   struct From {
     u32x4 a, w, s;
   };
@@ -110,17 +120,24 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
   uint32_t cur = 0;  // the buffer being formed, 0 or kBuffer
   const uint32_t buf0 = lds_offset(s_buf), scale0 = lds_offset(s_scale);
   // The XCDs begin at different steps, so that they are not all at the same memory channels.
-  const int turn = ragged ? 0 : int(xcd * uint32_t(steps) / 8);
-  auto fetch = [&](const From& f, int nth, uint32_t to) __attribute__((always_inline)) {
+  const int turn = ragged ? 0 : int(xcd * uint32_t(steps) / 8) & ~3;
+  uint32_t scales_to = 0, scales_cur = 1;  // of s_scale, where the next group of scales goes, and where the last one read is
+  // A quarter of this wave's part of a step.
+  auto fetch = [&](const From& f, int nth, uint32_t to, int i) __attribute__((always_inline)) {
     const int s = nth + turn < steps ? nth + turn : nth + turn - steps;
-    const uint32_t rows_at = buf0 + to + 32 * wave * kStepBytes;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t at = uint32_t(s) * kStepBytes + uint32_t(8 * i) * row;
-      fill_lds(f.a, lane_off[i % 2], at, rows_at + 8 * i * kStepBytes);
-      fill_lds(f.w, lane_off[i % 2], at, rows_at + kHalf + 8 * i * kStepBytes);
+    const uint32_t rows_at = buf0 + to + (32 * wave + 8 * i) * kStepBytes;
+    const uint32_t at = uint32_t(s) * kStepBytes + uint32_t(8 * i) * row;
+    fill_lds(f.a, lane_off[i % 2], at, rows_at);
+    fill_lds(f.w, lane_off[i % 2], at, rows_at + kHalf);
+    if (i == 0 && s % 4 == 0) {
+      if (wave <= 4) fill_lds(f.s, s_off, uint32_t(s) * 4, scale0 + scales_to * sizeof(s_scale[0]) + 1024 * wave);
+      scales_to ^= 1;
     }
-    fill_lds_words(f.s, s_off, uint32_t(min(s, blocks - 1)) * 4, scale0 + (to ? sizeof(s_scale[0]) : 0) + 256 * wave);
+  };
+  // The same of step s of the tile being formed or, past its end, of the next one.
+  auto fetch_ahead = [&](int s, uint32_t to, int i) __attribute__((always_inline)) {
+    const bool same = s < steps;
+    fetch(From{same ? from.a : after.a, same ? from.w : after.w, same ? from.s : after.s}, same ? s : s - steps, to, i);
   };
   // Waits until step s, in the buffer at `in`, is there for all waves.  Pieces past
   // the row's end become zeros in both operands: what was read there instead may be a NaN.
@@ -142,128 +159,154 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
     asm volatile("" ::: "memory");
   };
 
+  // Fragments of 16 rows: this lane has row lane%16, pieces lane/16 and 4 + lane/16 of its eight.
   const int wr = wave / 4, wc = wave % 4;
-  // Where this lane's pieces of fragment 0 lie.
-  const uint32_t lane_at = (lane % 32) * kStepBytes + ((lane / 32) ^ (lane / 2 % 8)) * 16;
-  u32x4 fw[2][2][2], fa[2][2];  // fragment, half of the block, piece
-  auto read_w = [&](int h) __attribute__((always_inline)) {
+  const uint32_t lane_at = (lane % 16) * kStepBytes + ((lane / 16) ^ (lane / 2 % 8)) * 16;
+  u32x4 fw[4][2], fa[2][2];
+  auto read_w = [&](int f) __attribute__((always_inline)) {
     uint32_t at = lane_at + cur + kHalf + 64 * wc * kStepBytes;
     asm volatile("" : "+v"(at));
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        fw[f][h][j] = *reinterpret_cast<const u32x4*>(s_buf + (at ^ ((2 * h + j) * 32)) + 32 * f * kStepBytes);
+    for (int j = 0; j < 2; ++j)
+      fw[f][j] = *reinterpret_cast<const u32x4*>(s_buf + (at ^ (j * 64)) + 16 * f * kStepBytes);
   };
-  auto read_a = [&](int wave_row, int g, int h) __attribute__((always_inline)) {
+  auto read_a = [&](int wave_row, int g) __attribute__((always_inline)) {
     uint32_t at = lane_at + cur + wave_row * kStepBytes;
     asm volatile("" : "+v"(at));
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      fa[h][j] = *reinterpret_cast<const u32x4*>(s_buf + (at ^ ((2 * h + j) * 32)) + 32 * g * kStepBytes);
+      fa[g % 2][j] = *reinterpret_cast<const u32x4*>(s_buf + (at ^ (j * 64)) + 16 * g * kStepBytes);
   };
   auto wave_row = [&](const TilePlace& t) { return t.n_rows > kTile / 2 ? 128 * wr : 64 * wr; };
 
-  fetch(from, 0, 0);
-  fetch(from, 1, kBuffer);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) fetch(from, 0, 0, i);
   arrived(0, 0);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    read_w(h);
-    read_a(wave_row(now), 0, h);
-  }
+  for (int i = 0; i < 4; ++i) fetch(from, 1, kBuffer, i);
+#pragma unroll
+  for (int f = 0; f < 4; ++f) read_w(f);
+  read_a(wave_row(now), 0);
 
-  // A tile of up to 64*G rows, 32*G for each wave.
+  // A tile of up to 32*G rows, 16*G for each wave.
   auto form = [&](auto frags) __attribute__((always_inline)) {
     constexpr int G = decltype(frags)::value;
-    f32x16 acc[2][G];
+    f32x4 acc[4][G], part[2][4];
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+    for (int f = 0; f < 4; ++f) {
 #pragma unroll
-      for (int g = 0; g < G; ++g) acc[f][g] = f32x16{};
+      for (int g = 0; g < G; ++g) acc[f][g] = f32x4{};
+      part[1][f] = f32x4{};
+    }
+    float by[2] = {0.0f, 0.0f};  // the scales of the sums in part[1], the step's last fragment
     for (int s = 0; s < steps; ++s) {
-      const float* scale = s_scale[cur ? 1 : 0];
-      const float by0 = scale[kTile + (kSwiglu ? 0 : wc / 2)], by1 = scale[kTile + (kSwiglu ? 1 : wc / 2)];
+      const int block = min(s + turn < steps ? s + turn : s + turn - steps, blocks - 1);
+      if (block % 4 == 0 && s < blocks) scales_cur ^= 1;
+      const float* scale = reinterpret_cast<const float*>(s_scale[scales_cur]) + block % 4;
+      const float bw[2] = {scale[4 * (kTile + (kSwiglu ? 0 : wc / 2))], scale[4 * (kTile + (kSwiglu ? 1 : wc / 2))]};
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float sr = scale[32 * G * wr + 32 * g + (lane_now() & 31)];
-        f32x16 part[2];
-        __builtin_amdgcn_sched_barrier(0);
-        part[0] = mac_f8(fw[0][0], fa[0], f32x16{});
-        part[1] = mac_f8(fw[1][0], fa[0], f32x16{});
+        const float sr = scale[4 * (16 * G * wr + 16 * g + (lane_now() & 15))];
+        const int next_row = s + 1 < steps ? 16 * G * wr : wave_row(next);
         __builtin_amdgcn_sched_barrier(0);
         if (g + 1 < G) {
-          read_a(32 * G * wr, g + 1, 0);
+          read_a(16 * G * wr, g + 1);
         } else {
           arrived(s + 1 < steps ? s + 1 : 0, cur ^ kBuffer);
-          const bool same = s + 2 < steps;
-          fetch(From{same ? from.a : after.a, same ? from.w : after.w, same ? from.s : after.s},
-                same ? s + 2 : s + 2 - steps, cur);
           cur ^= kBuffer;
-          read_w(0);
-          read_a(s + 1 < steps ? 32 * G * wr : wave_row(next), 0, 0);
+          read_a(next_row, 0);
+        }
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          __builtin_amdgcn_sched_barrier(0);
+          part[g % 2][f] = mac16_f8(fw[f], fa[g % 2]);
+          if (g + 1 == G) read_w(f);
+          // The vector unit adds the sums of the fragment before.
+          f32x4& to = acc[f][(g + G - 1) % G];
+          const f32x4& sum = part[(g + 1) % 2][f];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) to[i] = __builtin_fmaf(sum[i], by[f / 2], to[i]);
+          asm volatile("" : "+v"(to));  // here, or the additions are put off while their operands pile up
+          if (g == 0 && f >= 2 && s > 0) fetch_ahead(s + 1, cur ^ kBuffer, f);
+          if (g + 1 == G && f >= 2 && s + 1 < steps) fetch_ahead(s + 2, cur ^ kBuffer, f - 2);
         }
         __builtin_amdgcn_sched_barrier(0);
-        part[0] = mac_f8(fw[0][1], fa[1], part[0]);
-        part[1] = mac_f8(fw[1][1], fa[1], part[1]);
-        __builtin_amdgcn_sched_barrier(0);
-        if (g + 1 < G) {
-          read_a(32 * G * wr, g + 1, 1);
-        } else {
-          read_w(1);
-          read_a(s + 1 < steps ? 32 * G * wr : wave_row(next), 0, 1);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        add_scaled(acc[0][g], part[0], sr * by0);
-        add_scaled(acc[1][g], part[1], sr * by1);
-        asm volatile("" : "+v"(acc[0][g]), "+v"(acc[1][g]));  // here, or the additions are put off while their operands pile up
-        __builtin_amdgcn_sched_barrier(0);
+        by[0] = sr * bw[0];
+        by[1] = sr * bw[1];
       }
     }
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[f][G - 1][i] = __builtin_fmaf(part[1][f][i], by[f / 2], acc[f][G - 1][i]);
 
-    // Stores go through a buffer of the tile's rows: what a lane has for a row
-    // or channel past the end gets an offset past the buffer and is dropped.
-    constexpr int kOutFrags = kSwiglu ? 1 : 2;
+    // The results go through LDS, so that a store writes whole cache lines: this
+    // wave's part of the buffer that the next tile's second step is fetched into, 4 KB
+    // with the activations and 4 KB with the weights.  Stores go through a buffer of
+    // the tile's rows: what a lane has for a row or channel past the end gets an
+    // offset past the buffer and is dropped.
+    constexpr int kOutFrags = kSwiglu ? 2 : 4, kRowBytes = 32 * kOutFrags, kPieces = kRowBytes / 16;
+    constexpr int kChunkRows = 4096 / kRowBytes, kChunkFrags = kChunkRows / 16, kChunks = (G + kChunkFrags - 1) / kChunkFrags;
     const uint32_t row_bytes = uint32_t(p.n_out) * 2, out_bytes = uint32_t(now.n_rows) * row_bytes;
     const __amdgpu_buffer_rsrc_t out =
         __builtin_amdgcn_make_buffer_rsrc(p.out + int64_t(now.row0) * p.n_out, 0, out_bytes, 0x00027000);
+    const int c0 = now.c0 + 16 * kOutFrags * wc;
+    uint8_t* const own = s_buf + (cur ^ kBuffer) + 32 * wave * kStepBytes;
+    // Piece `at` of a row; rows in turn begin at all banks.
+    auto place = [&](int r, int at) { return r * kRowBytes + (at ^ (kSwiglu ? r / 4 % 4 : r / 2 % 8)) * 16; };
 #pragma unroll
-    for (int f = 0; f < kOutFrags; ++f) {
-      const int c0 = now.c0 + 32 * kOutFrags * wc + 32 * f;
+    for (int round = 0; round < kChunks; round += 2) {
+      constexpr int kMost = kChunks < 2 ? kChunks : 2;
+      u32x4 v[kMost][4];
+      const int l = int(lane_now());
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        u32x2 v[4];
+      for (int c = 0; c < kMost; ++c) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float x[4];
+        for (int j = 0; j < kChunkFrags; ++j) {
+          const int g = (round + c) * kChunkFrags + j;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = acc[f][g][4 * q + i];
-            if constexpr (kSwiglu) x[i] = silu_times(x[i], acc[1][g][4 * q + i]);
+          for (int f = 0; f < kOutFrags; ++f) {
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[i] = acc[f][g][i];
+              if constexpr (kSwiglu) x[i] = silu_times(x[i], acc[f + 2][g][i]);
+            }
+            *reinterpret_cast<u32x2*>(own + c * kHalf + place(16 * j + l % 16, 2 * f + l / 32) + l / 16 % 2 * 8) =
+                u32x2{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
           }
-          v[q] = u32x2{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
         }
-        // Lanes l and l+32 hold the two halves of each eight channels of one
-        // row: the lower one takes all of the even q, the upper of the odd.
-        const uint32_t l = lane_now();
-        const int r = 32 * G * wr + 32 * g + int(l % 32);
-        const uint32_t at = uint32_t(r) * row_bytes + uint32_t(c0 + 8 * (l / 32)) * 2;
-#pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-          const u32x2 x = permlane32_swap(v[q].x, v[q + 1].x), y = permlane32_swap(v[q].y, v[q + 1].y);
-          const bool some = r < now.n_rows && c0 + 8 * q < p.n_out;
-          __builtin_amdgcn_raw_buffer_store_b128(u32x4{x.x, y.x, x.y, y.y}, out, some ? at + 16 * q : 0xFFFFFFF0u, 0, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
       }
+      __builtin_amdgcn_s_waitcnt(kWaitLdsScalar);
+#pragma unroll
+      for (int c = 0; c < kMost; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[c][i] = *reinterpret_cast<const u32x4*>(own + c * kHalf + place(64 / kPieces * i + l / kPieces, l % kPieces));
+      __builtin_amdgcn_s_waitcnt(kWaitLdsScalar);
+      __builtin_amdgcn_sched_barrier(0);
+      if (round + 2 >= kChunks) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fetch(after, 1, cur ^ kBuffer, i);
+      }
+#pragma unroll
+      for (int c = 0; c < kMost; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 16 * G * wr + (round + c) * kChunkRows + 64 / kPieces * i + l / kPieces, ch = c0 + 8 * (l % kPieces);
+          __builtin_amdgcn_raw_buffer_store_b128(v[c][i], out,
+                                                 r < now.n_rows && ch < p.n_out ? uint32_t(r) * row_bytes + ch * 2 : 0xFFFFFFF0u,
+                                                 0, 0);
+        }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
   for (bool more = true; more;) {
     more = advance(at, next);
     if (!more) next = now;
     after = aim(next);
-    if (now.n_rows > kTile / 2) form(std::integral_constant<int, 4>{});
-    else form(std::integral_constant<int, 2>{});
+    if (now.n_rows > kTile / 2) form(std::integral_constant<int, 8>{});
+    else form(std::integral_constant<int, 4>{});
     now = next;
     from = after;
   }
