@@ -41,13 +41,13 @@ __device__ __forceinline__ f32x4 mac16_f8(const u32x4 (&w)[2], const u32x4 (&a)[
 // of operands and the scales of 256 rows and two blocks of weight rows, in one of
 // two buffers.
 //
-// A step goes through the wave's four fragments of rows: eight products for each,
-// whose sums the vector unit then adds while the matrix unit works for the other
-// wave of the SIMD.  Registers of a fragment are filled again as soon as the
-// products that read them have begun.  Before the last products of a step its
-// buffer is in registers: there is the step's barrier, after which the next
-// step's first fragments are read and the buffer is filled for the step after
-// that.  The stream of steps runs on across tiles.
+// A step goes through the wave's fragments of 16 rows: four products of a whole
+// block each, beside which the vector unit adds the sums of the fragment before.
+// Before the last fragment's products all of the step's buffer is in registers:
+// there is the step's barrier, after which the next step's first fragments are
+// read, each into the registers of the last product that used them, and the
+// buffer is filled for the step after that.  The stream of steps runs on across
+// tiles.
 template <bool kSwiglu>
 __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p) {
   constexpr uint32_t kHalf = kTile * kStepBytes, kBuffer = 2 * kHalf;  // activations, then weights
@@ -122,22 +122,26 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
   // The XCDs begin at different steps, so that they are not all at the same memory channels.
   const int turn = ragged ? 0 : int(xcd * uint32_t(steps) / 8) & ~3;
   uint32_t scales_to = 0, scales_cur = 1;  // of s_scale, where the next group of scales goes, and where the last one read is
-  // A quarter of this wave's part of a step.
-  auto fetch = [&](const From& f, int nth, uint32_t to, int i) __attribute__((always_inline)) {
+  // Rows 8*i .. of this wave's part of a step, of the activations or of the weights.
+  auto fetch = [&](const From& f, int nth, uint32_t to, int i, bool weights) __attribute__((always_inline)) {
     const int s = nth + turn < steps ? nth + turn : nth + turn - steps;
     const uint32_t rows_at = buf0 + to + (32 * wave + 8 * i) * kStepBytes;
     const uint32_t at = uint32_t(s) * kStepBytes + uint32_t(8 * i) * row;
-    fill_lds(f.a, lane_off[i % 2], at, rows_at);
-    fill_lds(f.w, lane_off[i % 2], at, rows_at + kHalf);
-    if (i == 0 && s % 4 == 0) {
+    fill_lds(weights ? f.w : f.a, lane_off[i % 2], at, rows_at + (weights ? kHalf : 0));
+    if (i == 0 && !weights && s % 4 == 0) {
       if (wave <= 4) fill_lds(f.s, s_off, uint32_t(s) * 4, scale0 + scales_to * sizeof(s_scale[0]) + 1024 * wave);
       scales_to ^= 1;
     }
   };
+  auto fetch_all = [&](const From& f, int nth, uint32_t to) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) fetch(f, nth, to, i / 2, i % 2);
+  };
   // The same of step s of the tile being formed or, past its end, of the next one.
-  auto fetch_ahead = [&](int s, uint32_t to, int i) __attribute__((always_inline)) {
+  auto fetch_ahead = [&](int s, uint32_t to, int i, bool weights) __attribute__((always_inline)) {
     const bool same = s < steps;
-    fetch(From{same ? from.a : after.a, same ? from.w : after.w, same ? from.s : after.s}, same ? s : s - steps, to, i);
+    fetch(From{same ? from.a : after.a, same ? from.w : after.w, same ? from.s : after.s}, same ? s : s - steps, to, i,
+          weights);
   };
   // Waits until step s, in the buffer at `in`, is there for all waves.  Pieces past
   // the row's end become zeros in both operands: what was read there instead may be a NaN.
@@ -179,11 +183,9 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
   };
   auto wave_row = [&](const TilePlace& t) { return t.n_rows > kTile / 2 ? 128 * wr : 64 * wr; };
 
-#pragma unroll
-  for (int i = 0; i < 4; ++i) fetch(from, 0, 0, i);
+  fetch_all(from, 0, 0);
   arrived(0, 0);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) fetch(from, 1, kBuffer, i);
+  fetch_all(from, 1, kBuffer);
 #pragma unroll
   for (int f = 0; f < 4; ++f) read_w(f);
   read_a(wave_row(now), 0);
@@ -206,6 +208,12 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
       const float bw[2] = {scale[4 * (kTile + (kSwiglu ? 0 : wc / 2))], scale[4 * (kTile + (kSwiglu ? 1 : wc / 2))]};
 #pragma unroll
       for (int g = 0; g < G; ++g) {
+        // The wave of a SIMD that is behind goes first.  Otherwise the older one does, waits 950 of the step's 4230
+        // cycles at the barrier, and leaves the matrix unit to a single wave meanwhile; like this 450 of 4050.
+        if (g == 0) __builtin_amdgcn_s_setprio(3);
+        if (g == G / 4) __builtin_amdgcn_s_setprio(2);
+        if (g == G / 2) __builtin_amdgcn_s_setprio(1);
+        if (g == 3 * G / 4) __builtin_amdgcn_s_setprio(0);
         const float sr = scale[4 * (16 * G * wr + 16 * g + (lane_now() & 15))];
         const int next_row = s + 1 < steps ? 16 * G * wr : wave_row(next);
         __builtin_amdgcn_sched_barrier(0);
@@ -227,8 +235,9 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
 #pragma unroll
           for (int i = 0; i < 4; ++i) to[i] = __builtin_fmaf(sum[i], by[f / 2], to[i]);
           asm volatile("" : "+v"(to));  // here, or the additions are put off while their operands pile up
-          if (g == 0 && f >= 2 && s > 0) fetch_ahead(s + 1, cur ^ kBuffer, f);
-          if (g + 1 == G && f >= 2 && s + 1 < steps) fetch_ahead(s + 2, cur ^ kBuffer, f - 2);
+          // Requests two at a time: one holds up the wave that makes it while the other waves' are taken.
+          if (g < 3 && f % 2 == 1 && s > 0) fetch_ahead(s + 1, cur ^ kBuffer, g + 1, f == 3);
+          if (g + 1 == G && f % 2 == 1 && s + 1 < steps) fetch_ahead(s + 2, cur ^ kBuffer, 0, f == 3);
         }
         __builtin_amdgcn_sched_barrier(0);
         by[0] = sr * bw[0];
@@ -285,10 +294,7 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
           v[c][i] = *reinterpret_cast<const u32x4*>(own + c * kHalf + place(64 / kPieces * i + l / kPieces, l % kPieces));
       __builtin_amdgcn_s_waitcnt(kWaitLdsScalar);
       __builtin_amdgcn_sched_barrier(0);
-      if (round + 2 >= kChunks) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) fetch(after, 1, cur ^ kBuffer, i);
-      }
+      if (round + 2 >= kChunks) fetch_all(after, 1, cur ^ kBuffer);
 #pragma unroll
       for (int c = 0; c < kMost; ++c)
 #pragma unroll
