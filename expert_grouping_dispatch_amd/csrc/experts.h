@@ -62,6 +62,7 @@ struct FewLayer {
   int inter;
   uint16_t* out;
   uint16_t* h;  // two [n_rows*top_k, inter], the workspace
+  bool f8;      // e4m3 weights with scales of their blocks; without, scales of their rows mean int8 ones
 };
 template <typename IdT>
 hipError_t launch_layer_few(const FewLayer<IdT>& p, hipStream_t s);

@@ -6,53 +6,7 @@
 #include "entry_experts.h"
 #include "experts.h"
 
-namespace {
-
 using namespace moe;
-
-template <typename IdT>
-int layer_few(const uint16_t* x, int64_t n_rows, int32_t hidden, int32_t top_k, const IdT* topk_ids,
-              const float* router_weights, const int32_t* real_token_count, int32_t tp_rank,
-              int32_t n_experts, const void* w_gate_up, const float* gate_up_scales,
-              const void* w_down, const float* down_scales, int32_t inter, uint16_t* output_tokens,
-              void* workspace, size_t workspace_bytes, void* stream) {
-  const size_t need = moe_layer_few_workspace_bytes(n_rows, top_k, inter);
-  if (need == 0 || !width_ok(hidden) || hidden > kMaxFewWidth || n_experts < 1 || n_experts > MOE_MAX_EXPERTS ||
-      tp_rank < 0)
-    return MOE_ERR_INVALID_ARGUMENT;
-  if (w_gate_up == nullptr || w_down == nullptr || (gate_up_scales == nullptr) != (down_scales == nullptr))
-    return MOE_ERR_INVALID_ARGUMENT;
-  if (n_rows > 0 && (x == nullptr || topk_ids == nullptr || router_weights == nullptr ||
-                     output_tokens == nullptr || workspace == nullptr))
-    return MOE_ERR_INVALID_ARGUMENT;
-  if (!aligned(x, 16) || !aligned(topk_ids, sizeof(IdT)) || !aligned(router_weights, 4) ||
-      !aligned(real_token_count, 4) || !aligned(w_gate_up, 16) || !aligned(gate_up_scales, 16) ||
-      !aligned(w_down, 16) || !aligned(down_scales, 16) || !aligned(output_tokens, 16) ||
-      !aligned(workspace, 256))
-    return MOE_ERR_INVALID_ARGUMENT;
-  if (n_rows > 0 && workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  const uint64_t row_bytes = uint64_t(n_rows) * uint64_t(hidden) * 2, slots = uint64_t(n_rows) * uint64_t(top_k);
-  const uint64_t w_bytes = uint64_t(n_experts) * uint64_t(hidden) * uint64_t(inter) * (gate_up_scales == nullptr ? 2 : 1);
-  const uint64_t channels = uint64_t(n_experts) * 4;
-  if (clash({{x, row_bytes},
-             {topk_ids, slots * sizeof(IdT)},
-             {router_weights, slots * 4},
-             {real_token_count, 4},
-             {w_gate_up, 2 * w_bytes},
-             {w_down, w_bytes},
-             {gate_up_scales, channels * 2 * uint64_t(inter)},
-             {down_scales, channels * uint64_t(hidden)}},
-            {{output_tokens, row_bytes}, {workspace, n_rows > 0 ? need : 0}}))
-    return MOE_ERR_INVALID_ARGUMENT;
-  if (const int d = check_device()) return d;
-  const moe::FewLayer<IdT> p{x, int(n_rows), hidden, top_k, topk_ids, router_weights,
-                             moe::PadMask{real_token_count, top_k, tp_rank}, n_experts, w_gate_up,
-                             gate_up_scales, w_down, down_scales, inter, output_tokens,
-                             static_cast<uint16_t*>(workspace)};
-  return launched(moe::launch_layer_few(p, static_cast<hipStream_t>(stream)));
-}
-
-}  // namespace
 
 extern "C" {
 
@@ -137,9 +91,9 @@ int moe_layer_few(const uint16_t* x, int64_t n_rows, int32_t hidden, int32_t top
                   const void* w_gate_up, const float* gate_up_scales, const void* w_down,
                   const float* down_scales, int32_t inter, uint16_t* output_tokens,
                   void* workspace, size_t workspace_bytes, void* stream) {
-  return layer_few(x, n_rows, hidden, top_k, topk_ids, router_weights, real_token_count, tp_rank,
-                   n_experts, w_gate_up, gate_up_scales, w_down, down_scales, inter, output_tokens,
-                   workspace, workspace_bytes, stream);
+  return layer_few_entry(false, x, n_rows, hidden, top_k, topk_ids, router_weights, real_token_count, tp_rank,
+                         n_experts, w_gate_up, gate_up_scales, w_down, down_scales, inter, output_tokens,
+                         workspace, workspace_bytes, stream);
 }
 
 int moe_layer_few_i64(const uint16_t* x, int64_t n_rows, int32_t hidden, int32_t top_k,
@@ -148,9 +102,9 @@ int moe_layer_few_i64(const uint16_t* x, int64_t n_rows, int32_t hidden, int32_t
                       const void* w_gate_up, const float* gate_up_scales, const void* w_down,
                       const float* down_scales, int32_t inter, uint16_t* output_tokens,
                       void* workspace, size_t workspace_bytes, void* stream) {
-  return layer_few(x, n_rows, hidden, top_k, topk_ids, router_weights, real_token_count, tp_rank,
-                   n_experts, w_gate_up, gate_up_scales, w_down, down_scales, inter, output_tokens,
-                   workspace, workspace_bytes, stream);
+  return layer_few_entry(false, x, n_rows, hidden, top_k, topk_ids, router_weights, real_token_count, tp_rank,
+                         n_experts, w_gate_up, gate_up_scales, w_down, down_scales, inter, output_tokens,
+                         workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

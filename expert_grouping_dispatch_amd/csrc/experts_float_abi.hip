@@ -12,8 +12,6 @@ using namespace moe;
 
 static_assert(MOE_F8_BLOCK == kBlock);
 
-uint64_t blocks_of(int32_t n) { return (uint64_t(n) + kBlock - 1) / kBlock; }
-
 // Both grouped products; bf16 has no scales.
 int expert_matmul(bool f8, const void* a, const float* a_scales, int64_t a_rows, const uint32_t* starts,
                   const int32_t* expert_ids, int32_t n_experts, const void* w, const float* w_scales, int32_t n_out,
@@ -95,6 +93,28 @@ int moe_expert_matmul_f8(const uint8_t* a_q, const float* a_scales, int64_t a_ro
                          int32_t depth, uint32_t flags, uint16_t* out, void* stream) {
   return expert_matmul(true, a_q, a_scales, a_rows, expert_start_indices, expert_ids, n_experts, w_q, w_scales, n_out,
                        depth, flags, out, stream);
+}
+
+int moe_layer_few_f8(const uint16_t* x, int64_t n_rows, int32_t hidden, int32_t top_k,
+                     const int32_t* topk_ids, const float* router_weights,
+                     const int32_t* real_token_count, int32_t tp_rank, int32_t n_experts,
+                     const uint8_t* w_gate_up, const float* gate_up_scales, const uint8_t* w_down,
+                     const float* down_scales, int32_t inter, uint16_t* output_tokens,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  return layer_few_entry(true, x, n_rows, hidden, top_k, topk_ids, router_weights, real_token_count, tp_rank, n_experts,
+                         w_gate_up, gate_up_scales, w_down, down_scales, inter, output_tokens, workspace,
+                         workspace_bytes, stream);
+}
+
+int moe_layer_few_f8_i64(const uint16_t* x, int64_t n_rows, int32_t hidden, int32_t top_k,
+                     const int64_t* topk_ids, const float* router_weights,
+                     const int32_t* real_token_count, int32_t tp_rank, int32_t n_experts,
+                     const uint8_t* w_gate_up, const float* gate_up_scales, const uint8_t* w_down,
+                     const float* down_scales, int32_t inter, uint16_t* output_tokens,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  return layer_few_entry(true, x, n_rows, hidden, top_k, topk_ids, router_weights, real_token_count, tp_rank, n_experts,
+                         w_gate_up, gate_up_scales, w_down, down_scales, inter, output_tokens, workspace,
+                         workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -77,6 +77,7 @@ constexpr int kUpWBytes = 2 * kUpChannels * 128, kUpXBytes = 8192;
 // int8, against 128 or 256 bytes of every activation row.
 struct UpBf16 {
   static constexpr int kStep = 64, kXRow = 128, kWSize = 2;
+  static constexpr bool kBlocks = false;  // whether each 128 values of k and each 128 weight rows have a scale
   // Products of the 16 bytes this lane has of a weight row, piece c of 8, with n activation rows in x.
   static __device__ __forceinline__ f32x16 mac(const u32x4& w, const uint8_t* x, int row, int c, f32x16 acc) {
     const u32x4 v = *reinterpret_cast<const u32x4*>(x + row * kXRow + (c ^ (row / 2 % 8)) * 16);
@@ -86,6 +87,7 @@ struct UpBf16 {
 };
 struct UpI8 {
   static constexpr int kStep = 128, kXRow = 256, kWSize = 1;
+  static constexpr bool kBlocks = false;
   static __device__ __forceinline__ f32x16 mac(const u32x4& w, const uint8_t* x, int row, int c, f32x16 acc) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -97,6 +99,23 @@ struct UpI8 {
     return acc;
   }
 };
+
+struct UpF8 {  // a step is a block of k
+  static constexpr int kStep = 128, kXRow = 256, kWSize = 1;
+  static constexpr bool kBlocks = true;
+  static __device__ __forceinline__ f32x16 mac(const u32x4& w, const uint8_t* x, int row, int c, f32x16 acc) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(x + row * kXRow + ((2 * c + j) ^ (row % 16)) * 16);
+      const u32x2 lo = bf16_of_f8(w[2 * j]), hi = bf16_of_f8(w[2 * j + 1]);
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, (u32x4{lo.x, lo.y, hi.x, hi.y})),
+                                                    __builtin_bit_cast(bf16x8, v), acc, 0, 0, 0);
+    }
+    return acc;
+  }
+};
+
+__device__ __forceinline__ int blocks_of(int n) { return (n + kBlock - 1) / kBlock; }
 
 // Grids of k_few_up of at least this many workgroups of 64 channels; smaller
 // ones leave CUs idle and take 16 channels a workgroup (k_few_up_split).  The
@@ -193,8 +212,14 @@ __device__ __forceinline__ void few_up(const uint8_t* x, int n_rows, int hidden,
   // Workgroups begin at different steps: rows whose length is a power of two
   // would have all of them at the same few memory channels at any time.
   const int turn = ragged ? 0 : int((blockIdx.x * 5 + blockIdx.y * 3) % uint32_t(steps));
-  auto fetch = [&](int nth, uint8_t* to_w, uint8_t* xa, uint8_t* xb) {
+  struct BlockScales {
+    float gate, up;
+  };
+  const float* s_gate = C::kBlocks ? w_scales + int64_t(c / kBlock) * steps : nullptr;
+  const float* s_up = C::kBlocks ? s_gate + int64_t(blocks_of(inter)) * steps : nullptr;
+  auto fetch = [&](int nth, uint8_t* to_w, uint8_t* xa, uint8_t* xb, BlockScales& by) {
     const int s = nth + turn < steps ? nth + turn : nth + turn - steps;
+    if constexpr (C::kBlocks) by = BlockScales{s_gate[s], s_up[s]};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       load_to_lds<true>(i < 2 ? gate : up, w_off[i % 2], uint32_t(s) * 128 + uint32_t(8 * (i % 2)) * w_row,
@@ -207,7 +232,9 @@ __device__ __forceinline__ void few_up(const uint8_t* x, int n_rows, int hidden,
   for (int g = 0; g < G; ++g)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[g][i] = 0.0f;
-  auto step = [&](int s, uint8_t* w, uint8_t* xa, uint8_t* xb, uint8_t* next_w, uint8_t* next_xa, uint8_t* next_xb) {
+  BlockScales by[NB] = {};
+  auto step = [&](int s, uint8_t* w, uint8_t* xa, uint8_t* xb, const BlockScales& by, uint8_t* next_w, uint8_t* next_xa,
+                  uint8_t* next_xb, BlockScales& next_by) {
     if (NB == 3 && s + 1 < steps) __builtin_amdgcn_s_waitcnt(wait_all_but(NB == 3 ? kFills : 0));
     else __builtin_amdgcn_s_waitcnt(kWaitLoads);
     asm volatile("" ::: "memory");
@@ -225,25 +252,35 @@ __device__ __forceinline__ void few_up(const uint8_t* x, int n_rows, int hidden,
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (s + NB - 1 < steps) fetch(s + NB - 1, next_w, next_xa, next_xb);
+    if (s + NB - 1 < steps) fetch(s + NB - 1, next_w, next_xa, next_xb, next_by);
+    f32x16 part[C::kBlocks ? G : 1];
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       const int c = 2 * kk + lane / 32, r = 32 * wave + lane % 32;
       const u32x4 v = *reinterpret_cast<const u32x4*>(w + r * 128 + (c ^ (r / 2 % 8)) * 16);
 #pragma unroll
-      for (int g = 0; g < G; ++g) acc[g] = C::mac(v, g == 0 ? xa : xb, lane % 32, c, acc[g]);
+      for (int g = 0; g < G; ++g) {
+        if constexpr (C::kBlocks) part[g] = C::mac(v, g == 0 ? xa : xb, lane % 32, c, kk == 0 ? f32x16{} : part[g]);
+        else acc[g] = C::mac(v, g == 0 ? xa : xb, lane % 32, c, acc[g]);
+      }
+    }
+    if constexpr (C::kBlocks) {  // gate rows in the first eight of a lane's sums, up rows in the others
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[g][i] = __builtin_fmaf(part[g][i], i < 8 ? by.gate : by.up, acc[g][i]);
     }
   };
 #pragma unroll
   for (int b = 0; b < NB - 1; ++b)
-    if (b < steps) fetch(b, buf.w[b], buf.xa[b], buf.xb[b]);
+    if (b < steps) fetch(b, buf.w[b], buf.xa[b], buf.xb[b], by[b]);
   for (int s = 0; s < steps; s += NB) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       constexpr int kBack = NB - 1;
       const int next = (b + kBack) % NB;
       if (s + b < steps)
-        step(s + b, buf.w[b], buf.xa[b], buf.xb[b], buf.w[next], buf.xa[next], buf.xb[next]);
+        step(s + b, buf.w[b], buf.xa[b], buf.xb[b], by[b], buf.w[next], buf.xa[next], buf.xb[next], by[next]);
     }
   }
   // This lane's channels: 8*q + 4*(lane/32) + i of the wave's 16, gate in acc[8*.. of q 0, 1], up in q 2, 3.
@@ -320,7 +357,9 @@ __global__ __launch_bounds__(kUpThreads, 2) void k_few_up(const uint8_t* __restr
   const int64_t h_rest = int64_t(n_rows) * top_k * inter;
   const uint64_t each = uint64_t(2) * inter * hidden * C::kWSize;
   const uint8_t* we = w + e * each;
-  const float* se = kScaled ? w_scales + int64_t(e) * 2 * inter : nullptr;
+  const float* se = C::kBlocks  ? w_scales + int64_t(e) * 2 * blocks_of(inter) * blocks_of(hidden)
+                    : kScaled ? w_scales + int64_t(e) * 2 * inter
+                              : nullptr;
   const uint64_t w_bytes = (n_experts - e) * each;
   const int c0 = blockIdx.x * kUpChannels;
   for (int i = 0; i < total; i += 64) {
@@ -345,7 +384,7 @@ __global__ __launch_bounds__(kUpThreads, 2) void k_few_up(const uint8_t* __restr
 // The same for small grids: 16 channels a workgroup, k split over its waves,
 // weights straight to registers (stream.h), the parts joined in LDS.
 // list[0 .. n), n <= 16*NG.
-template <class C, int NG, bool kScaled>
+template <class C, int NG, bool kScaled, bool kBlocks>
 __device__ __forceinline__ void few_up_split(const uint8_t* x, int hidden, int top_k, const uint8_t* w,
                                              const float* w_scales, int inter, int tile, const uint16_t* list, int n,
                                              uint16_t* h, int64_t h_rest, f32x4* s_part) {
@@ -368,7 +407,14 @@ __device__ __forceinline__ void few_up_split(const uint8_t* x, int hidden, int t
   int begin, end;
   step_range(hidden, wave, kUpWaves, begin, end);
   constexpr int U = 128 / C::kWBytes / NG;  // what the registers hold
-  stream_products<C, 2, NG, U>(wp, xp, begin, end, hidden, acc);
+  if constexpr (kBlocks) {
+    const int blocks = blocks_of(hidden);
+    const float* const sp[2] = {w_scales + int64_t(tile / (kBlock / 16)) * blocks,
+                                w_scales + int64_t(blocks_of(inter) + tile / (kBlock / 16)) * blocks};
+    stream_scaled<C, 2, NG, U>(wp, xp, sp, begin, end, hidden, acc);
+  } else {
+    stream_products<C, 2, NG, U>(wp, xp, begin, end, hidden, acc);
+  }
 #pragma unroll
   for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -402,7 +448,7 @@ __device__ __forceinline__ void few_up_split(const uint8_t* x, int hidden, int t
 }
 
 // blockIdx.x: 16 channels.
-template <class C, bool kScaled, typename IdT>
+template <class Up, class C, bool kScaled, typename IdT>
 __global__ __launch_bounds__(kUpThreads, 2) void k_few_up_split(
     const uint8_t* __restrict__ x, int n_rows, int hidden, int top_k, const IdT* __restrict__ ids, PadMask pad,
     int n_experts, bool by_slot, const uint8_t* __restrict__ w, const float* __restrict__ w_scales, int inter,
@@ -414,27 +460,38 @@ __global__ __launch_bounds__(kUpThreads, 2) void k_few_up_split(
   const int total = list_slots(ids, real_slots(pad, n_rows, top_k), n_experts, by_slot, s_list, s_n, e);
   const int64_t h_rest = int64_t(n_rows) * top_k * inter;
   const uint8_t* we = w + int64_t(e) * 2 * inter * hidden * (C::kWBytes / 16);
-  const float* se = kScaled ? w_scales + int64_t(e) * 2 * inter : nullptr;
+  const float* se = Up::kBlocks ? w_scales + int64_t(e) * 2 * blocks_of(inter) * blocks_of(hidden)
+                    : kScaled   ? w_scales + int64_t(e) * 2 * inter
+                                : nullptr;
   for (int i = 0; i < total; i += 64) {
     const int n = min(total - i, 64);
     if (n <= 16)
-      few_up_split<C, 1, kScaled>(x, hidden, top_k, we, se, inter, blockIdx.x, s_list + i, n, h, h_rest, s_part);
+      few_up_split<C, 1, kScaled, Up::kBlocks>(x, hidden, top_k, we, se, inter, blockIdx.x, s_list + i, n, h, h_rest, s_part);
     else if (n <= 32)
-      few_up_split<C, 2, kScaled>(x, hidden, top_k, we, se, inter, blockIdx.x, s_list + i, n, h, h_rest, s_part);
+      few_up_split<C, 2, kScaled, Up::kBlocks>(x, hidden, top_k, we, se, inter, blockIdx.x, s_list + i, n, h, h_rest, s_part);
     else
-      few_up_split<C, 4, kScaled>(x, hidden, top_k, we, se, inter, blockIdx.x, s_list + i, n, h, h_rest, s_part);
+      few_up_split<C, 4, kScaled, Up::kBlocks>(x, hidden, top_k, we, se, inter, blockIdx.x, s_list + i, n, h, h_rest, s_part);
   }
 }
 
 // ---- down and the weighted sum ------------------------------------------------
 
+// The scales of a workgroup's rows of w_down, which lie in one block of 128 or in two.
+struct BlockRows {
+  const float* first;  // of the first row's block, one for each block of k
+  int second_at, rows;  // the first row of the second block; blocks there are, 1 or 2
+  // Whether row r (below the workgroup's own rows) is in the second one.
+  __device__ __forceinline__ bool of(int r) const { return rows > 1 && r >= second_at; }
+};
+
 // The results of n <= 16*NG slots over steps [begin, end), U of them requested
 // at a time.  Each slot has two columns: its h in bf16 and, `rest` bytes
 // further, what bf16 left of it.
-template <class C, int RT, int NG, int U>
+template <class D, int RT, int NG, int U>
 __device__ __forceinline__ void few_down_tile(const uint8_t* h, uint32_t rest, int inter, const uint8_t* w,
-                                              int w_rows, const uint16_t* list, int n, int begin, int end, int base,
-                                              f32x4* s_y) {
+                                              int w_rows, const BlockRows& by, const uint16_t* list, int n, int begin,
+                                              int end, int base, f32x4* s_y) {
+  typedef typename D::Core C;
   const int lane = threadIdx.x % kWave;
   const uint8_t* wp[RT];
   const uint8_t* hp[2 * NG];
@@ -450,7 +507,14 @@ __device__ __forceinline__ void few_down_tile(const uint8_t* h, uint32_t rest, i
     hp[g] = h + int64_t(list[min(g * 16 + lane % 16, n - 1)]) * inter * 2;
     hp[NG + g] = hp[g] + rest;
   }
-  stream_products<C, RT, 2 * NG, U>(wp, hp, begin, end, inter, acc);
+  if constexpr (D::kBlocks) {
+    const float* sp[RT];  // of the four rows of this lane's sums
+#pragma unroll
+    for (int r = 0; r < RT; ++r) sp[r] = by.first + (by.of(16 * r + lane / 16 * 4) ? blocks_of(inter) : 0);
+    stream_scaled<C, RT, 2 * NG, U>(wp, hp, sp, begin, end, inter, acc);
+  } else {
+    stream_products<C, RT, 2 * NG, U>(wp, hp, begin, end, inter, acc);
+  }
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     const int at = g * 16 + lane % 16;
@@ -479,16 +543,23 @@ __device__ __forceinline__ void few_down_tile(const uint8_t* h, uint32_t rest, i
 // buffer and read nothing.
 struct DownItem {
   const uint8_t* w;      // the expert's rows of weights, 16 for each of RT
+  const float* scales;   // of their blocks, if there are such
   const uint16_t* list;  // its slots
   f32x4* y;              // where the results of this part of k go
   int n, part;
 };
 constexpr int kDppRowShl8 = 0x108;  // lane l of 16 reads lane l + 8, the upper eight read 0
-template <class C, int RT, int NW, int U, bool kWide, class Find>
+template <class D, int RT, int NW, int U, bool kWide, class Find>
 __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_bytes, uint32_t rest, int inter,
-                                                int w_rows, int base, int first, int items, int bits, Find find) {
+                                                int w_rows, const BlockRows& by, int base, int first, int items,
+                                                int bits, Find find) {
+  typedef typename D::Core C;
   const int lane = threadIdx.x % kWave, group = lane / 16;
   const int steps = (inter + kStreamStep - 1) / kStreamStep;
+  // With block scales parts and batches begin with a block of two steps, whose sums are scaled together.
+  constexpr int kPer = D::kBlocks ? 2 : 1, NS = D::kBlocks ? U / 2 : 1;
+  static_assert(U % kPer == 0);
+  const int whole = (steps + kPer - 1) / kPer;
   constexpr int WV = C::kWBytes / 16, XV = C::kXBytes / 16, NX = kWide ? 2 : 1;
   const uint32_t w_row = uint32_t(inter) * WV, nowhere = 0x80000000u;
   const __amdgpu_buffer_rsrc_t rows = buffer_of(h, h_bytes);
@@ -499,8 +570,8 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
   auto turn = [&](Walk& k) {  // to the next item; at >= items when there is none
     do k.at += NW;
     while (k.at < items && !find(k.at, k.i));
-    k.s = steps * k.i.part >> bits;
-    k.end = steps * (k.i.part + 1) >> bits;
+    k.s = (whole * k.i.part >> bits) * kPer;
+    k.end = min((whole * (k.i.part + 1) >> bits) * kPer, steps);
   };
   Walk ask{}, form;
   ask.at = first - NW;
@@ -517,11 +588,28 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
     return uint32_t(i.list[at]) * uint32_t(inter * 2) + (at < column ? rest : 0u) + group * C::kXBytes;
   };
   uint32_t x_lane = row_of(ask.i);
-  auto request = [&](typename C::W(&w)[U][RT], typename C::X(&x)[U][NX]) {
+  uint32_t s_lane[RT];
+  if constexpr (D::kBlocks)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) s_lane[r] = by.of(16 * r + 4 * group) ? uint32_t(blocks_of(inter)) * 4 : 0u;
+  typedef float Scales[NS][RT];
+  auto request = [&](typename C::W(&w)[U][RT], typename C::X(&x)[U][NX], Scales& sc) {
     const bool live = ask.at < items;
     // Scalars, or each load becomes a loop over the lanes' values.
     const __amdgpu_buffer_rsrc_t from = buffer_of(uniform(ask.i.w), uint64_t(w_rows) * w_row);
     const int s0 = uniform(ask.s);
+    if constexpr (D::kBlocks) {
+      const __amdgpu_buffer_rsrc_t from_s =
+          buffer_of(uniform(reinterpret_cast<const uint8_t*>(ask.i.scales)), uint64_t(by.rows) * blocks_of(inter) * 4);
+#pragma unroll
+      for (int u = 0; u < NS; ++u) {
+        uint32_t out = live && s0 + 2 * u < ask.end ? 0u : nowhere;
+        asm("" : "+v"(out));
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          sc[u][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(from_s, (s_lane[r] | out) + 4 * u, s0 * 2, 0));
+      }
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int s = s0 + u;
@@ -552,13 +640,30 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
     for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   };
   clear();
-  auto products = [&](const typename C::W(&w)[U][RT], const typename C::X(&x)[U][NX]) {
+  auto products = [&](const typename C::W(&w)[U][RT], const typename C::X(&x)[U][NX], const Scales& sc) {
+    if constexpr (D::kBlocks) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; u += 2) {
+        f32x4 part[RT];
 #pragma unroll
-      for (int b = 0; b < NX; ++b)
+        for (int v = 0; v < 2; ++v)
 #pragma unroll
-        for (int r = 0; r < RT; ++r) acc[r] = C::mac(w[u][r], x[u][b], acc[r]);
+          for (int b = 0; b < NX; ++b)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) part[r] = C::mac(w[u + v][r], x[u + v][b], v + b == 0 ? f32x4{} : part[r]);
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[r][q] = __builtin_fmaf(part[r][q], sc[u / 2][r], acc[r][q]);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int b = 0; b < NX; ++b)
+#pragma unroll
+          for (int r = 0; r < RT; ++r) acc[r] = C::mac(w[u][r], x[u][b], acc[r]);
+    }
     form.s += U;
     if (form.at < items && form.s >= form.end) {
       if constexpr (!kWide) {
@@ -576,13 +681,14 @@ __device__ __forceinline__ void few_down_stream(const uint8_t* h, uint64_t h_byt
   };
   typename C::W w0[U][RT], w1[U][RT];
   typename C::X x0[U][NX], x1[U][NX];
-  request(w0, x0);
-  request(w1, x1);
+  Scales c0, c1;
+  request(w0, x0, c0);
+  request(w1, x1, c1);
   while (form.at < items) {
-    products(w0, x0);
-    request(w0, x0);
-    products(w1, x1);  // of zeros after the last item; a way out here would let the first products wait for both
-    request(w1, x1);
+    products(w0, x0, c0);
+    request(w0, x0, c0);
+    products(w1, x1, c1);  // of zeros after the last item; a way out here would let the first products wait for both
+    request(w1, x1, c1);
   }
 }
 
@@ -599,6 +705,7 @@ __device__ __forceinline__ f32x4 mac_4x4(uint32_t w0, uint32_t w1, uint32_t x0, 
 }
 struct DownBf16 {  // kStep values of k are 256 bytes of a weight row
   typedef CoreBf16 Core;
+  static constexpr bool kBlocks = false;
   static constexpr int kStep = 128, kWSize = 2, kXLoads = 1;
   struct W { u32x4 v; };
   static __device__ __forceinline__ W weights(const u32x4& w) { return W{w}; }
@@ -610,10 +717,27 @@ struct DownBf16 {  // kStep values of k are 256 bytes of a weight row
 };
 struct DownI8 {
   typedef CoreI8Bf16 Core;
+  static constexpr bool kBlocks = false;
   static constexpr int kStep = 256, kWSize = 1, kXLoads = 2;
   struct W { u32x2 v[4]; };
   static __device__ __forceinline__ W weights(const u32x4& w) {
     return W{{bf16_of_i8(w[0]), bf16_of_i8(w[1]), bf16_of_i8(w[2]), bf16_of_i8(w[3])}};
+  }
+  static __device__ __forceinline__ f32x4 mac(const W& w, const u32x4 (&x)[2], f32x4 acc) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      acc = mac_4x4(w.v[j].x, w.v[j].y, x[j / 2][j % 2 * 2], x[j / 2][j % 2 * 2 + 1], acc);
+    return acc;
+  }
+};
+
+struct DownF8 {
+  typedef CoreF8Bf16 Core;
+  static constexpr bool kBlocks = true;
+  static constexpr int kStep = 256, kWSize = 1, kXLoads = 2;
+  struct W { u32x2 v[4]; };
+  static __device__ __forceinline__ W weights(const u32x4& w) {
+    return W{{bf16_of_f8(w[0]), bf16_of_f8(w[1]), bf16_of_f8(w[2]), bf16_of_f8(w[3])}};
   }
   static __device__ __forceinline__ f32x4 mac(const W& w, const u32x4 (&x)[2], f32x4 acc) {
 #pragma unroll
@@ -639,7 +763,8 @@ constexpr int kOnce = 2;  // non-temporal: data that no other read wants
 constexpr int kDppRowRor4 = 0x124, kDppRowRor8 = 0x128;  // lane l of 16 reads lane l - 4 or l - 8, cyclically
 template <class D, int RT, int NW, int U, class Find>
 __device__ __forceinline__ void few_down_lines(const uint8_t* h, uint64_t h_bytes, uint32_t rest, int inter,
-                                                int w_rows, int base, int first, int items, int bits, Find find) {
+                                              int w_rows, const BlockRows& by, int base, int first, int items,
+                                               int bits, Find find) {
   constexpr int RG = 4 * RT, XV = D::kXLoads, kStep = D::kStep;
   const int lane = threadIdx.x % kWave, column = lane % 4, block = lane / 4;
   const uint32_t w_row = uint32_t(inter) * D::kWSize, nowhere = 0x80000000u;
@@ -672,7 +797,9 @@ __device__ __forceinline__ void few_down_lines(const uint8_t* h, uint64_t h_byte
     }
   };
   columns();
-  auto request = [&](u32x4(&w)[U][RG], u32x4(&x)[U][2][XV]) {
+  // A lane's sums are of its own piece of k, in one block of it: a scale for either block of rows.
+  typedef float Scales[U][2];
+  auto request = [&](u32x4(&w)[U][RG], u32x4(&x)[U][2][XV], Scales& sc) {
     const bool live = ask.at < items;
     const __amdgpu_buffer_rsrc_t from = buffer_of(uniform(ask.i.w), uint64_t(w_rows) * w_row);
     const int s0 = uniform(ask.s);
@@ -681,6 +808,15 @@ __device__ __forceinline__ void few_down_lines(const uint8_t* h, uint64_t h_byte
       const int s = s0 + u;
       uint32_t out = live && s < ask.end && s * kStep + block * (16 / D::kWSize) < inter ? 0u : nowhere;
       asm("" : "+v"(out));
+      if constexpr (D::kBlocks) {
+        const uint32_t k_blocks = blocks_of(inter);
+        const __amdgpu_buffer_rsrc_t from_s =
+            buffer_of(uniform(reinterpret_cast<const uint8_t*>(ask.i.scales)), uint64_t(by.rows) * k_blocks * 4);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          sc[u][b] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+              from_s, (uint32_t(block / 8 * 4) | out) + b * k_blocks * 4 + 8 * u, s0 * 8, 0));
+      }
 #pragma unroll
       for (int q = 0; q < RG; ++q)
         w[u][q] = __builtin_amdgcn_raw_buffer_load_b128(from, (w_lane[q] | out) + 256 * u, s0 * 256, kOnce);
@@ -703,14 +839,24 @@ __device__ __forceinline__ void few_down_lines(const uint8_t* h, uint64_t h_byte
     for (int q = 0; q < RG; ++q) acc[q][0] = acc[q][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   };
   clear();
-  auto products = [&](const u32x4(&w)[U][RG], const u32x4(&x)[U][2][XV]) {
+  auto products = [&](const u32x4(&w)[U][RG], const u32x4(&x)[U][2][XV], const Scales& sc) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int q = 0; q < RG; ++q) {
         const typename D::W wq = D::weights(w[u][q]);
-        acc[q][0] = D::mac(wq, x[u][0], acc[q][0]);
-        acc[q][1] = D::mac(wq, x[u][1], acc[q][1]);
+        if constexpr (D::kBlocks) {
+          const float scale = by.of(4 * q) ? sc[u][1] : sc[u][0];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const f32x4 part = D::mac(wq, x[u][g], f32x4{});
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[q][g][i] = __builtin_fmaf(part[i], scale, acc[q][g][i]);
+          }
+        } else {
+          acc[q][0] = D::mac(wq, x[u][0], acc[q][0]);
+          acc[q][1] = D::mac(wq, x[u][1], acc[q][1]);
+        }
       }
     form.s += U;
     if (form.at < items && form.s >= form.end) {
@@ -736,13 +882,14 @@ __device__ __forceinline__ void few_down_lines(const uint8_t* h, uint64_t h_byte
     }
   };
   u32x4 w0[U][RG], w1[U][RG], x0[U][2][XV], x1[U][2][XV];
-  request(w0, x0);
-  request(w1, x1);
+  Scales c0, c1;
+  request(w0, x0, c0);
+  request(w1, x1, c1);
   while (form.at < items) {
-    products(w0, x0);
-    request(w0, x0);
-    products(w1, x1);
-    request(w1, x1);
+    products(w0, x0, c0);
+    request(w0, x0, c0);
+    products(w1, x1, c1);
+    request(w1, x1, c1);
   }
 }
 
@@ -768,6 +915,8 @@ __global__ __launch_bounds__(kDownWaves* kWave, 2) void k_few_down(
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int all = n_rows * top_k, routed_end = real_slots(pad, n_rows, top_k);
   const int c0 = blockIdx.x * channels, w_rows = min(channels, hidden - c0);
+  const int second_at = kBlock - c0 % kBlock;
+  const BlockRows by{nullptr, second_at, w_rows > second_at ? 2 : 1};
   constexpr int kBatch = 64 / (C::kWBytes * RT);  // steps: 4 KB of weights a wave
   for (int base = 0; base < all; base += chunk) {
     const int end = min(base + chunk, all), slots = min(end, routed_end);
@@ -831,6 +980,8 @@ __global__ __launch_bounds__(kDownWaves* kWave, 2) void k_few_down(
       i.n = uniform(s_start[a + 1]) - first;
       i.list = s_list + first;
       i.w = w + (int64_t(uniform(s_expert[a])) * hidden + c0) * inter * (C::kWBytes / 16);
+      if constexpr (D::kBlocks)
+        i.scales = w_scales + (int64_t(uniform(s_expert[a])) * blocks_of(hidden) + c0 / kBlock) * blocks_of(inter);
       i.y = s_y + p * chunk * kQuads;
       i.part = p;
     };
@@ -838,19 +989,19 @@ __global__ __launch_bounds__(kDownWaves* kWave, 2) void k_few_down(
     const uint64_t h_bytes = uint64_t(all) * inter * 4;
     const int forms = uniform(s_forms);
     if (forms & 1)
-      few_down_lines<D, RT, NW, 2 / RT>(h, h_bytes, rest, inter, w_rows, base, uniform(wave), active * parts, bits,
+      few_down_lines<D, RT, NW, 2 / RT>(h, h_bytes, rest, inter, w_rows, by, base, uniform(wave), active * parts, bits,
                                         [&](int item, DownItem& i) {
                                           item_of(item, i);
                                           return i.n <= lines;
                                         });
     if (forms & 2)
-      few_down_stream<C, RT, NW, kBatch, false>(h, h_bytes, rest, inter, w_rows, base, uniform(wave), active * parts,
+      few_down_stream<D, RT, NW, kBatch, false>(h, h_bytes, rest, inter, w_rows, by, base, uniform(wave), active * parts,
                                                 bits, [&](int item, DownItem& i) {
                                                   item_of(item, i);
                                                   return i.n > lines && i.n <= 8;
                                                 });
     if (forms & 4)
-      few_down_stream<C, RT, NW, kBatch, true>(h, h_bytes, rest, inter, w_rows, base, uniform(wave), active * parts,
+      few_down_stream<D, RT, NW, kBatch, true>(h, h_bytes, rest, inter, w_rows, by, base, uniform(wave), active * parts,
                                                bits, [&](int item, DownItem& i) {
                                                  item_of(item, i);
                                                  return i.n > 8 && i.n <= 16;
@@ -862,7 +1013,8 @@ __global__ __launch_bounds__(kDownWaves* kWave, 2) void k_few_down(
       int begin, end;
       step_range(inter, i.part, parts, begin, end);
       for (int j = 0; j < i.n; j += 32)
-        few_down_tile<C, RT, 2, 2>(h, rest, inter, i.w, w_rows, i.list + j, min(i.n - j, 32), begin, end, base, i.y);
+        few_down_tile<D, RT, 2, 2>(h, rest, inter, i.w, w_rows, BlockRows{i.scales, by.second_at, by.rows}, i.list + j,
+                                   min(i.n - j, 32), begin, end, base, i.y);
     }
     __syncthreads();
 
@@ -910,8 +1062,8 @@ hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
   const int slots = p.n_rows * p.top_k;
   const bool by_slot = slots < p.n_experts;
   const uint32_t strips = (p.inter + kUpChannels - 1) / kUpChannels, groups = by_slot ? slots : p.n_experts;
-#define MOE_GO(KERNEL, X)                                                                                          \
-  hipLaunchKernelGGL((KERNEL<X, kScaled, IdT>), grid, dim3(kUpThreads), 0, s, reinterpret_cast<const uint8_t*>(p.x), \
+#define MOE_GO(KERNEL, ...)                                                                                        \
+  hipLaunchKernelGGL((KERNEL<__VA_ARGS__, kScaled, IdT>), grid, dim3(kUpThreads), 0, s, reinterpret_cast<const uint8_t*>(p.x), \
                      p.n_rows, p.hidden, p.top_k, p.ids, p.pad, p.n_experts, by_slot,                              \
                      static_cast<const uint8_t*>(p.w_gate_up), p.gate_up_scales, p.inter, p.h)
   if (strips * groups >= uint32_t(kUpStripsMin)) {
@@ -919,7 +1071,7 @@ hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
     MOE_GO(k_few_up, Up);
   } else {
     const dim3 grid(p.inter / 16, groups);
-    MOE_GO(k_few_up_split, typename D::Core);
+    MOE_GO(k_few_up_split, Up, typename D::Core);
   }
 #undef MOE_GO
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
@@ -946,6 +1098,7 @@ hipError_t go(const FewLayer<IdT>& p, hipStream_t s) {
 template <typename IdT>
 hipError_t launch_layer_few(const FewLayer<IdT>& p, hipStream_t s) {
   if (p.n_rows == 0) return hipSuccess;
+  if (p.f8) return go<UpF8, DownF8, false, IdT>(p, s);
   return p.gate_up_scales != nullptr ? go<UpI8, DownI8, true, IdT>(p, s) : go<UpBf16, DownBf16, false, IdT>(p, s);
 }
 

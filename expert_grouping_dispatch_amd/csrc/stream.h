@@ -59,6 +59,29 @@ struct CoreI8Bf16 {  // int8 weights, bf16 activations
   }
 };
 
+// Four e4m3 values to bf16, exact: four bits of mantissa, exponents from -9 to 8.
+__device__ __forceinline__ u32x2 bf16_of_f8(uint32_t w) {
+  return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))};
+}
+
+struct CoreF8Bf16 {  // e4m3 weights, bf16 activations; block scales are the caller's
+  typedef f32x4 Acc;
+  static constexpr int kWBytes = 16, kXBytes = 32;
+  struct W { u32x4 v[1]; };
+  struct X { u32x4 v[2]; };
+  static __device__ __forceinline__ Acc mac(const W& w, const X& x, Acc c) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const u32x2 a = bf16_of_f8(w.v[0][2 * i]), b = bf16_of_f8(w.v[0][2 * i + 1]);
+      const u32x4 wb{a.x, a.y, b.x, b.y};
+      c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wb),
+                                                  __builtin_bit_cast(bf16x8, x.v[i]), c, 0, 0, 0);
+    }
+    return c;
+  }
+};
+
 struct CoreI8 {  // int8 weights, int8 activations
   typedef i32x4 Acc;
   static constexpr int kWBytes = 16, kXBytes = 16;
@@ -140,6 +163,51 @@ __device__ __forceinline__ void stream_products(const uint8_t* const (&w)[RT], c
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int g = 0; g < NG; ++g) acc[r][g] = C::mac(wv[r], xv[g], acc[r][g]);
+  }
+}
+
+// The same for weights with a scale for each 128 values of k, two steps:
+// scales[r][s / 2] is that of step s for the weight rows of this lane's sums.
+template <class C, int RT, int NG, int U>
+__device__ __forceinline__ void stream_scaled(const uint8_t* const (&w)[RT], const uint8_t* const (&x)[NG],
+                                              const float* const (&scales)[RT], int begin, int end, int depth,
+                                              typename C::Acc (&acc)[RT][NG]) {
+  constexpr int WV = C::kWBytes / 16, XV = C::kXBytes / 16;
+  const int group = __lane_id() / 16;
+  for (int s = begin; s < end; s += U) {
+    typename C::W wv[U][RT];
+    typename C::X xv[U][NG];
+    float sv[U][RT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool some = s + u < end && (s + u) * kStreamStep + group * 16 < depth;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        sv[u][r] = s + u < end ? scales[r][(s + u) / 2] : 0.0f;  // the sums are of all lane groups
+#pragma unroll
+        for (int i = 0; i < WV; ++i)
+          wv[u][r].v[i] = some ? load_weight(w[r] + (int64_t(s + u) * 4 + group) * C::kWBytes + 16 * i)
+                               : u32x4{0u, 0u, 0u, 0u};
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < XV; ++i)
+          xv[u][g].v[i] =
+              some ? *reinterpret_cast<const u32x4*>(x[g] + (int64_t(s + u) * 4 + group) * C::kXBytes + 16 * i)
+                   : u32x4{0u, 0u, 0u, 0u};
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const typename C::Acc part = C::mac(wv[u][r], xv[u][g], typename C::Acc{});
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[r][g][i] = __builtin_fmaf(part[i], sv[u][r], acc[r][g][i]);
+        }
   }
 }
 

@@ -21,7 +21,7 @@ lib.moe_expert_matmul_i8.argtypes = [_p, _p, _i64, _p, _p, _i32, _p, _p, _i32, _
 lib.moe_expert_matmul_i8.restype = ctypes.c_int
 lib.moe_layer_few_workspace_bytes.argtypes = [_i64, _i32, _i32]
 lib.moe_layer_few_workspace_bytes.restype = _sz
-for _f in (lib.moe_layer_few, lib.moe_layer_few_i64):
+for _f in (lib.moe_layer_few, lib.moe_layer_few_i64, lib.moe_layer_few_f8, lib.moe_layer_few_f8_i64):
     _f.argtypes = [_p, _i64, _i32, _i32, _p, _p, _p, _i32, _i32, _p, _p, _p, _p, _i32, _p, _p, _sz, _p]
     _f.restype = ctypes.c_int
 
@@ -147,8 +147,10 @@ def moe_layer_few(x: torch.Tensor, topk_ids: torch.Tensor, router_weights: torch
                   w_down: torch.Tensor, output_tokens: torch.Tensor, workspace: torch.Tensor,
                   gate_up_scales: torch.Tensor = None, down_scales: torch.Tensor = None,
                   real_token_count: torch.Tensor = None, tp_rank: int = 0) -> None:
-    """The whole layer for up to FEW_MAX_SLOTS slots: bf16 weights, or int8 weights with a scale per output
-    channel.  w_gate_up is [E, 2*inter, hidden] (gate rows first), w_down [E, hidden, inter]."""
+    """The whole layer for up to FEW_MAX_SLOTS slots: bf16 weights, int8 weights with a scale per output channel, or
+    e4m3 weights (float8_e4m3fn) with a scale per block of 128 x 128: gate_up_scales [E, 2*ceil(inter/128),
+    ceil(hidden/128)], gate blocks first, and down_scales [E, ceil(hidden/128), ceil(inter/128)].  w_gate_up is
+    [E, 2*inter, hidden] (gate rows first), w_down [E, hidden, inter]."""
     dev = _index_of(x)
     src = _at(x, "x", torch.bfloat16, dev)
     dt = _id_dtype(topk_ids, "topk_ids")
@@ -163,7 +165,10 @@ def moe_layer_few(x: torch.Tensor, topk_ids: torch.Tensor, router_weights: torch
     n, h = x.shape
     if (gate_up_scales is None) != (down_scales is None):
         raise ValueError("gate_up_scales and down_scales come together")
-    wdt = torch.bfloat16 if gate_up_scales is None else torch.int8
+    f8 = isinstance(w_gate_up, torch.Tensor) and w_gate_up.dtype is torch.float8_e4m3fn
+    if f8 and gate_up_scales is None:
+        raise ValueError("e4m3 weights need gate_up_scales and down_scales")
+    wdt = torch.float8_e4m3fn if f8 else torch.bfloat16 if gate_up_scales is None else torch.int8
     w1, w2 = _at(w_gate_up, "w_gate_up", wdt, dev), _at(w_down, "w_down", wdt, dev)
     if w_down.dim() != 3 or w_down.shape[1] != h:
         raise ValueError("w_down must be [E, hidden, inter]")
@@ -174,11 +179,19 @@ def moe_layer_few(x: torch.Tensor, topk_ids: torch.Tensor, router_weights: torch
     if gate_up_scales is not None:
         sg = _at(gate_up_scales, "gate_up_scales", torch.float32, dev)
         sd = _at(down_scales, "down_scales", torch.float32, dev)
-        if gate_up_scales.shape != (e, 2 * inter) or down_scales.shape != (e, h):
+        if f8:
+            hb, ib = -(-h // 128), -(-inter // 128)
+            if gate_up_scales.shape != (e, 2 * ib, hb) or down_scales.shape != (e, hb, ib):
+                raise ValueError(f"gate_up_scales must be [E, {2 * ib}, {hb}] and down_scales [E, {hb}, {ib}]")
+        elif gate_up_scales.shape != (e, 2 * inter) or down_scales.shape != (e, h):
             raise ValueError("gate_up_scales must be [E, 2*inter] and down_scales [E, hidden]")
     if real_token_count is not None:
         count = _at(real_token_count, "real_token_count", torch.int32, dev)
         if real_token_count.numel() != 1:
             raise ValueError("real_token_count must have one element")
-    _call(lib.moe_layer_few if dt == torch.int32 else lib.moe_layer_few_i64, "moe_layer_few", dev, src, n, h,
+    if f8:
+        fn = lib.moe_layer_few_f8 if dt == torch.int32 else lib.moe_layer_few_f8_i64
+    else:
+        fn = lib.moe_layer_few if dt == torch.int32 else lib.moe_layer_few_i64
+    _call(fn, "moe_layer_few", dev, src, n, h,
           topk_ids.shape[1], ids, rw, count, int(tp_rank), e, w1, sg, w2, sd, inter, out, space, workspace.numel())

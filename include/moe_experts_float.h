@@ -13,6 +13,7 @@
  *   moe_expert_matmul_f8   every expert's product in e4m3, with a scale for each
  *                          128 values of a row and each 128 x 128 block of the
  *                          weights, optionally with SwiGLU
+ *   moe_layer_few_f8       the whole layer for a few tokens on such weights
  *
  * e4m3 is the 8-bit format with four exponent and three mantissa bits, no
  * infinity, one NaN and 448 as its largest value; its values are passed as
@@ -20,7 +21,8 @@
  * moe_dispatch, moe_expert_matmul with MOE_MATMUL_SWIGLU, moe_expert_matmul and
  * moe_combine; one in e4m3 moe_create_indices, moe_dispatch_f8,
  * moe_expert_matmul_f8 with MOE_MATMUL_SWIGLU, moe_quantize_f8,
- * moe_expert_matmul_f8 and moe_combine.
+ * moe_expert_matmul_f8 and moe_combine.  A decode step runs moe_layer_few or
+ * moe_layer_few_f8 on the same weights.
  */
 #ifndef MOE_EXPERTS_FLOAT_H
 #define MOE_EXPERTS_FLOAT_H
@@ -128,6 +130,33 @@ int moe_expert_matmul_f8(const uint8_t* a_q, const float* a_scales, int64_t a_ro
                          const uint32_t* expert_start_indices, const int32_t* expert_ids,
                          int32_t n_experts, const uint8_t* w_q, const float* w_scales, int32_t n_out,
                          int32_t depth, uint32_t flags, uint16_t* out, void* stream);
+
+/*
+ * The whole layer for a few tokens, as moe_layer_few, on e4m3 weights with a
+ * scale for each 128 x 128 block; the activations stay bf16.
+ *
+ *   w_gate_up      [device] e4m3 [n_experts, 2*inter, hidden], 16-byte aligned.
+ *   gate_up_scales [device] fp32 [n_experts, 2 * ceil(inter / 128), ceil(hidden / 128)],
+ *                  laid out as w_scales of moe_expert_matmul_f8 with SwiGLU.
+ *   w_down         [device] e4m3 [n_experts, hidden, inter], 16-byte aligned.
+ *   down_scales    [device] fp32 [n_experts, ceil(hidden / 128), ceil(inter / 128)].
+ *   The others as moe_layer_few, the workspace's size among them.
+ */
+int moe_layer_few_f8(const uint16_t* x, int64_t n_rows, int32_t hidden, int32_t top_k,
+                     const int32_t* topk_ids, const float* router_weights,
+                     const int32_t* real_token_count, int32_t tp_rank, int32_t n_experts,
+                     const uint8_t* w_gate_up, const float* gate_up_scales, const uint8_t* w_down,
+                     const float* down_scales, int32_t inter, uint16_t* output_tokens,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* As moe_layer_few_f8 for an int64 routing map. */
+int moe_layer_few_f8_i64(const uint16_t* x, int64_t n_rows, int32_t hidden, int32_t top_k,
+                         const int64_t* topk_ids, const float* router_weights,
+                         const int32_t* real_token_count, int32_t tp_rank, int32_t n_experts,
+                         const uint8_t* w_gate_up, const float* gate_up_scales,
+                         const uint8_t* w_down, const float* down_scales, int32_t inter,
+                         uint16_t* output_tokens, void* workspace, size_t workspace_bytes,
+                         void* stream);
 
 #ifdef __cplusplus
 }

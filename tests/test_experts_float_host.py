@@ -28,7 +28,8 @@ def _declared():
 
 def test_every_declared_symbol_is_exported():
     names = _declared()
-    assert {"moe_dispatch_f8", "moe_expert_matmul", "moe_expert_matmul_f8", "moe_quantize_f8"} <= set(names)
+    assert names == ["moe_dispatch_f8", "moe_expert_matmul", "moe_expert_matmul_f8", "moe_layer_few_f8",
+                     "moe_layer_few_f8_i64", "moe_quantize_f8"]
     out = subprocess.run(["nm", "-D", "--defined-only", mod.LIB_PATH], capture_output=True, text=True,
                          check=True).stdout
     exported = {line.split()[-1] for line in out.splitlines() if " T " in line}
@@ -92,6 +93,29 @@ def test_outputs_on_inputs_are_refused():
               [(1, P((7 << 20) - 76)), (7, P((7 << 20) - 124)), (6, P((7 << 20) - 4 * 288 * 144 + 16))])
 
 
+LAYER = [P(1 << 20), 4, 144, 2, P(2 << 20), P(3 << 20), P(10 << 20), 0, 8, P(4 << 20), P(8 << 20), P(5 << 20),
+         P(9 << 20), 48, P(6 << 20), P(7 << 20), 1 << 16, None]
+LAYERS = (mod.lib.moe_layer_few_f8, mod.lib.moe_layer_few_f8_i64)
+
+
+@pytest.mark.parametrize("fn", LAYERS)
+def test_layer_refusals(fn):
+    _refusals(fn, LAYER,
+              [(0, None), (0, P(8)), (1, -1), (1, 1025), (2, 0), (2, 40), (2, (1 << 17) + 16), (3, 0), (3, 513),
+               (4, None), (4, P(2)), (5, None), (5, P(2)), (6, P(2)), (7, -1), (8, 0), (8, 1025), (9, None), (9, P(8)),
+               (10, None), (10, P(2)), (11, None), (11, P(8)), (12, None), (12, P(2)), (13, 0), (13, 24),
+               (13, (1 << 17) + 16), (14, None), (14, P(8)), (15, None), (15, P(128))])
+    # 2 blocks of hidden, 1 of inter: 8 experts' scales are 128 and 64 bytes
+    _refusals(fn, LAYER, [(out, LAYER[i]) for out in (14, 15) for i in (0, 4, 5, 6, 9, 10, 11, 12)] +
+              [(10, P((6 << 20) - 124)), (12, P((6 << 20) - 60)), (6, P((7 << 20) + 1532)), (15, LAYER[14])])
+    small = list(LAYER)
+    small[16] = mod.moe_layer_few_workspace_bytes(4, 2, 48) - 1
+    assert fn(*small) == 2
+    both = list(LAYER)
+    both[10] = both[12] = None  # no scales: not bf16 weights, refused
+    assert fn(*both) == 1
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="a HIP device is present: valid arguments would launch")
 def test_valid_arguments_reach_the_device_check():
     assert mod.lib.moe_dispatch_f8(*DISPATCH) == OK_ON_HOST
@@ -100,12 +124,17 @@ def test_valid_arguments_reach_the_device_check():
     assert mod.lib.moe_quantize_f8(F, 10, 32, P(64), P(1 << 22), P(1 << 23), None) == OK_ON_HOST
     assert mod.lib.moe_expert_matmul(*MATMUL) == OK_ON_HOST
     assert mod.lib.moe_expert_matmul_f8(*MATMUL_F8) == OK_ON_HOST
+    for fn in LAYERS:
+        assert fn(*LAYER) == OK_ON_HOST
+        beside = list(LAYER)
+        beside[10], beside[12] = P((6 << 20) - 128), P((6 << 20) + 4 * 288)
+        assert fn(*beside) == OK_ON_HOST
     beside = list(MATMUL_F8)  # buffers that touch and do not overlap
     beside[1], beside[7] = P((7 << 20) - 80), P((7 << 20) + 10 * 288)
     assert mod.lib.moe_expert_matmul_f8(*beside) == OK_ON_HOST
 
 
-@pytest.mark.parametrize("call", ["dispatch", "quantize", "matmul", "matmul_f8"])
+@pytest.mark.parametrize("call", ["dispatch", "quantize", "matmul", "matmul_f8", "layer"])
 def test_host_tensors_are_refused(call):
     x, i = torch.zeros(2, 32, dtype=torch.bfloat16), torch.zeros(2, 1, dtype=torch.int32)
     q, s = torch.zeros(2, 32).to(F8), torch.zeros(2, 1)
@@ -116,6 +145,8 @@ def test_host_tensors_are_refused(call):
             mod.moe_quantize_f8(x, q, s)
         elif call == "matmul":
             mod.moe_expert_matmul(x, i.view(-1).view(torch.uint32), i, x, x)
+        elif call == "layer":
+            mod.moe_layer_few(x, i, s, q, q, x, q, gate_up_scales=s, down_scales=s)
         else:
             mod.moe_expert_matmul_f8(q, s, i.view(-1).view(torch.uint32), i, q, s, x)
 
