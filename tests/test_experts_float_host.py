@@ -224,5 +224,9 @@ def test_block_weights_and_products_pin():
     assert v[130, 0] == 5 and v[257, 128] == 6 and v[258, 0] == 7 and v[259, 128] == 8
     out, bound = oracle.products(np.array([[1.0, -2.0]]), np.array([[3.0, 4.0], [-128.0, 127.0]]), False)
     assert out.tolist() == [[-5.0, -382.0]] and (bound >= np.abs(out) / 256).all() and (bound < np.abs(out) / 250).all()
+    # e4m3: seven products of an eight may lose 2^-13 of the largest each
+    a8, w8 = np.array([[256.0, -256.0] + [1.0] * 6]), np.array([[256.0, 256.0] + [1.0] * 6])
+    plain, cut = (oracle.products(a8, w8, False, f8)[1][0, 0] for f8 in (False, True))
+    assert oracle.products(a8, w8, False, True)[0][0, 0] == 6 and abs(cut - plain - 56 * (1 + 2.0 ** -8)) < 1e-3
     out, bound = oracle.products(np.array([[40.0]]), np.array([[1.0], [0.5]]), True)
     assert abs(out[0, 0] - 800) < 1e-9 and 800 / 256 <= bound[0, 0] < 3.2

@@ -266,10 +266,36 @@ def test_matmul_against_the_bound(case, kind, swiglu):
     out, at = c.call(), 0
     for e, n in enumerate(c.counts):
         if n:
-            want, bound = oracle.products(*(f64(t) for t in c.values(at, at + n, e)), swiglu)
+            want, bound = oracle.products(*(f64(t) for t in c.values(at, at + n, e)), swiglu, kind == "f8")
             bad = ~(np.abs(f64(out[at:at + n]) - want) <= bound)
             assert not bad.any(), (e, np.argwhere(bad)[:4], f64(out[at:at + n])[bad][:4], want[bad][:4], bound[bad][:4])
         at += n
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f8"])
+@pytest.mark.parametrize("counts, n", [([8], 16), ([8, 40] * 130, 16), ([80, 200], 272)])
+def test_matmul_small_products_beside_large_ones(kind, counts, n):
+    """Pairs of +-2^16 that cancel, with products of 2^-18 to 2^12 in the same eight, in the same sixteen and further
+    off: what the sums may lose is bounded, in bf16 by fp32 alone."""
+    depth = 272
+    c = Case(kind, counts, 0, depth, n, False, 12, True)
+    g = np.random.default_rng(13)
+    a = np.exp2(g.integers(-9, 7, (c.rows, depth)).astype(np.float64)) * g.choice([-1, 1], (c.rows, depth))
+    w = np.exp2(g.integers(-9, 7, (len(counts), n, depth)).astype(np.float64))
+    for at in (0, 7, 17, 40, 41, 130, 200, 270):
+        a[:, at] = w[:, :, at] = 256
+        other = at + 1 if at % 2 == 0 else at - 1 if at != 41 else 43
+        a[:, other], w[:, :, other] = 256, -256
+    c.a, c.w = dev(a.astype(np.float32)).to(c.a.dtype), dev(w.astype(np.float32)).to(c.w.dtype)
+    if kind == "f8":
+        c.sa.fill_(1.0)
+        c.sw.fill_(1.0)
+    out, at = c.call(), 0
+    for e, m in enumerate(counts):
+        want, bound = oracle.products(a[at:at + m], w[e], False, kind == "f8")
+        bad = ~(np.abs(f64(out[at:at + m]) - want) <= bound)
+        assert not bad.any(), (e, np.argwhere(bad)[:4], f64(out[at:at + m])[bad][:4], want[bad][:4], bound[bad][:4])
+        at += m
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f8"])
@@ -435,12 +461,12 @@ def _path_want(kind, x, ids, real, rw, w1, s1, w2, s2, e, h, i):
             a = int(ids[t, j])
             if not 0 <= a < e:
                 continue
-            act, d_act = oracle.products(xv[t:t + 1], fw[0][a], True)
+            act, d_act = oracle.products(xv[t:t + 1], fw[0][a], True, kind == "f8")
             if kind == "f8":  # half a step of e4m3 of the value, of the block's largest 2^-9 / 448 below; the scale
                 big = np.abs(act).reshape(-1)
                 top = np.array([big[128 * b:128 * b + 128].max() for b in range(blocks(i))])[np.arange(i) // 128]
                 d_act = d_act * 1.1 + (np.abs(act) + d_act) * 2.0 ** -4 * 1.01 + (top + d_act.max()) * 2.0 ** -10 / 448
-            y, d_y = oracle.products(act, fw[1][a], False)
+            y, d_y = oracle.products(act, fw[1][a], False, kind == "f8")
             d_y = d_y + np.abs(fw[1][a]).dot(d_act[0]) * 1.01
             w = abs(float(rw[t, j]))
             out[t] += float(rw[t, j]) * y[0]
