@@ -92,7 +92,7 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
   // last one what is read is not used), for four steps at a time: one by one they
   // cost as many cache lines as the operands' bytes do (217 us of 1963).
   struct From {
-    u32x4 a, w, s;
+    BufferAt a, w, s;
   };
   auto aim = [&](const TilePlace& t) __attribute__((always_inline)) {
     From f;
@@ -100,14 +100,14 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
     const uint64_t a0 = (uint64_t(t.row0) + (rows > 0 ? 32 * wave : 0)) * row;
     const int first_w = t.c0 + (kSwiglu ? 32 * (wave / 2) + (wave % 2) * p.n_out : 32 * wave);
     const uint64_t w0 = (uint64_t(t.e) * wide + first_w) * row;
-    f.a = buffer_words(static_cast<const uint8_t*>(p.a) + a0, uint64_t(rows) * row);
-    f.w = buffer_words(static_cast<const uint8_t*>(p.w) + min(w0, w_bytes), w0 < w_bytes ? w_bytes - w0 : 0);
+    f.a = buffer_at(static_cast<const uint8_t*>(p.a) + a0, uint64_t(rows) * row);
+    f.w = buffer_at(static_cast<const uint8_t*>(p.w) + min(w0, w_bytes), w0 < w_bytes ? w_bytes - w0 : 0);
     if (wave < 4) {
-      f.s = buffer_words(reinterpret_cast<const uint8_t*>(p.a_scales + uint64_t(t.row0) * blocks),
+      f.s = buffer_at(reinterpret_cast<const uint8_t*>(p.a_scales + uint64_t(t.row0) * blocks),
                          uint64_t(t.n_rows) * blocks * 4);
     } else {
       const uint64_t each = uint64_t(kSwiglu ? 2 : 1) * half, b = t.e * each + t.c0 / kBlock;
-      f.s = buffer_words(reinterpret_cast<const uint8_t*>(p.w_scales + b * blocks),
+      f.s = buffer_at(reinterpret_cast<const uint8_t*>(p.w_scales + b * blocks),
                          (p.n_experts * each - b) * blocks * 4);
     }
     return f;
@@ -119,32 +119,29 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
   TilePlace now, next;
   Walk at{first, 0};
   if (!advance(at, now)) return;
-  From from = aim(now), after;
   uint32_t cur = 0;  // the buffer being formed, 0 or kBuffer
   const uint32_t buf0 = lds_offset(s_buf), scale0 = lds_offset(s_scale);
   // The XCDs begin at different steps, so that they are not all at the same memory channels.
   const int turn = ragged ? 0 : int(xcd * uint32_t(steps) / 8) & ~3;
-  uint32_t scales_to = 0, scales_cur = 1;  // of s_scale, where the next group of scales goes, and where the last one read is
+  From from = aim(now);     // the tile that is being fetched,
+  int fk = turn;            // the step of it,
+  uint32_t scales_to = 0;   // where its next group of scales goes in s_scale,
+  uint32_t scales_cur = 1;  // and where the last one read is
+  auto after = [&](int k) { return k + 1 == steps ? 0 : k + 1; };
   // Rows 8*i .. of this wave's part of a step, of the activations or of the weights.
-  auto fetch = [&](const From& f, int nth, uint32_t to, int i, bool weights) __attribute__((always_inline)) {
-    const int s = nth + turn < steps ? nth + turn : nth + turn - steps;
+  auto fetch = [&](uint32_t to, int i, bool weights) __attribute__((always_inline)) {
     const uint32_t rows_at = buf0 + to + (32 * wave + 8 * i) * kStepBytes;
-    const uint32_t at = uint32_t(s) * kStepBytes + uint32_t(8 * i) * row;
-    fill_lds(weights ? f.w : f.a, lane_off[i % 2], at, rows_at + (weights ? kHalf : 0));
-    if (i == 0 && !weights && s % 4 == 0) {
-      if (wave <= 4) fill_lds(f.s, s_off, uint32_t(s) * 4, scale0 + scales_to * sizeof(s_scale[0]) + 1024 * wave);
+    const uint32_t at = uint32_t(fk) * kStepBytes + uint32_t(8 * i) * row;
+    fill_lds(buffer_words(weights ? from.w : from.a), lane_off[i % 2], at, rows_at + (weights ? kHalf : 0));
+    if (i == 0 && !weights && fk % 4 == 0) {
+      if (wave <= 4) fill_lds(buffer_words(from.s), s_off, uint32_t(fk) * 4, scale0 + scales_to * sizeof(s_scale[0]) + 1024 * wave);
       scales_to ^= 1;
     }
+    if (i == 3 && weights) fk = after(fk);
   };
-  auto fetch_all = [&](const From& f, int nth, uint32_t to) __attribute__((always_inline)) {
+  auto fetch_all = [&](uint32_t to) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) fetch(f, nth, to, i / 2, i % 2);
-  };
-  // The same of step s of the tile being formed or, past its end, of the next one.
-  auto fetch_ahead = [&](int s, uint32_t to, int i, bool weights) __attribute__((always_inline)) {
-    const bool same = s < steps;
-    fetch(From{same ? from.a : after.a, same ? from.w : after.w, same ? from.s : after.s}, same ? s : s - steps, to, i,
-          weights);
+    for (int i = 0; i < 8; ++i) fetch(to, i / 2, i % 2);
   };
   // Waits until step s, in the buffer at `in`, is there for all waves.  Pieces past
   // the row's end become zeros in both operands: what was read there instead may be a NaN.
@@ -170,28 +167,31 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
   const int wr = wave / 4, wc = wave % 4;
   const uint32_t lane_at = (lane % 16) * kStepBytes + ((lane / 16) ^ (lane / 2 % 8)) * 16;
   u32x4 fw[4][2], fa[2][2];
-  auto read_w = [&](int f) __attribute__((always_inline)) {
-    uint32_t at = lane_at + cur + kHalf + 64 * wc * kStepBytes;
-    asm volatile("" : "+v"(at));
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      fw[f][j] = *reinterpret_cast<const u32x4*>(s_buf + (at ^ (j * 64)) + 16 * f * kStepBytes);
+  uint32_t at_a[2], at_w[2];  // where this lane's pieces of the first fragments lie in the buffer being formed
+  auto look_at = [&](int wave_row) __attribute__((always_inline)) {
+    at_a[0] = lane_at + (cur + wave_row * kStepBytes);
+    at_w[0] = lane_at + (cur + kHalf + 64 * wc * kStepBytes);
+    at_a[1] = at_a[0] ^ 64;
+    at_w[1] = at_w[0] ^ 64;
+    asm volatile("" : "+v"(at_a[0]), "+v"(at_a[1]), "+v"(at_w[0]), "+v"(at_w[1]));  // or each fragment's are kept
   };
-  auto read_a = [&](int wave_row, int g) __attribute__((always_inline)) {
-    uint32_t at = lane_at + cur + wave_row * kStepBytes;
-    asm volatile("" : "+v"(at));
+  auto read_w = [&](int f) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      fa[g % 2][j] = *reinterpret_cast<const u32x4*>(s_buf + (at ^ (j * 64)) + 16 * g * kStepBytes);
+    for (int j = 0; j < 2; ++j) fw[f][j] = *reinterpret_cast<const u32x4*>(s_buf + at_w[j] + 16 * f * kStepBytes);
+  };
+  auto read_a = [&](int g) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) fa[g % 2][j] = *reinterpret_cast<const u32x4*>(s_buf + at_a[j] + 16 * g * kStepBytes);
   };
   auto wave_row = [&](const TilePlace& t) { return t.n_rows > kTile / 2 ? 128 * wr : 64 * wr; };
 
-  fetch_all(from, 0, 0);
+  fetch_all(0);
   arrived(0, 0);
-  fetch_all(from, 1, kBuffer);
+  fetch_all(kBuffer);
+  look_at(wave_row(now));
 #pragma unroll
   for (int f = 0; f < 4; ++f) read_w(f);
-  read_a(wave_row(now), 0);
+  read_a(0);
 
   // A tile of up to 32*G rows, 16*G for each wave.
   auto form = [&](auto frags) __attribute__((always_inline)) {
@@ -204,11 +204,16 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
       part[1][f] = f32x4{};
     }
     float by[2] = {0.0f, 0.0f};  // the scales of the sums in part[1], the step's last fragment
+    int rk = turn;               // the step being formed, counted from the row's start
     for (int s = 0; s < steps; ++s) {
-      const int block = min(s + turn < steps ? s + turn : s + turn - steps, blocks - 1);
-      if (block % 4 == 0 && s < blocks) scales_cur ^= 1;
-      const float* scale = reinterpret_cast<const float*>(s_scale[scales_cur]) + block % 4;
-      const float bw[2] = {scale[4 * (kTile + (kSwiglu ? 0 : wc / 2))], scale[4 * (kTile + (kSwiglu ? 1 : wc / 2))]};
+      if (rk % 4 == 0) scales_cur ^= 1;
+      const uint32_t scales_at = scales_cur * (sizeof(s_scale[0]) / 4) + min(rk, blocks - 1) % 4;
+      uint32_t at_s = scales_at + 4 * (16 * G * wr + (lane & 15));
+      asm volatile("" : "+v"(at_s));
+      const float* const scales = reinterpret_cast<const float*>(s_scale);
+      const float bw[2] = {scales[scales_at + 4 * (kTile + (kSwiglu ? 0 : wc / 2))],
+                           scales[scales_at + 4 * (kTile + (kSwiglu ? 1 : wc / 2))]};
+      rk = after(rk);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         // The wave of a SIMD that is behind goes first.  Otherwise the older one does, waits 950 of the step's 4230
@@ -217,15 +222,19 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
         if (g == G / 4) __builtin_amdgcn_s_setprio(2);
         if (g == G / 2) __builtin_amdgcn_s_setprio(1);
         if (g == 3 * G / 4) __builtin_amdgcn_s_setprio(0);
-        const float sr = scale[4 * (16 * G * wr + 16 * g + (lane_now() & 15))];
-        const int next_row = s + 1 < steps ? 16 * G * wr : wave_row(next);
+        const float sr = scales[at_s + 4 * 16 * g];
         __builtin_amdgcn_sched_barrier(0);
         if (g + 1 < G) {
-          read_a(16 * G * wr, g + 1);
+          read_a(g + 1);
         } else {
           arrived(s + 1 < steps ? s + 1 : 0, cur ^ kBuffer);
           cur ^= kBuffer;
-          read_a(next_row, 0);
+          look_at(s + 1 < steps ? 16 * G * wr : wave_row(next));
+          read_a(0);
+          if (s + 2 == steps) {
+            from = aim(next);
+            fk = turn;
+          }
         }
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
@@ -239,8 +248,8 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
           for (int i = 0; i < 4; ++i) to[i] = __builtin_fmaf(sum[i], by[f / 2], to[i]);
           asm volatile("" : "+v"(to));  // here, or the additions are put off while their operands pile up
           // Requests two at a time: one holds up the wave that makes it while the other waves' are taken.
-          if (g < 3 && f % 2 == 1 && s > 0) fetch_ahead(s + 1, cur ^ kBuffer, g + 1, f == 3);
-          if (g + 1 == G && f % 2 == 1 && s + 1 < steps) fetch_ahead(s + 2, cur ^ kBuffer, 0, f == 3);
+          if (g < 3 && f % 2 == 1 && s > 0) fetch(cur ^ kBuffer, g + 1, f == 3);
+          if (g + 1 == G && f % 2 == 1 && s + 1 < steps) fetch(cur ^ kBuffer, 0, f == 3);
         }
         __builtin_amdgcn_sched_barrier(0);
         by[0] = sr * bw[0];
@@ -297,7 +306,7 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
           v[c][i] = *reinterpret_cast<const u32x4*>(own + c * kHalf + place(64 / kPieces * i + l / kPieces, l % kPieces));
       __builtin_amdgcn_s_waitcnt(kWaitLdsScalar);
       __builtin_amdgcn_sched_barrier(0);
-      if (round + 2 >= kChunks) fetch_all(after, 1, cur ^ kBuffer);
+      if (round + 2 >= kChunks) fetch_all(cur ^ kBuffer);
 #pragma unroll
       for (int c = 0; c < kMost; ++c)
 #pragma unroll
@@ -313,11 +322,9 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
   for (bool more = true; more;) {
     more = advance(at, next);
     if (!more) next = now;
-    after = aim(next);
     if (now.n_rows > kTile / 2) form(std::integral_constant<int, 8>{});
     else form(std::integral_constant<int, 4>{});
     now = next;
-    from = after;
   }
   __builtin_amdgcn_s_waitcnt(kWaitLoads);  // nothing may still be on its way to LDS
 }

@@ -28,10 +28,15 @@ constexpr int kWaitLoads = 0x0F70;     // s_waitcnt vmcnt(0)
 // loads, before the barrier after which their LDS is read.  They have no output
 // register.  A buffer as four scalars; `dst` is an offset into LDS.  M0, which
 // nothing else in such a kernel uses, is set each time.
-__device__ __forceinline__ u32x4 buffer_words(const uint8_t* base, uint64_t bytes) {
-  const uint64_t at = reinterpret_cast<uint64_t>(base);
-  const uint32_t size = bytes < (uint64_t(1) << 31) ? uint32_t(bytes) : 0x7FFFFFF0u;
-  return u32x4{uniform(uint32_t(at)), uniform(uint32_t(at >> 32) & 0xFFFFu), uniform(size), 0x00027000u};
+struct BufferAt {
+  uint64_t base;
+  uint32_t bytes;
+};
+__device__ __forceinline__ BufferAt buffer_at(const uint8_t* base, uint64_t bytes) {
+  return BufferAt{reinterpret_cast<uint64_t>(base), bytes < (uint64_t(1) << 31) ? uint32_t(bytes) : 0x7FFFFFF0u};
+}
+__device__ __forceinline__ u32x4 buffer_words(const BufferAt& b) {
+  return u32x4{uniform(uint32_t(b.base)), uniform(uint32_t(b.base >> 32) & 0xFFFFu), uniform(b.bytes), 0x00027000u};
 }
 __device__ __forceinline__ void fill_lds(const u32x4& from, uint32_t off, uint32_t at, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
