@@ -7,6 +7,7 @@
 //   Acc, mac         the sums of 32 x 32 products and 128 bits (256 with kBlocks) of k a lane added to them
 //   value            a sum's value
 //   Few, FewAcc      the core of stream.h, and its sums
+//   kStripsMin       the smallest grid of strips
 //   tiles            launches the kernel for large groups
 //
 // The rows of an expert are known on the device only.  Kernels share the
@@ -37,12 +38,23 @@ constexpr int kFewWaves = 4, kFewThreads = kFewWaves * kWave;
 constexpr int kTile = 256, kStepBytes = 128;  // tile edge, and bytes of a row per step
 constexpr int kTileThreads = 256, kStripThreads = 256;
 constexpr int kStripFrags = 2;  // of 32 weight rows, for each wave
-// Grids of k_matmul_strip of at least this many workgroups; smaller ones leave
-// CUs idle and go to k_matmul_few.  Strips against k_matmul_few in us: 64
-// workgroups (8 experts, 20 rows each, 7168 -> 2048) 67 and 33, 128 (8, 20,
-// 4096 -> 4096) 45 and 36, 256 (16, 20, 4096 -> 4096) 49 and 66, 896 (32, 16,
-// 2048 -> 7168) 83 and 99.
-constexpr uint32_t kStripsMin = 256;
+// Grids of k_matmul_strip have at least C::kStripsMin workgroups; smaller ones
+// leave CUs idle and go to k_matmul_few.  Strips against k_matmul_few in us, int8,
+// bf16 and e4m3:
+//   64 workgroups (8 experts, 20 rows each, 7168 -> 2048)    67/33  139/54   69/36
+//   128 (8, 20, 4096 -> 4096)                                45/36   71/60   39/38
+//   192 (12, 20, 4096 -> 4096)                                 -     76/89   41/68
+//   256 (16, 20, 4096 -> 4096)                               49/66   85/117  46/84
+//   896 (32, 16, 2048 -> 7168)                               83/99  151/184  79/123
+// Buffers of up to kAloneRows rows over weights of up to kAloneWeights values an
+// expert take one launch: all of their groups go to the first kernel, 64 rows at a
+// time.  24 experts, 4 rows each, 1040 -> 528: 9.9 against 12.2 us in bf16, 8.7 and
+// 11.7 in e4m3, 8.6 and 11.4 in int8.  More rows would read the weights too often
+// where one expert has them all (250 rows, 4096 -> 4096: 91 and 81 us in bf16, 79
+// and 50 in e4m3), and so would larger weights (2 x 120 rows, 4096 -> 14336: 176
+// and 103).
+constexpr uint32_t kAloneRows = 128;
+constexpr int64_t kAloneWeights = int64_t(1) << 22;
 constexpr int kMaxActive = 1024;
 // Rows of tiles that are taken column by column together: 491520 rows on 253
 // experts in e4m3, 2048 -> 7168, 8.18 ms with 8, 8.22 with 6, 8.33 with 4, 8.47
@@ -153,18 +165,21 @@ __device__ __forceinline__ void matmul_few_tile(const ExpertMatmul& p, uint32_t 
 }
 
 template <class C, bool kSwiglu>
-__global__ __launch_bounds__(kFewThreads, 4) void k_matmul_few(ExpertMatmul p) {
+__global__ __launch_bounds__(kFewThreads, 4) void k_matmul_few(ExpertMatmul p, uint32_t most) {
   __shared__ typename C::FewAcc s_part[kFewWaves * 2 * (kFewRows / 16) * kWave];
   uint32_t lo, hi;
   group_rows(p.starts, blockIdx.y, p.a_rows, lo, hi);
-  const uint32_t n = hi - lo;
-  if (n == 0 || n > uint32_t(kFewRows)) return;
+  if (hi - lo > most) return;
   const int e = p.expert_ids[blockIdx.y];
   if (e < 0 || e >= p.n_experts) return;
   const int c0 = blockIdx.x * (kSwiglu ? 16 : 32);
-  if (n <= 16) matmul_few_tile<C, 1, kSwiglu>(p, lo, n, e, c0, s_part);
-  else if (n <= 32) matmul_few_tile<C, 2, kSwiglu>(p, lo, n, e, c0, s_part);
-  else matmul_few_tile<C, 4, kSwiglu>(p, lo, n, e, c0, s_part);
+  for (; lo < hi; lo += kFewRows) {
+    const int n = min(hi - lo, uint32_t(kFewRows));
+    if (n <= 16) matmul_few_tile<C, 1, kSwiglu>(p, lo, n, e, c0, s_part);
+    else if (n <= 32) matmul_few_tile<C, 2, kSwiglu>(p, lo, n, e, c0, s_part);
+    else matmul_few_tile<C, 4, kSwiglu>(p, lo, n, e, c0, s_part);
+    __syncthreads();  // s_part is rewritten for the next rows
+  }
 }
 
 // ---- strips ---------------------------------------------------------------------
@@ -345,18 +360,21 @@ __device__ __forceinline__ void strip(const ExpertMatmul& p, uint32_t lo, int n,
 }
 
 template <class C, bool kSwiglu>
-__global__ __launch_bounds__(kStripThreads, 2) void k_matmul_strip(ExpertMatmul p) {
+__global__ __launch_bounds__(kStripThreads, 2) void k_matmul_strip(ExpertMatmul p, uint32_t most) {
   __shared__ __align__(16) uint8_t s_a0[kFewRows * kStepBytes], s_a1[kFewRows * kStepBytes];
   __shared__ __align__(16) uint8_t s_w0[128 * kStripFrags * kStepBytes], s_w1[128 * kStripFrags * kStepBytes];
   uint32_t lo, hi;
   group_rows(p.starts, blockIdx.y, p.a_rows, lo, hi);
-  const uint32_t n = hi - lo;
-  if (n == 0 || n > uint32_t(kFewRows)) return;
+  if (hi - lo > most) return;
   const int e = p.expert_ids[blockIdx.y];
   if (e < 0 || e >= p.n_experts) return;
   const int c0 = blockIdx.x * (kSwiglu ? 64 * kStripFrags : 128 * kStripFrags);
-  if (n <= 32) strip<C, 1, kSwiglu>(p, lo, n, e, c0, s_a0, s_a1, s_w0, s_w1);
-  else strip<C, 2, kSwiglu>(p, lo, n, e, c0, s_a0, s_a1, s_w0, s_w1);
+  for (; lo < hi; lo += kFewRows) {
+    const int n = min(hi - lo, uint32_t(kFewRows));
+    if (n <= 32) strip<C, 1, kSwiglu>(p, lo, n, e, c0, s_a0, s_a1, s_w0, s_w1);
+    else strip<C, 2, kSwiglu>(p, lo, n, e, c0, s_a0, s_a1, s_w0, s_w1);
+    __syncthreads();  // the buffers are filled again for the next rows
+  }
 }
 
 // ---- tiles ----------------------------------------------------------------------
@@ -719,11 +737,15 @@ hipError_t go_matmul(const ExpertMatmul& p, hipStream_t s) {
   const uint32_t groups = p.a_rows < uint32_t(p.n_experts) ? p.a_rows : uint32_t(p.n_experts);
   const int per = kSwiglu ? 16 : 32, strip = (kSwiglu ? 64 : 128) * kStripFrags;
   const uint32_t strips = (p.n_out + strip - 1) / strip;
-  if (strips * groups >= kStripsMin)
-    hipLaunchKernelGGL((k_matmul_strip<C, kSwiglu>), dim3(strips, groups), dim3(kStripThreads), 0, s, p);
+  const bool alone = p.a_rows <= uint32_t(kFewRows) ||
+                     (p.a_rows <= kAloneRows && int64_t(p.n_out) * p.depth * (kSwiglu ? 2 : 1) <= kAloneWeights);
+  const uint32_t most = alone ? kAloneRows : kFewRows;  // rows of the groups that the first kernel takes
+  if (strips * groups >= C::kStripsMin)
+    hipLaunchKernelGGL((k_matmul_strip<C, kSwiglu>), dim3(strips, groups), dim3(kStripThreads), 0, s, p, most);
   else
-    hipLaunchKernelGGL((k_matmul_few<C, kSwiglu>), dim3((p.n_out + per - 1) / per, groups), dim3(kFewThreads), 0, s, p);
-  if (const hipError_t e = hipGetLastError(); e != hipSuccess || p.a_rows <= uint32_t(kFewRows)) return e;
+    hipLaunchKernelGGL((k_matmul_few<C, kSwiglu>), dim3((p.n_out + per - 1) / per, groups), dim3(kFewThreads), 0, s, p,
+                       most);
+  if (const hipError_t e = hipGetLastError(); e != hipSuccess || alone) return e;
   C::template tiles<kSwiglu>(p, s);
   return hipGetLastError();
 }

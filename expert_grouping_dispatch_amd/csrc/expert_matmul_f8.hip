@@ -345,6 +345,7 @@ namespace {
 struct MatF8 {
   static constexpr int kSize = 1;
   static constexpr bool kFloat = true, kChannels = false, kBlocks = true;
+  static constexpr uint32_t kStripsMin = 160;
   typedef f32x16 Acc;
   typedef f32x4 FewAcc;
   static __device__ __forceinline__ Acc mac(const u32x4 (&w)[2], const u32x4 (&a)[2], const Acc& c) {
