@@ -3,7 +3,8 @@
     python expert_grouping_dispatch_amd/build_lib.py
 
 Compiles every ``csrc/*.hip`` with hipcc (device code for gfx950 only) and
-links them into ``expert_grouping_dispatch_amd/libmoe_route.so``.
+links them into ``expert_grouping_dispatch_amd/libmoe_route.so``; then the
+module ``_fast.so`` that passes torch tensors to it (host code).
 """
 from __future__ import annotations
 
@@ -55,6 +56,35 @@ def _compile(src: str) -> str:
     return obj
 
 
+FAST_SRC = os.path.join(CSRC, "binding.cpp")
+FAST = os.path.join(PKG, "_fast.so")
+
+
+def build_fast(verbose: bool = True) -> str:
+    """The module that passes torch tensors to the library (binding.cpp), linked against it and torch's libraries.
+    Host code only."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    tmp = FAST + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           *[f"-isystem{d}" for d in cpp_extension.include_paths()], f"-isystem{os.path.join(rocm, 'include')}",
+           f"-isystem{sysconfig.get_paths()['include']}", FAST_SRC, "-o", tmp, "-L", PKG, "-lmoe_route",
+           "-Wl,-rpath,$ORIGIN", "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-lamdhip64"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"binding build failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, FAST)
+    if verbose:
+        print(f"built {FAST}", flush=True)
+    return FAST
+
+
 C_EXAMPLE_SRC = os.path.join(ROOT, "tests", "c_abi", "route_smoke.c")
 C_EXAMPLE_BIN = os.path.join(ROOT, "tests", "c_abi", "route_smoke.bin")
 
@@ -88,6 +118,7 @@ def build(verbose: bool = True) -> str:
     os.replace(tmp, LIB)
     if verbose:
         print(f"built {LIB} from {len(srcs)} sources", flush=True)
+    build_fast(verbose)
     build_c_example(verbose)
     return LIB
 

@@ -7,6 +7,7 @@ import ctypes
 
 import torch
 
+from . import _fast
 from . import _check, _device_of, _i32, _i64, _id_dtype, _need, _p, _sz, _u32, lib
 
 MATMUL_SWIGLU = 1          # flags bit of moe_expert_matmul_i8: gate and up rows, out = silu(gate) * up
@@ -151,6 +152,11 @@ def moe_layer_few(x: torch.Tensor, topk_ids: torch.Tensor, router_weights: torch
     e4m3 weights (float8_e4m3fn) with a scale per block of 128 x 128: gate_up_scales [E, 2*ceil(inter/128),
     ceil(hidden/128)], gate blocks first, and down_scales [E, ceil(hidden/128), ceil(inter/128)].  w_gate_up is
     [E, 2*inter, hidden] (gate rows first), w_down [E, hidden, inter]."""
+    if isinstance(w_gate_up, torch.Tensor) and w_gate_up.dtype is torch.float8_e4m3fn:
+        status = _fast.layer_few_f8(x, topk_ids, router_weights, w_gate_up, w_down, output_tokens, workspace,
+                                    gate_up_scales, down_scales, real_token_count, tp_rank)
+        if status >= 0:
+            return _check(status, "moe_layer_few")
     dev = _index_of(x)
     src = _at(x, "x", torch.bfloat16, dev)
     dt = _id_dtype(topk_ids, "topk_ids")

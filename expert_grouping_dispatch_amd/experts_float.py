@@ -1,14 +1,17 @@
 """Binding of the experts' products in floating point
 (``include/moe_experts_float.h``): the grouped products in bf16 and in e4m3
 with a scale for each block of 128, dispatch and rows in e4m3.  Same manner as
-``experts``."""
+``experts``; a call whose tensors are all as they should be goes to the library
+from ``_fast`` (``csrc/binding.cpp``), which returns its status, or -1 for any
+other call, whose arguments are then checked here one by one."""
 from __future__ import annotations
 
 import ctypes
 
 import torch
 
-from . import _i32, _i64, _p, _u32, lib
+from . import _check, _i32, _i64, _p, _u32, lib
+from . import _fast
 from .experts import MATMUL_SWIGLU, _at, _call, _index_of
 
 F8_BLOCK = 128  # values of a row, and weight rows, that share a scale
@@ -45,6 +48,9 @@ def _quantized(q, scales, hidden, dev, names):
 def moe_dispatch_f8(input_tokens: torch.Tensor, top_k: int, restore_token_order: torch.Tensor, out_q: torch.Tensor,
                     out_scales: torch.Tensor) -> None:
     """Token rows as e4m3 with a scale for each 128 values, at every position their slots map to."""
+    status = _fast.dispatch_f8(input_tokens, top_k, restore_token_order, out_q, out_scales)
+    if status >= 0:
+        return _check(status, "moe_dispatch_f8")
     dev = _index_of(input_tokens)
     x = _at(input_tokens, "input_tokens", torch.bfloat16, dev)
     restore = _at(restore_token_order, "restore_token_order", torch.uint32, dev)
@@ -61,6 +67,9 @@ def moe_quantize_f8(x: torch.Tensor, out_q: torch.Tensor, out_scales: torch.Tens
                     row_count: torch.Tensor = None) -> None:
     """Rows of x (bf16 [rows, hidden]) as e4m3 with a scale for each 128 values.  ``row_count`` (uint32 [1] on the
     device, for instance ``expert_start_indices[-1:]``) limits the rows without the host knowing."""
+    status = _fast.quantize_f8(x, out_q, out_scales, row_count)
+    if status >= 0:
+        return _check(status, "moe_quantize_f8")
     dev = _index_of(x)
     src = _at(x, "x", torch.bfloat16, dev)
     if x.dim() != 2:
@@ -104,6 +113,9 @@ def moe_expert_matmul(a: torch.Tensor, expert_start_indices: torch.Tensor, exper
                       out: torch.Tensor, flags: int = 0) -> None:
     """Every active expert's product over its rows of the expert-contiguous buffer, in bf16; w is [E, n, depth]
     (n = 2 * out.shape[1] with MATMUL_SWIGLU, gate rows first)."""
+    status = _fast.expert_matmul(a, expert_start_indices, expert_ids, w, out, flags)
+    if status >= 0:
+        return _check(status, "moe_expert_matmul")
     dev = _index_of(a)
     pa, pw, starts, ids, o, rows, depth, e, n_out = _grouped(a, w, expert_start_indices, expert_ids, out, flags,
                                                              torch.bfloat16, dev, ("a", "w"))
@@ -115,6 +127,9 @@ def moe_expert_matmul_f8(a_q: torch.Tensor, a_scales: torch.Tensor, expert_start
                          flags: int = 0) -> None:
     """The same in e4m3: a_scales is fp32 [rows, ceil(depth/128)], w_scales fp32 [E, ceil(n/128), ceil(depth/128)],
     with MATMUL_SWIGLU [E, 2 * ceil(out.shape[1]/128), ceil(depth/128)], the gate rows' blocks first."""
+    status = _fast.expert_matmul_f8(a_q, a_scales, expert_start_indices, expert_ids, w_q, w_scales, out, flags)
+    if status >= 0:
+        return _check(status, "moe_expert_matmul_f8")
     dev = _index_of(a_q)
     pa, pw, starts, ids, o, rows, depth, e, n_out = _grouped(a_q, w_q, expert_start_indices, expert_ids, out, flags,
                                                              F8, dev, ("a_q", "w_q"))

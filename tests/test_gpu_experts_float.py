@@ -523,3 +523,89 @@ def test_path_eager_and_replayed(kind, n, real, k, e, h, i):
         graph.replay()
         torch.cuda.synchronize()
         np.testing.assert_array_equal(u16(out), eager[turn % 3])
+
+
+# ---- refusals of tensors on the device ---------------------------------------------------
+
+
+def _calls():
+    """name -> (function, good keyword arguments)."""
+    n, h, e, o = 8, 144, 3, 272
+    x = torch.zeros((n, h), dtype=torch.bfloat16, device=DEV)
+    q, s = mod.alloc_quantized_f8(n, h, DEV)
+    starts, ids = u32_of([0, 2, 8, 8]), dev(np.array([0, 2, -1], np.int32))
+    w, out = torch.zeros((e, o, h), dtype=torch.bfloat16, device=DEV), torch.zeros((n, o), dtype=torch.bfloat16, device=DEV)
+    wq, sw = w.to(F8), torch.ones((e, blocks(o), blocks(h)), device=DEV)
+    i = 48
+    gu, d = torch.zeros((e, 2 * i, h), device=DEV).to(F8), torch.zeros((e, h, i), device=DEV).to(F8)
+    return {
+        "quantize": (mod.moe_quantize_f8, dict(x=x, out_q=q, out_scales=s, row_count=u32_of([3]))),
+        "dispatch": (mod.moe_dispatch_f8, dict(input_tokens=x, top_k=2, restore_token_order=u32_of(np.arange(2 * n)),
+                                               out_q=q, out_scales=s)),
+        "matmul": (mod.moe_expert_matmul, dict(a=x, expert_start_indices=starts, expert_ids=ids, w=w, out=out, flags=0)),
+        "matmul_f8": (mod.moe_expert_matmul_f8, dict(a_q=q, a_scales=s, expert_start_indices=starts, expert_ids=ids,
+                                                     w_q=wq, w_scales=sw, out=out, flags=0)),
+        "layer": (mod.moe_layer_few, dict(
+            x=x, topk_ids=torch.zeros((n, 2), dtype=torch.int64, device=DEV), router_weights=torch.ones((n, 2), device=DEV),
+            w_gate_up=gu, w_down=d, output_tokens=torch.zeros_like(x), workspace=mod.alloc_layer_few(n, 2, i, DEV),
+            gate_up_scales=torch.ones((e, 2, 2), device=DEV), down_scales=torch.ones((e, 2, 1), device=DEV),
+            real_token_count=dev(np.array([5], np.int32)), tp_rank=0)),
+    }
+
+
+@pytest.mark.parametrize("call", ["quantize", "dispatch", "matmul", "matmul_f8", "layer"])
+def test_each_tensor_is_checked(call):
+    fn, good = _calls()[call]
+    fn(**good)
+    for name, v in good.items():
+        if not isinstance(v, torch.Tensor):
+            continue
+        for bad, error in ((v.cpu(), ValueError), (None, (TypeError, ValueError, AttributeError)), (v.to(torch.float64), TypeError),
+                           (v.view(torch.uint8) if v.dtype != torch.uint8 else v.view(torch.int8), TypeError),
+                           (torch.stack((v, v), -1)[..., 0] if v.numel() > 1 else None, ValueError),
+                           (v.reshape(-1)[:-1] if v.numel() > 1 else v.expand(1).repeat(2), (ValueError, mod.MoeError)),
+                           (torch.cat((v, v)), (ValueError, mod.MoeError))):
+            optional = bad is None and name in ("row_count", "real_token_count")
+            larger = name == "workspace" and isinstance(bad, torch.Tensor) and bad.dtype == torch.uint8 and bad.is_cuda \
+                and bad.is_contiguous() and bad.numel() >= v.numel()
+            if optional or larger or (bad is None and v.numel() == 1):
+                continue
+            with pytest.raises(error):
+                fn(**{**good, name: bad})
+    torch.cuda.synchronize()
+
+
+def test_bad_numbers_are_refused():
+    calls = _calls()
+    for call, name, values in (("dispatch", "top_k", (0, -1, 3, 1025, 2 ** 40)), ("matmul", "flags", (2, 2 ** 33 + 2)),
+                               ("matmul_f8", "flags", (2, 4, 2 ** 33 + 2)), ("layer", "tp_rank", (-1,))):
+        fn, good = calls[call]
+        for v in values:
+            with pytest.raises((ValueError, mod.MoeError, OverflowError)):
+                fn(**{**good, name: v})
+    fn, good = calls["matmul_f8"]
+    with pytest.raises(ValueError):  # SwiGLU: the weights' scales are two halves of blocks
+        fn(**{**good, "flags": mod.MATMUL_SWIGLU})
+    with pytest.raises(ValueError):
+        calls["layer"][0](**{**calls["layer"][1], "gate_up_scales": None, "down_scales": None})
+
+
+def test_no_rows():
+    """Buffers without rows, and groups without rows: nothing to do, nothing written."""
+    calls = _calls()
+    empty = torch.zeros((0, 144), dtype=torch.bfloat16, device=DEV)
+    q, s = mod.alloc_quantized_f8(0, 144, DEV)
+    mod.moe_quantize_f8(empty, q, s)
+    mod.moe_dispatch_f8(empty, 2, u32_of([]), q, s)
+    g = calls["matmul_f8"][1]
+    none = torch.zeros((0, 272), dtype=torch.bfloat16, device=DEV)
+    mod.moe_expert_matmul_f8(q, s, g["expert_start_indices"], g["expert_ids"], g["w_q"], g["w_scales"], none)
+    mod.moe_expert_matmul(empty, g["expert_start_indices"], g["expert_ids"], calls["matmul"][1]["w"], none)
+    l = dict(calls["layer"][1])
+    for name in ("x", "topk_ids", "router_weights", "output_tokens"):
+        l[name] = l[name][:0]
+    mod.moe_layer_few(**l)
+    out = torch.full((8, 272), 7.0, dtype=torch.bfloat16, device=DEV)
+    for name in ("matmul", "matmul_f8"):
+        calls[name][0](**{**calls[name][1], "expert_start_indices": u32_of([0, 0, 0, 0]), "out": out})
+    assert (out == 7.0).all()
