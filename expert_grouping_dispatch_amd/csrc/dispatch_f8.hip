@@ -20,7 +20,7 @@ namespace moe {
 namespace {
 
 constexpr int kChunk = 1024;    // values a wave takes: eight blocks
-constexpr int kMaxF8Waves = 8;  // chunks of a row that a workgroup takes
+constexpr int kMaxF8Waves = 16; // chunks of a row that a workgroup takes
 // moe_quantize_f8 loads and stores past the caches when what it reads and
 // writes is more than the Infinity Cache holds.  moe_dispatch_f8 loads x
 // plainly, as it mostly still lies in that cache, and streams its top_k times
