@@ -48,11 +48,11 @@ constexpr int kStripFrags = 2;  // of 32 weight rows, for each wave
 //   896 (32, 16, 2048 -> 7168)                               83/99  151/184  79/123
 // Buffers of up to kAloneRows rows over weights of up to kAloneWeights values an
 // expert take one launch: all of their groups go to the first kernel, 64 rows at a
-// time.  24 experts, 4 rows each, 1040 -> 528: 9.9 against 12.2 us in bf16, 8.7 and
-// 11.7 in e4m3, 8.6 and 11.4 in int8.  More rows would read the weights too often
-// where one expert has them all (250 rows, 4096 -> 4096: 91 and 81 us in bf16, 79
-// and 50 in e4m3), and so would larger weights (2 x 120 rows, 4096 -> 14336: 176
-// and 103).
+// time.  24 experts, 4 rows each, 1040 -> 528: 7.2 against 9.4 us in bf16, 5.2 and
+// 7.4 in e4m3, 8.2 and 11.2 in int8; one expert with 100 rows, 4096 -> 1024: 41 and
+// 60, 31 and 33, 23 and 35.  More rows would read the weights too often where one
+// expert has them all (250 rows, 4096 -> 4096: 91 and 81 us in bf16, 79 and 50 in
+// e4m3), and so would larger weights (2 x 120 rows, 4096 -> 14336: 176 and 103).
 constexpr uint32_t kAloneRows = 128;
 constexpr int64_t kAloneWeights = int64_t(1) << 22;
 constexpr int kMaxActive = 1024;
@@ -108,12 +108,12 @@ __device__ __forceinline__ void matmul_few_tile(const ExpertMatmul& p, uint32_t 
     const float* sap[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) sap[g] = p.a_scales + (lo + min(g * 16 + lane % 16, n - 1)) * int64_t(blocks);
-    stream_blocks<2, NG, (NG == 4 ? 1 : 2)>(wp, ap, swp, sap, blocks * wave / kFewWaves,
+    stream_blocks<2, NG, 4 / NG>(wp, ap, swp, sap, blocks * wave / kFewWaves,
                                             blocks * (wave + 1) / kFewWaves, p.depth, acc);
   } else {
     int begin, end;
     step_range(p.depth, wave, kFewWaves, begin, end);
-    stream_products<typename C::Few, 2, NG, (NG == 4 ? 2 : 4) / C::kSize>(wp, ap, begin, end, p.depth, acc);
+    stream_products<typename C::Few, 2, NG, C::kSize == 1 ? (NG == 4 ? 2 : 4) : 4 / NG>(wp, ap, begin, end, p.depth, acc);
   }
 #pragma unroll
   for (int r = 0; r < 2; ++r)
@@ -164,8 +164,10 @@ __device__ __forceinline__ void matmul_few_tile(const ExpertMatmul& p, uint32_t 
   }
 }
 
+// Three waves a SIMD: with four the registers do not hold what is requested together, 2 rows of 4 steps (8 experts, 14
+// rows each, 4096 -> 4096 in bf16: 71 against 57 us; 24 experts, 2 rows, 1040 -> 528: 9.4 against 6.3).
 template <class C, bool kSwiglu>
-__global__ __launch_bounds__(kFewThreads, 4) void k_matmul_few(ExpertMatmul p, uint32_t most) {
+__global__ __launch_bounds__(kFewThreads, 3) void k_matmul_few(ExpertMatmul p, uint32_t most) {
   __shared__ typename C::FewAcc s_part[kFewWaves * 2 * (kFewRows / 16) * kWave];
   uint32_t lo, hi;
   group_rows(p.starts, blockIdx.y, p.a_rows, lo, hi);
