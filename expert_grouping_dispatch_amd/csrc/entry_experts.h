@@ -42,10 +42,9 @@ inline uint64_t blocks_of(int32_t n) { return (uint64_t(n) + kBlock - 1) / kBloc
 // f8: e4m3 weights and scales of their blocks; without, bf16 ones or int8 ones with scales of their rows.
 template <typename IdT>
 int layer_few_entry(bool f8, const uint16_t* x, int64_t n_rows, int32_t hidden, int32_t top_k, const IdT* topk_ids,
-              const float* router_weights, const int32_t* real_token_count, int32_t tp_rank,
-              int32_t n_experts, const void* w_gate_up, const float* gate_up_scales,
-              const void* w_down, const float* down_scales, int32_t inter, uint16_t* output_tokens,
-              void* workspace, size_t workspace_bytes, void* stream) {
+                    const float* router_weights, const int32_t* real_token_count, int32_t tp_rank, int32_t n_experts,
+                    const void* w_gate_up, const float* gate_up_scales, const void* w_down, const float* down_scales,
+                    int32_t inter, uint16_t* output_tokens, void* workspace, size_t workspace_bytes, void* stream) {
   const size_t need = moe_layer_few_workspace_bytes(n_rows, top_k, inter);
   if (need == 0 || !width_ok(hidden) || hidden > kMaxFewWidth || n_experts < 1 || n_experts > MOE_MAX_EXPERTS ||
       tp_rank < 0)
@@ -79,9 +78,8 @@ int layer_few_entry(bool f8, const uint16_t* x, int64_t n_rows, int32_t hidden, 
     return MOE_ERR_INVALID_ARGUMENT;
   if (const int d = check_device()) return d;
   const FewLayer<IdT> p{x, int(n_rows), hidden, top_k, topk_ids, router_weights,
-                             PadMask{real_token_count, top_k, tp_rank}, n_experts, w_gate_up,
-                             gate_up_scales, w_down, down_scales, inter, output_tokens,
-                             static_cast<uint16_t*>(workspace), f8};
+                        PadMask{real_token_count, top_k, tp_rank}, n_experts, w_gate_up, gate_up_scales, w_down,
+                        down_scales, inter, output_tokens, static_cast<uint16_t*>(workspace), f8};
   return launched(launch_layer_few(p, static_cast<hipStream_t>(stream)));
 }
 

@@ -108,8 +108,8 @@ __device__ __forceinline__ void matmul_few_tile(const ExpertMatmul& p, uint32_t 
     const float* sap[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) sap[g] = p.a_scales + (lo + min(g * 16 + lane % 16, n - 1)) * int64_t(blocks);
-    stream_blocks<2, NG, 4 / NG>(wp, ap, swp, sap, blocks * wave / kFewWaves,
-                                            blocks * (wave + 1) / kFewWaves, p.depth, acc);
+    stream_blocks<2, NG, 4 / NG>(wp, ap, swp, sap, blocks * wave / kFewWaves, blocks * (wave + 1) / kFewWaves, p.depth,
+                                 acc);
   } else {
     int begin, end;
     step_range(p.depth, wave, kFewWaves, begin, end);

@@ -106,11 +106,11 @@ __global__ __launch_bounds__(kF8Threads, 2) void k_matmul_tile_f8(ExpertMatmul p
     f.w = buffer_at(static_cast<const uint8_t*>(p.w) + min(w0, w_bytes), w0 < w_bytes ? w_bytes - w0 : 0);
     if (wave < 4) {
       f.s = buffer_at(reinterpret_cast<const uint8_t*>(p.a_scales + uint64_t(t.row0) * blocks),
-                         uint64_t(t.n_rows) * blocks * 4);
+                      uint64_t(t.n_rows) * blocks * 4);
     } else {
       const uint64_t each = uint64_t(kSwiglu ? 2 : 1) * half, b = t.e * each + t.c0 / kBlock;
       f.s = buffer_at(reinterpret_cast<const uint8_t*>(p.w_scales + b * blocks),
-                         (p.n_experts * each - b) * blocks * 4);
+                      (p.n_experts * each - b) * blocks * 4);
     }
     return f;
   };

@@ -44,13 +44,6 @@ __device__ __forceinline__ void fill_lds(const u32x4& from, uint32_t off, uint32
                : "s"(dst), "v"(off), "s"(from), "s"(at)
                : "memory");
 }
-// 64 lanes x 4 bytes.
-__device__ __forceinline__ void fill_lds_words(const u32x4& from, uint32_t off, uint32_t at, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-               :
-               : "s"(dst), "v"(off), "s"(from), "s"(at)
-               : "memory");
-}
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
 }

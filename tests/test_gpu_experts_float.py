@@ -321,6 +321,50 @@ def test_matmul_rows_and_experts_that_are_not_finite_stay_alone(kind, counts, n)
     np.testing.assert_array_equal(u16(out)[keep], u16(plain)[keep])
 
 
+def _moved(t, values):
+    """A copy of t that begins `values` elements into its memory, between NaNs (or 7s) that nothing may come of."""
+    fill = 0x7F if t.dtype == F8 else float("nan") if t.is_floating_point() else 7
+    room = torch.empty(t.numel() + 2 * values, dtype=t.dtype, device=DEV)
+    (room.view(torch.uint8) if t.dtype == F8 else room).fill_(fill)
+    room[values:values + t.numel()] = t.reshape(-1)
+    return room[values:values + t.numel()].view(t.shape)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f8"])
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("case", [2, 5, 11, 15, 21])
+def test_matmul_with_the_least_alignment(case, kind, swiglu):
+    """Operands at 16 bytes, scales at 4: the same bits."""
+    c = Case(kind, *FORMS[case], swiglu, case, True)
+    want = u16(c.call())
+    c.a, c.w = (_moved(t, 16 // t.element_size()) for t in (c.a, c.w))
+    for values in (1, 3):
+        if kind == "f8":
+            c.sa, c.sw = _moved(c.sa, values), _moved(c.sw, values)
+        out = _moved(torch.full((c.rows, c.n), 7.0, dtype=torch.bfloat16, device=DEV), 8)
+        np.testing.assert_array_equal(u16(c.call(out=out)), want)
+
+
+@pytest.mark.parametrize("counts, depth", [([20], 16), ([200, 90], 112), ([200, 90], 128), ([20, 30] * 40, 128),
+                                           ([300, 70], 640)])
+def test_matmul_f8_scales_that_are_not_finite(counts, depth):
+    """An infinite or NaN scale of a row, or of a block of an expert's weights, is in all of that row's or of those
+    channels' outputs, and in no other."""
+    n = 272
+    c = Case("f8", counts, 0, depth, n, False, 6, True)
+    plain = c.call()
+    rows, last = [3, counts[0] - 1], blocks(depth) - 1
+    c.sa[rows[0], 0], c.sa[rows[1], last] = float("inf"), float("nan")
+    c.sw[-1, 0, last], c.sw[-1, 2, 0] = float("-inf"), float("nan")
+    out = c.call()
+    hit = torch.zeros((c.rows, n), dtype=torch.bool, device=DEV)
+    hit[rows] = True
+    hit[c.rows - counts[-1]:, :128] = True
+    hit[c.rows - counts[-1]:, 256:] = True
+    assert not torch.isfinite(out[hit]).any()
+    np.testing.assert_array_equal(u16(out)[~hit.cpu().numpy()], u16(plain)[~hit.cpu().numpy()])
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f8"])
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_matmul_bad_data_stays_inside_the_buffers(kind, swiglu):
@@ -523,6 +567,30 @@ def test_path_eager_and_replayed(kind, n, real, k, e, h, i):
         graph.replay()
         torch.cuda.synchronize()
         np.testing.assert_array_equal(u16(out), eager[turn % 3])
+
+
+def test_rows_on_two_streams_and_the_least_alignment():
+    """Rows quantised from tensors that begin in the middle of their memory, on two streams at once."""
+    g = np.random.default_rng(31)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    work = []
+    for n, h in ((700, 7168), (33, 1040)):
+        xb = _f8_rows(g, n, h)
+        wq, ws = oracle.quantize_f8(xb)
+        q, s = mod.alloc_quantized_f8(n, h, DEV)
+        q.view(torch.uint8).fill_(77), s.fill_(-3.0)
+        work.append((_moved(bf16_from_bits(xb, DEV), 8), _moved(q, 16), _moved(s, 1), wq, ws))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for (x, q, s, _, _), stream in zip(work, streams):
+            q.view(torch.uint8).fill_(77)
+            torch.cuda.synchronize()
+            with torch.cuda.stream(stream):
+                mod.moe_quantize_f8(x, q, s)
+        torch.cuda.synchronize()
+        for _, q, s, wq, ws in work:
+            np.testing.assert_array_equal(codes(q), wq)
+            np.testing.assert_array_equal(s.cpu().numpy(), ws)
 
 
 # ---- refusals of tensors on the device ---------------------------------------------------

@@ -143,6 +143,52 @@ def test_a_tokens_result_does_not_depend_on_the_padding():
         assert not u16(out[n:]).any()
 
 
+@pytest.mark.parametrize("n, k, e, h, i", [(1, 2, 8, 4096, 1040), (12, 4, 9, 272, 400), (200, 2, 3, 144, 272)])
+def test_layer_captured_and_with_the_least_alignment(n, k, e, h, i):
+    """Scales that begin at 4 bytes; two captured calls with workspaces of their own, replayed at once on two streams
+    with other maps and other counts than the captured ones."""
+    steps = []
+    for turn in range(2):
+        per_map = []
+        for m in range(3):
+            ids = _ids(np.random.default_rng(10 * turn + m), n, k, e, "distinct")
+            args, _ = whole_layer(n, k, e, h, i, ids, 40 + turn)  # the same weights, other maps
+            per_map.append((ids, args, [_layer_call(*args, count=c) for c in (n, n // 2)]))
+        sg, sd = per_map[0][1][5:]
+        moved = []
+        for t in (sg, sd):
+            room = torch.full((t.numel() + 2,), float("nan"), device=DEV)
+            room[1:-1] = t.reshape(-1)
+            moved.append(room[1:-1].view(t.shape))
+        steps.append((per_map, moved))
+    graphs = []
+    for per_map, moved in steps:
+        _, args, _ = per_map[0]
+        x, rw = args[0].clone(), dev(args[2])
+        ids, count = dev(per_map[0][0]), dev(np.array([n], np.int32))
+        out, space = torch.zeros_like(x), mod.alloc_layer_few(n, k, i, DEV)
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            mod.moe_layer_few(x, ids, rw, args[3], args[4], out, space, gate_up_scales=moved[0], down_scales=moved[1],
+                              real_token_count=count)
+        graphs.append((graph, x, ids, rw, count, out))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for replay in range(6):
+        for (per_map, _), (graph, x, ids, rw, count, out) in zip(steps, graphs):
+            new_ids, args, _ = per_map[replay % 3]
+            x.copy_(args[0]), ids.copy_(dev(new_ids)), rw.copy_(dev(args[2]))
+            count.fill_((n, n // 2)[replay % 2])
+            out.fill_(7.0)
+        torch.cuda.synchronize()
+        for stream, g in zip(streams, graphs):
+            with torch.cuda.stream(stream):
+                g[0].replay()
+        torch.cuda.synchronize()
+        for (per_map, _), g in zip(steps, graphs):
+            np.testing.assert_array_equal(u16(g[5]), u16(per_map[replay % 3][2][replay % 2]))
+
+
 def test_layer_with_weights_beyond_4_gib():
     """Byte offsets of both weights pass 31 bits, and 32 in the first product."""
     n, k, e, h, i = 40, 4, 68, 8192, 4096
