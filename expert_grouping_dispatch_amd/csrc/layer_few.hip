@@ -36,6 +36,11 @@
 //                tokens, 8 of 256 experts in int8, 7168 x 2048, the layer 1734 us,
 //                1658 with h in bf16; 200 tokens, 2048 x 1024, 466 and 388; 256
 //                tokens on all of 8 experts, 4096 x 2048, 644 and 393.
+//
+// e4m3 weights have a scale for each 128 values of k and 128 rows: a block's sums
+// are multiplied with it and added in fp32.  The two experts above 40 us (5.5 TB/s)
+// and 29 us (4.0: starts and ends are a larger part), the 247 experts 1085 us (6.5
+// TB/s) and 666 us.
 #include <algorithm>
 
 #include "experts.h"
