@@ -131,6 +131,30 @@ def test_dispatch(n, k, e, h, spare):
     assert (codes(q)[m:] == 77).all() and (s[m:] == -3.0).all()
 
 
+def test_rows_beyond_4_gib():
+    """Byte offsets pass 32 bits in the payload: of the last rows in order, and of the places that slots map to."""
+    h = 8192
+    n = 2 ** 32 // h + 37
+    say("rows beyond 4 GiB", n, h)
+    xb = _f8_rows(np.random.default_rng(41), 40, h)
+    wq, ws = oracle.quantize_f8(xb)
+    x = torch.zeros((n, h), dtype=torch.bfloat16, device=DEV)
+    x[n - 40:] = bf16_from_bits(xb, DEV)
+    q, s = mod.alloc_quantized_f8(n, h, DEV)
+    mod.moe_quantize_f8(x, q, s)
+    np.testing.assert_array_equal(codes(q[n - 40:]), wq)
+    np.testing.assert_array_equal(s[n - 40:].cpu().numpy(), ws)
+    assert not codes(q[:50]).any() and (s[:50] == 2.0 ** -116 / 448).all()
+    q.view(torch.uint8).fill_(77), s.fill_(-3.0)
+    places = np.stack([np.arange(40), n - 1 - np.arange(40)], 1)  # each row at both ends
+    mod.moe_dispatch_f8(x[n - 40:], 2, u32_of(places.reshape(-1)), q, s)
+    for at in (slice(0, 40), slice(n - 40, n)):
+        order = slice(None) if at.start == 0 else slice(None, None, -1)
+        np.testing.assert_array_equal(codes(q[at]), wq[order])
+        np.testing.assert_array_equal(s[at].cpu().numpy(), ws[order])
+    assert (codes(q[40:90]) == 77).all() and (codes(q[n - 90:n - 40]) == 77).all()
+
+
 # ---- grouped products ----------------------------------------------------------------
 
 
