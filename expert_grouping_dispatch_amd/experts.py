@@ -8,7 +8,7 @@ import ctypes
 import torch
 
 from . import _fast
-from . import _check, _device_of, _i32, _i64, _id_dtype, _need, _p, _sz, _u32, lib
+from . import _check, _device_of, _fit32, _i32, _i64, _id_dtype, _need, _p, _sz, _u32, lib
 
 MATMUL_SWIGLU = 1          # flags bit of moe_expert_matmul_i8: gate and up rows, out = silu(gate) * up
 MATMUL_MAX_DEPTH = 131056  # largest depth of moe_expert_matmul_i8
@@ -30,7 +30,8 @@ for _f in (lib.moe_layer_few, lib.moe_layer_few_i64, lib.moe_layer_few_f8, lib.m
 # The smallest of these calls take a few microseconds on the GPU, so the checks
 # are kept to what they must read: a tensor's type, its device's number, its
 # layout and its address, and the stream comes as a number, without an object
-# for it (row quantisation of 64 x 256: 6.4 us against 7.5 us a call).
+# for it (row quantisation of 64 x 256: 6.4 us against 7.5 us a call).  Whether
+# numbers fit 32 bits is first asked of all of them together.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -72,12 +73,16 @@ def _quantized(q, scales, hidden, dev, names):
 def moe_dispatch_i8(input_tokens: torch.Tensor, top_k: int, restore_token_order: torch.Tensor, out_q: torch.Tensor,
                     out_scales: torch.Tensor) -> None:
     """Token rows as int8 with a scale each, at every position their slots map to."""
+    if int(top_k) >> 31:
+        _fit32(top_k)
     dev = _index_of(input_tokens)
     x = _at(input_tokens, "input_tokens", torch.bfloat16, dev)
     restore = _at(restore_token_order, "restore_token_order", torch.uint32, dev)
     if input_tokens.dim() != 2:
         raise ValueError("input_tokens must be [N, hidden]")
     n, h = input_tokens.shape
+    if h >> 31:
+        _fit32(h)
     if restore_token_order.numel() != n * top_k:
         raise ValueError("restore_token_order must have N*top_k elements")
     q, scales = _quantized(out_q, out_scales, h, dev, ("out_q", "out_scales"))
@@ -93,6 +98,8 @@ def moe_quantize_i8(x: torch.Tensor, out_q: torch.Tensor, out_scales: torch.Tens
     if x.dim() != 2:
         raise ValueError("x must be [rows, hidden]")
     n, h = x.shape
+    if h >> 31:
+        _fit32(h)
     q, scales = _quantized(out_q, out_scales, h, dev, ("out_q", "out_scales"))
     if out_q.shape[0] != n:
         raise ValueError("out_q must have x's rows")
@@ -109,6 +116,8 @@ def moe_expert_matmul_i8(a_q: torch.Tensor, a_scales: torch.Tensor, expert_start
                          flags: int = 0) -> None:
     """Every active expert's product over its rows of the expert-contiguous buffer; w_q is int8 [E, n, depth]
     (n = 2 * out.shape[1] with MATMUL_SWIGLU, gate rows first), w_scales fp32 [E, n]."""
+    if int(flags) >> 31:
+        _fit32(flags)
     dev = _index_of(a_q)
     if a_q.dim() != 2:
         raise ValueError("a_q must be [rows, depth]")
@@ -121,6 +130,8 @@ def moe_expert_matmul_i8(a_q: torch.Tensor, a_scales: torch.Tensor, expert_start
     if w_q.dim() != 3 or w_q.shape[2] != depth or w_scales.shape != w_q.shape[:2]:
         raise ValueError("w_q must be [E, n, depth] and w_scales [E, n]")
     e, wide = w_q.shape[:2]
+    if (e | wide | depth) >> 31:
+        _fit32(e, wide, depth)
     n_out = wide // 2 if flags & MATMUL_SWIGLU else wide
     if (flags & MATMUL_SWIGLU) and wide % 2:
         raise ValueError("w_q must hold as many up rows as gate rows")
@@ -133,6 +144,9 @@ def moe_expert_matmul_i8(a_q: torch.Tensor, a_scales: torch.Tensor, expert_start
 
 
 def moe_layer_few_workspace_bytes(n_rows: int, top_k: int, inter: int) -> int:
+    """The workspace's size in bytes, 0 if a size is out of range."""
+    if (int(n_rows) | int(top_k) | int(inter)) >> 31:
+        return 0
     return int(lib.moe_layer_few_workspace_bytes(int(n_rows), int(top_k), int(inter)))
 
 
@@ -157,6 +171,8 @@ def moe_layer_few(x: torch.Tensor, topk_ids: torch.Tensor, router_weights: torch
                                     gate_up_scales, down_scales, real_token_count, tp_rank)
         if status >= 0:
             return _check(status, "moe_layer_few")
+    if int(tp_rank) >> 31:
+        _fit32(tp_rank)
     dev = _index_of(x)
     src = _at(x, "x", torch.bfloat16, dev)
     dt = _id_dtype(topk_ids, "topk_ids")
@@ -179,6 +195,8 @@ def moe_layer_few(x: torch.Tensor, topk_ids: torch.Tensor, router_weights: torch
     if w_down.dim() != 3 or w_down.shape[1] != h:
         raise ValueError("w_down must be [E, hidden, inter]")
     e, _, inter = w_down.shape
+    if (h | topk_ids.shape[1] | e | inter) >> 31:
+        _fit32(h, topk_ids.shape[1], e, inter)
     if w_gate_up.shape != (e, 2 * inter, h):
         raise ValueError("w_gate_up must be [E, 2*inter, hidden]")
     sg = sd = count = 0

@@ -10,7 +10,7 @@ import ctypes
 
 import torch
 
-from . import _check, _i32, _i64, _p, _u32, lib
+from . import _check, _fit32, _i32, _i64, _p, _u32, lib
 from . import _fast
 from .experts import MATMUL_SWIGLU, _at, _call, _index_of
 
@@ -51,12 +51,14 @@ def moe_dispatch_f8(input_tokens: torch.Tensor, top_k: int, restore_token_order:
     status = _fast.dispatch_f8(input_tokens, top_k, restore_token_order, out_q, out_scales)
     if status >= 0:
         return _check(status, "moe_dispatch_f8")
+    _fit32(top_k)
     dev = _index_of(input_tokens)
     x = _at(input_tokens, "input_tokens", torch.bfloat16, dev)
     restore = _at(restore_token_order, "restore_token_order", torch.uint32, dev)
     if input_tokens.dim() != 2:
         raise ValueError("input_tokens must be [N, hidden]")
     n, h = input_tokens.shape
+    _fit32(h)
     if restore_token_order.numel() != n * top_k:
         raise ValueError("restore_token_order must have N*top_k elements")
     q, scales = _quantized(out_q, out_scales, h, dev, ("out_q", "out_scales"))
@@ -75,6 +77,7 @@ def moe_quantize_f8(x: torch.Tensor, out_q: torch.Tensor, out_scales: torch.Tens
     if x.dim() != 2:
         raise ValueError("x must be [rows, hidden]")
     n, h = x.shape
+    _fit32(h)
     q, scales = _quantized(out_q, out_scales, h, dev, ("out_q", "out_scales"))
     if out_q.shape[0] != n:
         raise ValueError("out_q must have x's rows")
@@ -98,6 +101,7 @@ def _grouped(a, w, expert_start_indices, expert_ids, out, flags, dtype, dev, nam
     if w.dim() != 3 or w.shape[2] != depth:
         raise ValueError(f"{names[1]} must be [E, n, depth]")
     e, n_out = w.shape[:2]
+    _fit32(e, n_out, depth)
     if flags & MATMUL_SWIGLU:
         if n_out % 2:
             raise ValueError(f"{names[1]} must hold as many up rows as gate rows")
@@ -116,6 +120,7 @@ def moe_expert_matmul(a: torch.Tensor, expert_start_indices: torch.Tensor, exper
     status = _fast.expert_matmul(a, expert_start_indices, expert_ids, w, out, flags)
     if status >= 0:
         return _check(status, "moe_expert_matmul")
+    _fit32(flags)
     dev = _index_of(a)
     pa, pw, starts, ids, o, rows, depth, e, n_out = _grouped(a, w, expert_start_indices, expert_ids, out, flags,
                                                              torch.bfloat16, dev, ("a", "w"))
@@ -130,6 +135,7 @@ def moe_expert_matmul_f8(a_q: torch.Tensor, a_scales: torch.Tensor, expert_start
     status = _fast.expert_matmul_f8(a_q, a_scales, expert_start_indices, expert_ids, w_q, w_scales, out, flags)
     if status >= 0:
         return _check(status, "moe_expert_matmul_f8")
+    _fit32(flags)
     dev = _index_of(a_q)
     pa, pw, starts, ids, o, rows, depth, e, n_out = _grouped(a_q, w_q, expert_start_indices, expert_ids, out, flags,
                                                              F8, dev, ("a_q", "w_q"))
