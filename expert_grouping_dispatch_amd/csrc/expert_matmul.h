@@ -7,6 +7,7 @@
 //   Acc, mac         the sums of 32 x 32 products and 128 bits (256 with kBlocks) of k a lane added to them
 //   value            a sum's value
 //   Few, FewAcc      the core of stream.h, and its sums
+//   kFewPerSimd      waves a SIMD of k_matmul_few
 //   kStripsMin       the smallest grid of strips
 //   tiles            launches the kernel for large groups
 //
@@ -85,7 +86,10 @@ __device__ __forceinline__ void add_scaled(Acc& to, const Acc& part, float scale
 template <class C, int NG, bool kSwiglu>
 __device__ __forceinline__ void matmul_few_tile(const ExpertMatmul& p, uint32_t lo, int n, int e, int c0,
                                                 typename C::FewAcc* s_part) {
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  // Numbers that the compiler knows nothing of, or it forms addresses of all three sizes ahead of the loop over the
+  // group's rows and keeps them: 52 bytes a lane of scratch in int8.
+  asm volatile("" : "+v"(lane), "+v"(wave));
   const int wide = kSwiglu ? 2 * p.n_out : p.n_out;
   const int64_t w_row = int64_t(p.depth) * C::kSize;  // bytes
   const uint8_t* w = static_cast<const uint8_t*>(p.w) + int64_t(e) * wide * w_row;
@@ -164,10 +168,12 @@ __device__ __forceinline__ void matmul_few_tile(const ExpertMatmul& p, uint32_t 
   }
 }
 
-// Three waves a SIMD: with four the registers do not hold what is requested together, 2 rows of 4 steps (8 experts, 14
-// rows each, 4096 -> 4096 in bf16: 71 against 57 us; 24 experts, 2 rows, 1040 -> 528: 9.4 against 6.3).
+// C::kFewPerSimd waves a SIMD.  In int8 four hold all of a grid of 1024 workgroups at once (8 experts, 16 rows each,
+// 2048 -> 2 x 2048: 16.5 against 18.2 us with three).  In bf16 and e4m3 the registers of four do not hold what is
+// requested together, 2 rows of 4 steps (8 experts, 14 rows each, 4096 -> 4096 in bf16: 71 against 57 us; 24
+// experts, 2 rows, 1040 -> 528: 9.4 against 6.3).
 template <class C, bool kSwiglu>
-__global__ __launch_bounds__(kFewThreads, 3) void k_matmul_few(ExpertMatmul p, uint32_t most) {
+__global__ __launch_bounds__(kFewThreads, C::kFewPerSimd) void k_matmul_few(ExpertMatmul p, uint32_t most) {
   __shared__ typename C::FewAcc s_part[kFewWaves * 2 * (kFewRows / 16) * kWave];
   uint32_t lo, hi;
   group_rows(p.starts, blockIdx.y, p.a_rows, lo, hi);

@@ -20,6 +20,7 @@ namespace {
 struct MatBf16 {
   static constexpr int kSize = 2;
   static constexpr bool kFloat = true, kChannels = false, kBlocks = false;
+  static constexpr int kFewPerSimd = 3;
   static constexpr uint32_t kStripsMin = 160;
   typedef f32x16 Acc;
   typedef CoreBf16 Few;

@@ -351,6 +351,7 @@ namespace {
 struct MatF8 {
   static constexpr int kSize = 1;
   static constexpr bool kFloat = true, kChannels = false, kBlocks = true;
+  static constexpr int kFewPerSimd = 3;
   static constexpr uint32_t kStripsMin = 160;
   typedef f32x16 Acc;
   typedef f32x4 FewAcc;

@@ -16,6 +16,7 @@ namespace {
 struct MatI8 {
   static constexpr int kSize = 1;
   static constexpr bool kFloat = false, kChannels = true, kBlocks = false;
+  static constexpr int kFewPerSimd = 4;
   static constexpr uint32_t kStripsMin = 256;
   typedef i32x16 Acc;
   typedef CoreI8 Few;
