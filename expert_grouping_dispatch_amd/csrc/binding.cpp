@@ -70,6 +70,16 @@ bool number(PyObject* o, int64_t* out) {
 
 PyObject* status(int s) { return PyLong_FromLong(s); }
 
+// The status of a call into the library, made without the interpreter's lock: a launch that waits for room in a full
+// queue does not stop the other Python threads.  The caller's arguments hold the tensors meanwhile.
+template <class F>
+PyObject* unlocked(F call) {
+  PyThreadState* const state = PyEval_SaveThread();
+  const int s = call();  // a C entry point, throws nothing
+  PyEval_RestoreThread(state);
+  return status(s);
+}
+
 constexpr auto kBf16 = c10::ScalarType::BFloat16, kF8 = c10::ScalarType::Float8_e4m3fn, kF32 = c10::ScalarType::Float,
                kU32 = c10::ScalarType::UInt32, kI32 = c10::ScalarType::Int, kI64 = c10::ScalarType::Long,
                kU8 = c10::ScalarType::Byte;
@@ -89,7 +99,7 @@ PyObject* quantize_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   c.need(fits(h) && is(q, rows, h) && is(s, rows, blocks(h)));
   void* stream;
   if (!c.ready(&stream)) return status(kElse);
-  return status(moe_quantize_f8(px, rows, int32_t(h), pm, pq, ps, stream));
+  return unlocked([&] { return moe_quantize_f8(px, rows, int32_t(h), pm, pq, ps, stream); });
 }
 
 // (input_tokens, top_k, restore_token_order, out_q, out_scales)
@@ -107,7 +117,7 @@ PyObject* dispatch_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   c.need(fits(h) && fits(rows) && r->numel() == rows * k && is(q, out, h) && is(s, out, blocks(h)));
   void* stream;
   if (!c.ready(&stream)) return status(kElse);
-  return status(moe_dispatch_f8(px, rows, int32_t(h), int32_t(k), pr, pq, ps, out, stream));
+  return unlocked([&] { return moe_dispatch_f8(px, rows, int32_t(h), int32_t(k), pr, pq, ps, out, stream); });
 }
 
 // What both grouped products have: the groups, the output and the sizes.
@@ -145,8 +155,10 @@ PyObject* expert_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto* pa = static_cast<const uint16_t*>(c.at(a[0], kBf16, &ta));
   const auto* pw = static_cast<const uint16_t*>(c.at(a[3], kBf16, &tw));
   if (!c.ok() || !grouped(c, ta, tw, a[1], a[2], a[4], flags, &g) || !c.ready(&g.stream)) return status(kElse);
-  return status(moe_expert_matmul(pa, g.rows, g.starts, g.ids, int32_t(g.experts), pw, int32_t(g.n_out),
-                                  int32_t(g.depth), uint32_t(flags), g.out, g.stream));
+  return unlocked([&] {
+    return moe_expert_matmul(pa, g.rows, g.starts, g.ids, int32_t(g.experts), pw, int32_t(g.n_out), int32_t(g.depth),
+                             uint32_t(flags), g.out, g.stream);
+  });
 }
 
 // (a_q, a_scales, expert_start_indices, expert_ids, w_q, w_scales, out, flags)
@@ -163,8 +175,10 @@ PyObject* expert_matmul_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!c.ok() || !grouped(c, ta, tw, a[2], a[3], a[6], flags, &g)) return status(kElse);
   c.need(is(sa, g.rows, blocks(g.depth)) && is(sw, g.experts, g.halves * blocks(g.n_out), blocks(g.depth)));
   if (!c.ready(&g.stream)) return status(kElse);
-  return status(moe_expert_matmul_f8(pa, psa, g.rows, g.starts, g.ids, int32_t(g.experts), pw, psw, int32_t(g.n_out),
-                                     int32_t(g.depth), uint32_t(flags), g.out, g.stream));
+  return unlocked([&] {
+    return moe_expert_matmul_f8(pa, psa, g.rows, g.starts, g.ids, int32_t(g.experts), pw, psw, int32_t(g.n_out),
+                                int32_t(g.depth), uint32_t(flags), g.out, g.stream);
+  });
 }
 
 // (x, topk_ids, router_weights, w_gate_up, w_down, output_tokens, workspace, gate_up_scales, down_scales,
@@ -196,10 +210,12 @@ PyObject* layer_few_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* s;
   if (!c.ready(&s)) return status(kElse);
   const size_t bytes = size_t(space->numel());
-  return status(wide ? moe_layer_few_f8_i64(px, rows, int32_t(h), int32_t(k), static_cast<const int64_t*>(pi), pr, pm,
-                                            int32_t(rank), int32_t(e), pg, psg, pd, psd, int32_t(i), po, ps, bytes, s)
-                     : moe_layer_few_f8(px, rows, int32_t(h), int32_t(k), static_cast<const int32_t*>(pi), pr, pm,
-                                        int32_t(rank), int32_t(e), pg, psg, pd, psd, int32_t(i), po, ps, bytes, s));
+  return unlocked([&] {
+    return wide ? moe_layer_few_f8_i64(px, rows, int32_t(h), int32_t(k), static_cast<const int64_t*>(pi), pr, pm,
+                                       int32_t(rank), int32_t(e), pg, psg, pd, psd, int32_t(i), po, ps, bytes, s)
+                : moe_layer_few_f8(px, rows, int32_t(h), int32_t(k), static_cast<const int32_t*>(pi), pr, pm,
+                                   int32_t(rank), int32_t(e), pg, psg, pd, psd, int32_t(i), po, ps, bytes, s);
+  });
 }
 
 // No C++ exception may leave a call of Python's: the Python binding makes such a call again and says what is wrong.
