@@ -103,7 +103,8 @@ def _check(status: int, what: str) -> None:
 
 
 def _fit32(*numbers) -> None:
-    """For sizes and numbers that the library takes as 32 bits: ctypes would drop the bits above those silently."""
+    """For sizes and numbers that the library takes as 32 bits: ctypes would drop the bits above those silently.  Callers
+    ask first whether any of them passes 31 bits, which takes less time."""
     for v in numbers:
         if not -0x80000000 <= v <= 0xFFFFFFFF:
             raise ValueError(f"{v} does not fit 32 bits")
@@ -142,7 +143,8 @@ def _id_dtype(t: torch.Tensor, name: str):
 
 def moe_mask_padding(routing_map: torch.Tensor, real_token_count: torch.Tensor, tp_rank: int = 0) -> None:
     """In place: rows r with r + tp_rank*N >= *real_token_count become -1 (int32 or int64 map)."""
-    _fit32(tp_rank)
+    if int(tp_rank) >> 31:
+        _fit32(tp_rank)
     dev = _device_of(routing_map)
     dt = _id_dtype(routing_map, "routing_map")
     _need(routing_map, "routing_map", dt, dev)
@@ -150,7 +152,8 @@ def moe_mask_padding(routing_map: torch.Tensor, real_token_count: torch.Tensor, 
     if routing_map.dim() != 2 or real_token_count.numel() != 1:
         raise ValueError("routing_map must be [N, top_k] and real_token_count [1]")
     n, k = routing_map.shape
-    _fit32(k)
+    if k >> 31:
+        _fit32(k)
     with torch.cuda.device(dev):
         fn = lib.moe_mask_padding if dt == torch.int32 else lib.moe_mask_padding_i64
         _check(fn(_ptr(routing_map), n, k, _ptr(real_token_count), int(tp_rank), _stream(dev)),
@@ -200,7 +203,8 @@ def moe_create_indices(topk_ids: torch.Tensor, n_experts: int, token_expert_orde
                        expert_ids: torch.Tensor, expert_usage_stats: torch.Tensor,
                        workspace: torch.Tensor, scales_offset: torch.Tensor = None,
                        scales_align: int = 128) -> None:
-    _fit32(n_experts, scales_align)
+    if (int(n_experts) | int(scales_align)) >> 31:
+        _fit32(n_experts, scales_align)
     dev = _device_of(topk_ids)
     dt = _id_dtype(topk_ids, "topk_ids")
     _need(topk_ids, "topk_ids", dt, dev)
@@ -221,7 +225,8 @@ def moe_create_indices_noalloc(topk_ids: torch.Tensor, n_experts: int, token_exp
     """moe_create_indices with the library's static per-GPU scratch instead of a workspace (nothing is
     allocated).  Inputs past the scratch raise MoeError with status ERR_SCRATCH_LIMIT; calls on one
     GPU must not overlap."""
-    _fit32(n_experts, scales_align)
+    if (int(n_experts) | int(scales_align)) >> 31:
+        _fit32(n_experts, scales_align)
     dev = _device_of(topk_ids)
     _need(topk_ids, "topk_ids", torch.int32, dev)
     s = topk_ids.numel()
@@ -261,7 +266,8 @@ def moe_mask_create_indices(routing_map: torch.Tensor, real_token_count: torch.T
                             workspace: torch.Tensor, scales_offset: torch.Tensor = None,
                             scales_align: int = 128) -> None:
     """moe_mask_padding then moe_create_indices on the masked map, in one call."""
-    _fit32(tp_rank, n_experts, scales_align)
+    if (int(tp_rank) | int(n_experts) | int(scales_align)) >> 31:
+        _fit32(tp_rank, n_experts, scales_align)
     dev = _device_of(routing_map)
     dt = _id_dtype(routing_map, "routing_map")
     _need(routing_map, "routing_map", dt, dev)
@@ -269,7 +275,8 @@ def moe_mask_create_indices(routing_map: torch.Tensor, real_token_count: torch.T
     if routing_map.dim() != 2 or real_token_count.numel() != 1:
         raise ValueError("routing_map must be [N, top_k] and real_token_count [1]")
     n, k = routing_map.shape
-    _fit32(k)
+    if k >> 31:
+        _fit32(k)
     soff = _index_outputs(dev, n * k, n_experts, token_expert_order, expert_start_indices,
                           restore_token_order, expert_ids, expert_usage_stats, workspace, scales_offset)
     fn = lib.moe_mask_create_indices if dt == torch.int32 else lib.moe_mask_create_indices_i64
@@ -298,7 +305,8 @@ def _rows_and_restore(input_tokens, restore_token_order, top_k, dev):
     if input_tokens.dim() != 2:
         raise ValueError("input_tokens must be [N, hidden]")
     n, h = input_tokens.shape
-    _fit32(h)
+    if h >> 31:
+        _fit32(h)
     if restore_token_order.numel() != n * top_k:
         raise ValueError("restore_token_order must have N*top_k elements")
     return n, h
@@ -306,7 +314,8 @@ def _rows_and_restore(input_tokens, restore_token_order, top_k, dev):
 
 def moe_dispatch(input_tokens: torch.Tensor, top_k: int, restore_token_order: torch.Tensor,
                  out: torch.Tensor) -> None:
-    _fit32(top_k)
+    if int(top_k) >> 31:
+        _fit32(top_k)
     dev = _device_of(input_tokens)
     n, h = _rows_and_restore(input_tokens, restore_token_order, top_k, dev)
     _need(out, "out", torch.bfloat16, dev)
@@ -319,7 +328,8 @@ def moe_dispatch(input_tokens: torch.Tensor, top_k: int, restore_token_order: to
 
 def moe_dispatch_mxfp4(input_tokens: torch.Tensor, top_k: int, restore_token_order: torch.Tensor,
                        out_q: torch.Tensor, out_scales, flags: int = 0) -> None:
-    _fit32(top_k, flags)
+    if (int(top_k) | int(flags)) >> 31:
+        _fit32(top_k, flags)
     dev = _device_of(input_tokens)
     n, h = _rows_and_restore(input_tokens, restore_token_order, top_k, dev)
     _need(out_q, "out_q", torch.uint8, dev)
@@ -342,7 +352,8 @@ def moe_dispatch_mxfp4(input_tokens: torch.Tensor, top_k: int, restore_token_ord
 
 def moe_combine(y: torch.Tensor, router_weights: torch.Tensor, restore_token_order: torch.Tensor,
                 top_k: int, output_tokens: torch.Tensor) -> None:
-    _fit32(top_k)
+    if int(top_k) >> 31:
+        _fit32(top_k)
     dev = _device_of(y)
     _need(y, "y", torch.bfloat16, dev)
     _need(router_weights, "router_weights", torch.float32, dev)
@@ -351,7 +362,8 @@ def moe_combine(y: torch.Tensor, router_weights: torch.Tensor, restore_token_ord
     if y.dim() != 2 or output_tokens.dim() != 2 or y.shape[1] != output_tokens.shape[1]:
         raise ValueError("y must be [rows, hidden] and output_tokens [N, hidden]")
     n, h = output_tokens.shape
-    _fit32(h)
+    if h >> 31:
+        _fit32(h)
     if router_weights.numel() != n * top_k or restore_token_order.numel() != n * top_k:
         raise ValueError("router_weights / restore_token_order must have N*top_k elements")
     with torch.cuda.device(dev):
@@ -363,7 +375,8 @@ def moe_combine_epilogue(y: torch.Tensor, router_weights: torch.Tensor, restore_
                          top_k: int, output_tokens: torch.Tensor, scale: float = 1.0,
                          residual: torch.Tensor = None) -> None:
     """moe_combine followed by out = bf16(fl(scale * acc) [+ residual])."""
-    _fit32(top_k)
+    if int(top_k) >> 31:
+        _fit32(top_k)
     dev = _device_of(y)
     _need(y, "y", torch.bfloat16, dev)
     _need(router_weights, "router_weights", torch.float32, dev)
@@ -372,7 +385,8 @@ def moe_combine_epilogue(y: torch.Tensor, router_weights: torch.Tensor, restore_
     if y.dim() != 2 or output_tokens.dim() != 2 or y.shape[1] != output_tokens.shape[1]:
         raise ValueError("y must be [rows, hidden] and output_tokens [N, hidden]")
     n, h = output_tokens.shape
-    _fit32(h)
+    if h >> 31:
+        _fit32(h)
     if router_weights.numel() != n * top_k or restore_token_order.numel() != n * top_k:
         raise ValueError("router_weights / restore_token_order must have N*top_k elements")
     res = ctypes.c_void_p(0)
