@@ -33,6 +33,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
+import warnings
 
 import torch
 
@@ -400,6 +402,35 @@ def moe_combine_epilogue(y: torch.Tensor, router_weights: torch.Tensor, restore_
                                         h, int(top_k), float(scale), res, _ptr(output_tokens), _stream(dev)),
                "moe_combine_epilogue")
 
+
+
+
+class _CheckInPython:
+    """Stands for the module _fast where it cannot be used: takes no call, so that each one's arguments are checked
+    in Python and passed through ctypes."""
+
+    def __getattr__(self, name):
+        return lambda *args: -1
+
+
+def _load_fast():
+    """The module that passes torch tensors to the library from C++ (csrc/binding.cpp).  It is made for one version of
+    torch and Python; every call works without it, a few microseconds slower."""
+    running = f"torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
+    try:
+        from . import _fast
+        made_for = _fast.made_for
+        if made_for == running:
+            return _fast
+        reason = f"it is made for {made_for}, this is {running}"
+    except (ImportError, AttributeError) as e:
+        reason = str(e)
+    warnings.warn(f"{__name__}._fast is not used ({reason}): calls in floating point take a few microseconds more on the "
+                  "host; run `python expert_grouping_dispatch_amd/build_lib.py`", RuntimeWarning, stacklevel=3)
+    return _CheckInPython()
+
+
+_fast = _load_fast()
 
 from .experts import (  # noqa: E402  (needs the names above)
     FEW_MAX_SLOTS, MATMUL_MAX_DEPTH, MATMUL_SWIGLU, alloc_layer_few, alloc_quantized, moe_dispatch_i8,

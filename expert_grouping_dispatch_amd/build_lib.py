@@ -3,8 +3,10 @@
     python expert_grouping_dispatch_amd/build_lib.py
 
 Compiles every ``csrc/*.hip`` with hipcc (device code for gfx950 only) and
-links them into ``expert_grouping_dispatch_amd/libmoe_route.so``; then the
-module ``_fast.so`` that passes torch tensors to it (host code).
+links them into ``expert_grouping_dispatch_amd/libmoe_route.so``; then a C
+program that uses it, and the module ``_fast.so`` that passes torch tensors to it
+(host code), which needs torch's and Python's headers.  Without that module
+everything works, with the arguments checked in Python.
 """
 from __future__ import annotations
 
@@ -72,7 +74,9 @@ def build_fast(verbose: bool = True) -> str:
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     tmp = FAST + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DMOE_MADE_FOR="torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"',
+           "-I", INCLUDE,
            *[f"-isystem{d}" for d in cpp_extension.include_paths()], f"-isystem{os.path.join(rocm, 'include')}",
            f"-isystem{sysconfig.get_paths()['include']}", FAST_SRC, "-o", tmp, "-L", PKG, "-lmoe_route",
            "-Wl,-rpath,$ORIGIN", "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-lamdhip64"]
@@ -118,8 +122,13 @@ def build(verbose: bool = True) -> str:
     os.replace(tmp, LIB)
     if verbose:
         print(f"built {LIB} from {len(srcs)} sources", flush=True)
-    build_fast(verbose)
     build_c_example(verbose)
+    try:
+        build_fast(verbose)
+    except Exception as e:  # no torch, no headers, no compiler: the package does without it, and says so when imported
+        if os.path.exists(FAST):
+            os.remove(FAST)  # of an older library
+        print(f"NOT built: {FAST}: {type(e).__name__}: {e}", file=sys.stderr, flush=True)
     return LIB
 
 

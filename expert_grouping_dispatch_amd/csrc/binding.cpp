@@ -15,6 +15,10 @@
 
 #include "moe_experts_float.h"
 
+#ifndef MOE_MADE_FOR  // the versions of torch and Python that this is compiled for, as the package compares them
+#error "MOE_MADE_FOR is not defined"
+#endif
+
 namespace {
 
 constexpr int kElse = -1;
@@ -236,4 +240,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, methods, null
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fast() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__fast() {
+  PyObject* const m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "made_for", MOE_MADE_FOR) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
