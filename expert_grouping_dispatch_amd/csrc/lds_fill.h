@@ -26,8 +26,8 @@ constexpr int kWaitLoads = 0x0F70;     // s_waitcnt vmcnt(0)
 // The same fills where the compiler does not see that they write LDS, and so puts
 // no wait for them before reads of it: the kernel has to wait itself, for its own
 // loads, before the barrier after which their LDS is read.  They have no output
-// register.  A buffer as four scalars; `dst` is an offset into LDS.  M0, which
-// nothing else in such a kernel uses, is set each time.
+// register.  A buffer as four scalars; `dst` is an offset into LDS.  M0 is set each
+// time, and the compiler knows that it is.
 struct BufferAt {
   uint64_t base;
   uint32_t bytes;
@@ -42,7 +42,7 @@ __device__ __forceinline__ void fill_lds(const u32x4& from, uint32_t off, uint32
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(dst), "v"(off), "s"(from), "s"(at)
-               : "memory");
+               : "memory", "m0");
 }
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
