@@ -32,8 +32,9 @@ namespace moe {
 
 namespace {
 
-// Largest group of the first two: 256 experts with 33 or 64 rows each, 2048 ->
-// 7168, took 712 and 762 us as strips, 862 and 872 us as tiles.
+// Largest group of the first two.  256 experts with 33 and with 64 rows each, 2048
+// -> 7168, as strips and as tiles: 672, 729 and 797, 853 us in int8, 1224, 1386
+// and 1518, 1559 in bf16, 649, 691 and 701, 753 in e4m3.
 constexpr int kFewRows = 64;
 constexpr int kFewWaves = 4, kFewThreads = kFewWaves * kWave;
 constexpr int kTile = 256, kStepBytes = 128;  // tile edge, and bytes of a row per step
@@ -42,24 +43,29 @@ constexpr int kStripFrags = 2;  // of 32 weight rows, for each wave
 // Grids of k_matmul_strip have at least C::kStripsMin workgroups; smaller ones
 // leave CUs idle and go to k_matmul_few.  Strips against k_matmul_few in us, int8,
 // bf16 and e4m3:
-//   64 workgroups (8 experts, 20 rows each, 7168 -> 2048)    67/33  139/54   69/36
-//   128 (8, 20, 4096 -> 4096)                                45/36   71/60   39/38
-//   192 (12, 20, 4096 -> 4096)                                 -     76/89   41/68
-//   256 (16, 20, 4096 -> 4096)                               49/66   85/117  46/84
-//   896 (32, 16, 2048 -> 7168)                               83/99  151/184  79/123
+//   64 workgroups (8 experts, 20 rows each, 7168 -> 2048)    67/27  138/52   69/35
+//   128 (8, 20, 4096 -> 4096)                                39/32   70/60   39/40
+//   160 (10, 20, 4096 -> 4096)                               40/42   72/73   40/55
+//   192 (12, 20, 4096 -> 4096)                               41/52   75/87   41/63
+//   192 (24, 4, 2048 -> 2048)                                22/18   37/38   21/20
+//   256 (16, 20, 4096 -> 4096)                               45/66   83/113  45/83
+//   896 (32, 16, 2048 -> 7168)                               81/97  149/174  79/121
+// Between 160 and 256 int8 gains with many rows and loses with few.
 // Buffers of up to kAloneRows rows over weights of up to kAloneWeights values an
 // expert take one launch: all of their groups go to the first kernel, 64 rows at a
-// time.  24 experts, 4 rows each, 1040 -> 528: 7.2 against 9.4 us in bf16, 5.2 and
-// 7.4 in e4m3, 8.2 and 11.2 in int8; one expert with 100 rows, 4096 -> 1024: 41 and
-// 60, 31 and 33, 23 and 35.  More rows would read the weights too often where one
-// expert has them all (250 rows, 4096 -> 4096: 91 and 81 us in bf16, 79 and 50 in
-// e4m3), and so would larger weights (2 x 120 rows, 4096 -> 14336: 176 and 103).
+// time.  24 experts, 4 rows each, 1040 -> 528: 6.7 against 8.9 us in bf16, 5.1 and
+// 7.3 in e4m3, 4.2 and 7.4 in int8; one expert with 100 rows, 4096 -> 1024: 41 and
+// 59, 31 and 33, 23 and 34.  More rows would read the weights too often where one
+// expert has them all (250 rows, 4096 -> 4096: 89 and 81 us in bf16, 74 and 50 in
+// e4m3, 50 and 47 in int8), and so would larger weights (2 x 120 rows, 4096 ->
+// 14336: 170 and 99, 120 and 41, 86 and 42).
 constexpr uint32_t kAloneRows = 128;
 constexpr int64_t kAloneWeights = int64_t(1) << 22;
 constexpr int kMaxActive = 1024;
-// Rows of tiles that are taken column by column together: 491520 rows on 253
-// experts in e4m3, 2048 -> 7168, 8.18 ms with 8, 8.22 with 6, 8.33 with 4, 8.47
-// with all of an expert's (int8 and 1750 rows an expert do not depend on it).
+// Rows of tiles that are taken column by column together: 491366 rows on 253
+// experts, 2048 -> 7168, with 8, 6, 4 and with all of an expert's 6.75, 6.74, 6.83
+// and 7.07 ms in e4m3, 7.31, 7.32, 7.47 and 7.73 in int8, 12.4, 12.4, 12.6 and 13.0
+// in bf16 (1750 rows an expert hardly depend on it).
 constexpr uint32_t kRowGroup = 8;
 
 // Rows [lo, hi) of active expert j, inside the buffer whatever the starts hold.
@@ -170,8 +176,8 @@ __device__ __forceinline__ void matmul_few_tile(const ExpertMatmul& p, uint32_t 
 
 // C::kFewPerSimd waves a SIMD.  In int8 four hold all of a grid of 1024 workgroups at once (8 experts, 16 rows each,
 // 2048 -> 2 x 2048: 16.5 against 18.2 us with three).  In bf16 and e4m3 the registers of four do not hold what is
-// requested together, 2 rows of 4 steps (8 experts, 14 rows each, 4096 -> 4096 in bf16: 71 against 57 us; 24
-// experts, 2 rows, 1040 -> 528: 9.4 against 6.3).
+// requested together, 2 rows of 4 steps, and with four and three 8 experts, 14 rows each, 4096 -> 4096, take 55.6 and
+// 54.2 us in bf16, 35.7 and 32.4 in e4m3; 12 experts, 2 rows each, 7168 -> 2048, 62 and 60, 42 and 37.
 template <class C, bool kSwiglu>
 __global__ __launch_bounds__(kFewThreads, C::kFewPerSimd) void k_matmul_few(ExpertMatmul p, uint32_t most) {
   __shared__ typename C::FewAcc s_part[kFewWaves * 2 * (kFewRows / 16) * kWave];
@@ -195,7 +201,7 @@ __global__ __launch_bounds__(kFewThreads, C::kFewPerSimd) void k_matmul_few(Expe
 // One workgroup: 128*F weight rows (with SwiGLU half of them gate rows, half
 // the up rows of the same channels) times the n <= 32*G rows of one group.
 // Bound by reading the weights: they go to LDS in whole cache lines,
-// non-temporal, in two buffers of a step (128 values of k).  Layout of a
+// non-temporal, in two buffers of a step (128 bytes of a row).  Layout of a
 // buffer, 16-byte pieces and their order as in k_matmul_tile; each wave takes
 // 32*F weight rows, with SwiGLU first its gate and then its up rows.
 template <class C, int G, bool kSwiglu>
@@ -224,7 +230,8 @@ __device__ __forceinline__ void strip(const ExpertMatmul& p, uint32_t lo, int n,
   // Workgroups begin at different steps: rows whose length is a power of two
   // would have all of them at the same few memory channels at any time (64
   // experts, 4 rows each, 4096 x 4096: 235 us against 171 us; no difference at
-  // 2048 and 7168).  The sums are exact in any order.
+  // 2048 and 7168).  In int8 the sums are exact in any order; in fp32 a
+  // workgroup's place fixes theirs.
   const int turn = ragged ? 0 : int((blockIdx.x * 5 + blockIdx.y * 3) % uint32_t(steps));
   const int blocks = C::kBlocks ? steps : 0;  // a step of e4m3 is a block of k
   const int half = (p.n_out + kBlock - 1) / kBlock, w_block = min(c, p.n_out - 1) / kBlock;
@@ -468,15 +475,16 @@ struct TileList {
 };
 
 // One workgroup per CU takes tiles in turn.  Four waves, 2 by 2: each forms
-// 128 rows by 128 weight rows with the 32x32x32 instruction, which halves what
-// has to be read from LDS against eight waves of 128 by 64.
+// 128 rows by 128 weight rows with the 32x32 instruction that takes 16 bytes a
+// lane, which halves what has to be read from LDS against eight waves of 128 by 64.
 //
-// A step is 128 values of k of 256 rows of both operands, 64 KB, in two
-// buffers that are filled straight from global memory.  A row's 128 bytes lie
-// in LDS as eight 16-byte pieces, piece c at c ^ (row/2 % 8), so that sixteen
-// lanes of a read (consecutive rows, one piece) touch all 64 banks once.
+// A step is 128 bytes (128 values of k in int8, 64 in bf16) of 256 rows of both
+// operands, 64 KB, in two buffers that are filled straight from global memory.  A
+// row's 128 bytes lie in LDS as eight 16-byte pieces, piece c at c ^ (row/2 % 8),
+// so that sixteen lanes of a read (consecutive rows, one piece) touch all 64 banks
+// once.
 //
-// A step has four parts of 32 values of k.  The fragments of a part are read
+// A step has four parts of 32 bytes of a row.  The fragments of a part are read
 // while the matrix units work on the part before it; the last part's are in
 // registers before its products start, so there the buffer is free: one
 // barrier, then it is filled for the step after next.  The stream of steps runs

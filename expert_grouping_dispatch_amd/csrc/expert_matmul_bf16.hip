@@ -7,10 +7,10 @@
 // 64 values of k, and a matrix instruction takes the same 16 bytes a lane.
 //
 // Tiles are bound by the matrix units and the clock that random operands leave
-// them (14000 rows on 8 experts, 4096 -> 2 x 14336: 2690 to 2760 us, 1.2e15
+// them (14000 rows on 8 experts, 4096 -> 2 x 14336: 2690 to 2770 us, 1.2e15
 // operations/s, 69% busy at 1.6 GHz; the instructions alone would take 2260), strips
 // by reading the weights (6.2 TB/s), few rows by a few rounds of loads (24 experts,
-// 2 rows each, 1040 -> 528: 6.8 us a call).
+// 2 rows each, 1040 -> 528: 6.7 us a call).
 #include "expert_matmul.h"
 
 namespace moe {

@@ -13,8 +13,8 @@
 // values, a hundredth of the output's rounding.
 //
 // Tiles are bound by the matrix unit and the vector unit beside it at the clock that
-// both leave (14000 rows on 8 experts, 4096 -> 2 x 14336: 1485 to 1515 us, 2.2e15
-// operations/s, 59% and 54% busy at 1.6 GHz; 491520 rows, 2048 -> 7168: 6.9 to 7.0
+// both leave (14000 rows on 8 experts, 4096 -> 2 x 14336: 1485 to 1530 us, 2.2e15
+// operations/s, 59% and 54% busy at 1.6 GHz; 491520 rows, 2048 -> 7168: 6.9 to 7.1
 // ms), strips by reading the weights (776 rows on 247 experts, 7168 -> 2 x 2048: 1040
 // us, 7.0 TB/s).
 #include "expert_matmul.h"

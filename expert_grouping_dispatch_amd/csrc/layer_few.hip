@@ -6,9 +6,10 @@
 // With more slots the first product reads them once for every 64 of them, past
 // the caches, and the second once for every 32, mostly from L2; and the second
 // fetches all of h for each workgroup's few channels, so its time grows with
-// the slots: 8 experts, 4096 x 2048 in int8, 32, 64 and 128 slots on each take
-// 114, 208 and 366 us, the grouped path 82, 154 and 117 us.  Grouping costs each
-// workgroup one pass over the few ids instead of a kernel of its own.
+// the slots: 8 experts, 4096 x 2048, 32, 64 and 128 slots on each take 117, 208 and
+// 368 us in int8, 123, 215 and 375 in e4m3, 142, 263 and 458 in bf16, the grouped
+// calls 75, 142 and 111, 90, 153 and 105, 127, 263 and 187 us (replayed).  Grouping
+// costs each workgroup one pass over the few ids instead of a kernel of its own.
 //
 //   k_few_up     one workgroup per (expert, 64 intermediate channels): lists the
 //                expert's slots and forms gate, up and h = silu(gate)*up for up to
@@ -38,9 +39,9 @@
 //                tokens on all of 8 experts, 4096 x 2048, 644 and 393.
 //
 // e4m3 weights have a scale for each 128 values of k and 128 rows: a block's sums
-// are multiplied with it and added in fp32.  The two experts above 40 us (5.5 TB/s)
-// and 29 us (4.0: starts and ends are a larger part), the 247 experts 1085 us (6.5
-// TB/s) and 666 us.
+// are multiplied with it and added in fp32.  The two experts above 40 us (5.9 TB/s)
+// and 29 us (4.0: starts and ends are a larger part), the 247 experts 1085 us (6.7
+// TB/s) and 666 us (5.4).
 #include <algorithm>
 
 #include "experts.h"
@@ -124,26 +125,34 @@ __device__ __forceinline__ int blocks_of(int n) { return (n + kBlock - 1) / kBlo
 
 // Grids of k_few_up of at least this many workgroups of 64 channels; smaller
 // ones leave CUs idle and take 16 channels a workgroup (k_few_up_split).  The
-// layer in us, 64 channels against 16: 32 workgroups (1 token, 1 of 8 experts,
-// 8192 x 2048, bf16) 83 and 33, 128 workgroups (4 tokens, 2 of 8, 4096 x 1024)
-// 53 and 34, 256 workgroups (1 token, 8 of 64, 7168 x 2048) 122 and 121, 512
-// workgroups (1 token, 8 of 32, 4096 x 4096) 141 and 144.
+// layer in us, 64 channels against 16, in bf16, int8 and e4m3:
+//   32 workgroups (1 token, 1 of 8 experts, 8192 x 2048)    81/32   66/25  60/28
+//   128 (4 tokens, 2 of 8, 4096 x 1024)                     53/34   40/24  37/25
+//   256 (1 token, 8 of 64, 7168 x 2048)                    122/121  78/67  75/68
+//   256 (2 tokens, 8 of 64, 4096 x 1024)                    69/68   49/42  46/44
+//   512 (1 token, 8 of 32, 4096 x 4096)                    138/144  75/75  75/78
+// At 256 itself the smaller form is still ahead with 8-bit weights.
 constexpr int kUpStripsMin = 256;
 // Output channels a workgroup of k_few_down: what spreads them over this many
 // workgroups, in groups of four, at most 32; above 16 the workgroup has two
 // row tiles.  Rows of a tile past the workgroup's are not read.
-// Layers, 256 experts in int8, 776 slots, 7168 channels: 1734 us with 28 each,
-// 1755 us with 32 on 224 workgroups, 1925 us with 16; in bf16, 2048 channels, 32
-// tokens, 8 of 64 experts: 210 us with 8 each, 235 us with 16; 5120 channels, 1
-// token, 8 of 64: 53 us with 20 each, 64 with 16.
+// Layers in int8, bf16 and e4m3: 256 experts, 776 slots, 7168 channels, 1765, 3218
+// and 1726 us with 28 each, 1776, 3260 and 1733 with 32 on 224 workgroups, 1947, 3409
+// and 1929 with 16; 2048 channels, 32 tokens, 8 of 64 experts, 188, 294 and 187 with 8
+// each, 207, 333 and 205 with 16; 5120 channels, 1 token, 8 of 64, 47, 68 and 47 with
+// 20 each, 59, 80 and 59 with 16.
 constexpr int kDownGroups = 256;
 constexpr int kDownWaves = 8;
 // Rows of w_down of at least this many values are read in whole lines
-// (few_down_lines) for experts with few slots.  The layer with and without: 97
-// tokens, 8 of 256 experts, 7168 x 2048 in int8, 1734 and 1806 us; 1 token, 2 of
-// 8, 4096 x 14336 in bf16, 116 and 121 us; 4 tokens, 8 of 64, 2048 x 2048, 120
-// and 126 us; 32 tokens, 8 of 64, 2048 x 1408, 210 and 213 us; 1 token, 8 of 64,
-// 2048 x 1024, 27.3 and 26.3 us.
+// (few_down_lines) for experts with few slots.  The layer with and without, in
+// int8, bf16 and e4m3:
+//   97 tokens, 8 of 256 experts, 7168 x 2048  1750/1827  3217/3368  1710/1805
+//   32 tokens, 8 of 64, 2048 x 1408            141/144    208/212    140/142
+//   4 tokens, 8 of 64, 2048 x 2048              76/78     114/116     74/76
+//   4 tokens, 8 of 64, 2048 x 1280              65/63      88/89      63/60
+//   1 token, 8 of 64, 2048 x 1024               23/21      27/27      23/21
+//   1 token, 2 of 8, 4096 x 14336               69/68     116/111     68/66.5
+// Two long experts lose a little by it, many experts gain.
 constexpr int kLinesMin = 1280;
 constexpr int kUpMost = 3;  // buffers
 // What bf16 leaves of two values whose bf16 forms are `hi`, in bf16; nothing
@@ -975,7 +984,8 @@ __global__ __launch_bounds__(kDownWaves* kWave, 2) void k_few_down(
       if (own_e[i] >= 0) s_list[s_count[own_e[i]] + own_rank[i]] = uint16_t(base + tid + i * kThreads);
     __syncthreads();
 
-    // With fewer experts than waves, k is split so that every wave has work; every part has a step.
+    // With fewer experts than waves, k is split so that every wave has work.  Every part has a step; with block scales,
+    // whose parts are whole blocks, some may have none and give zeros.
     int bits = 0;  // of the number of parts
     while ((2 << bits) <= max_parts && (2 << bits) * kStreamStep <= inter && (active << bits) < 2 * NW) ++bits;
     const int parts = 1 << bits;

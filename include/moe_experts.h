@@ -85,6 +85,8 @@ int moe_quantize_i8(const uint16_t* x, int64_t n_rows, int32_t hidden, const uin
  * With MOE_MATMUL_SWIGLU the weights of an expert are 2*n_out rows, the gate
  * rows first and the up rows after them, and
  *   out[p, n] = bf16(silu(v[p, n]) * v[p, n_out + n]),  silu(v) = v / (1 + exp(-v)).
+ * Below v = -88.72 exp(-v) is infinite in fp32 and silu(v), less than 2^-121 in
+ * magnitude, becomes -0.
  *
  *   a_q           [device] int8 [a_rows, depth], 16-byte aligned.
  *   a_scales      [device] fp32 [a_rows].
@@ -123,10 +125,12 @@ size_t moe_layer_few_workspace_bytes(int64_t n_rows, int32_t top_k, int32_t inte
  *   g = w_gate_up[e][0:inter] x[t],  u = w_gate_up[e][inter:2*inter] x[t]
  *   h = silu(g) * u,                 y_j = w_down[e] h
  *   out[t] = bf16( sum_{j routed, ascending} router_weights[t, j] * y_j )
- * with fp32 sums.  Between the kernels h is held as two bf16 values, 16 bits of
- * mantissa.  Made for few slots on an expert: its time grows with them, and from
- * about four on each active expert the grouped calls (moe_create_indices to
- * moe_combine) take less time on the GPU with int8 weights.  Tokens without a routed choice are written as +0.
+ * with fp32 sums, and silu as in moe_expert_matmul_i8.  Between the kernels h is
+ * held as two bf16 values, 16 bits of mantissa.  Made for few slots on an expert:
+ * its time grows with them.  From about two on each active expert the grouped
+ * calls (moe_create_indices to moe_combine), whose activations have 8 bits then,
+ * take less time on the GPU with 8-bit weights, and from about eight with bf16
+ * ones.  Tokens without a routed choice are written as +0.
  * Infinities and NaNs in a token stay in its own output; an infinite weight
  * may give NaN where the formula gives an infinity.
  *

@@ -44,6 +44,8 @@ extern "C" {
  * With MOE_MATMUL_SWIGLU the weights of an expert are 2*n_out rows, the gate
  * rows first and the up rows after them, and
  *   out[p, n] = bf16(silu(v[p, n]) * v[p, n_out + n]),  silu(v) = v / (1 + exp(-v)).
+ * Below v = -88.72 exp(-v) is infinite in fp32 and silu(v), less than 2^-121 in
+ * magnitude, becomes -0.
  * The order of a sum depends on the sizes, the other rows and the row's place among
  * them, but not on time: the same call gives the same bits.  Infinities and
  * NaNs in a row stay in its own output.
