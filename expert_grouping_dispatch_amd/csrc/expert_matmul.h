@@ -183,16 +183,17 @@ __global__ __launch_bounds__(kFewThreads, C::kFewPerSimd) void k_matmul_few(Expe
   __shared__ typename C::FewAcc s_part[kFewWaves * 2 * (kFewRows / 16) * kWave];
   uint32_t lo, hi;
   group_rows(p.starts, blockIdx.y, p.a_rows, lo, hi);
-  if (hi - lo > most) return;
+  if (lo == hi || hi - lo > most) return;
   const int e = p.expert_ids[blockIdx.y];
   if (e < 0 || e >= p.n_experts) return;
   const int c0 = blockIdx.x * (kSwiglu ? 16 : 32);
-  for (; lo < hi; lo += kFewRows) {
+  for (;; lo += kFewRows) {
     const int n = min(hi - lo, uint32_t(kFewRows));
     if (n <= 16) matmul_few_tile<C, 1, kSwiglu>(p, lo, n, e, c0, s_part);
     else if (n <= 32) matmul_few_tile<C, 2, kSwiglu>(p, lo, n, e, c0, s_part);
     else matmul_few_tile<C, 4, kSwiglu>(p, lo, n, e, c0, s_part);
-    __syncthreads();  // s_part is rewritten for the next rows
+    if (hi - lo <= uint32_t(kFewRows)) return;  // before lo, which may pass 2^32 with the buffer's last rows
+    __syncthreads();                            // s_part is rewritten for the next rows
   }
 }
 
@@ -380,15 +381,16 @@ __global__ __launch_bounds__(kStripThreads, 2) void k_matmul_strip(ExpertMatmul 
   __shared__ __align__(16) uint8_t s_w0[128 * kStripFrags * kStepBytes], s_w1[128 * kStripFrags * kStepBytes];
   uint32_t lo, hi;
   group_rows(p.starts, blockIdx.y, p.a_rows, lo, hi);
-  if (hi - lo > most) return;
+  if (lo == hi || hi - lo > most) return;
   const int e = p.expert_ids[blockIdx.y];
   if (e < 0 || e >= p.n_experts) return;
   const int c0 = blockIdx.x * (kSwiglu ? 64 * kStripFrags : 128 * kStripFrags);
-  for (; lo < hi; lo += kFewRows) {
+  for (;; lo += kFewRows) {
     const int n = min(hi - lo, uint32_t(kFewRows));
     if (n <= 32) strip<C, 1, kSwiglu>(p, lo, n, e, c0, s_a0, s_a1, s_w0, s_w1);
     else strip<C, 2, kSwiglu>(p, lo, n, e, c0, s_a0, s_a1, s_w0, s_w1);
-    __syncthreads();  // the buffers are filled again for the next rows
+    if (hi - lo <= uint32_t(kFewRows)) return;  // before lo, which may pass 2^32 with the buffer's last rows
+    __syncthreads();                            // the buffers are filled again for the next rows
   }
 }
 
@@ -404,6 +406,9 @@ struct Walk {
   uint32_t tile;  // next tile to look at
   int j;          // place of its expert, found going forward
 };
+
+// Of any number of rows up to 2^32 - 1: a sum with kTile - 1 would pass 32 bits.
+__device__ __forceinline__ uint32_t row_tiles(uint32_t rows) { return rows / kTile + (rows % kTile != 0); }
 
 // The tiles of all groups of more than kFewRows rows, in the order of the groups, filled by the whole workgroup.
 template <int kThreads>
@@ -427,7 +432,7 @@ struct TileList {
       row[j] = lo;
       expert[j] = j < p.n_experts ? p.expert_ids[j] : -1;
       if (j == kMaxActive - 1) row[kMaxActive] = hi;
-      tiles[i] = hi - lo > uint32_t(kFewRows) ? ((hi - lo + kTile - 1) / kTile) * col_tiles : 0u;
+      tiles[i] = hi - lo > uint32_t(kFewRows) ? row_tiles(hi - lo) * col_tiles : 0u;
       sum += tiles[i];
     }
     const uint32_t upto = wave_inclusive_sum(sum);
@@ -455,13 +460,13 @@ struct TileList {
     for (; at.tile < total; at.tile += grid) {
       while (at.j + 1 < kMaxActive && uniform(first[at.j + 1]) <= at.tile) ++at.j;
       const uint32_t lo = uniform(row[at.j]), hi = max(min(uniform(row[at.j + 1]), p.a_rows), lo);
-      const uint32_t row_tiles = (hi - lo + kTile - 1) / kTile;
-      if (row_tiles == 0) continue;
+      const uint32_t down = row_tiles(hi - lo);
+      if (down == 0) continue;
       // Rows by kRowGroup, within them columns, within a column its rows: the tiles that an XCD's workgroups take at
       // once then share both operands in its L2.
       const uint32_t in = at.tile - uniform(first[at.j]), col_tiles = (uint32_t(p.n_out) + channels - 1) / channels;
       const uint32_t group = in / (kRowGroup * col_tiles), rest = in % (kRowGroup * col_tiles);
-      const uint32_t rows = min(row_tiles - group * kRowGroup, kRowGroup);
+      const uint32_t rows = min(down - group * kRowGroup, kRowGroup);
       t.row0 = lo + (group * kRowGroup + rest % rows) * kTile;
       t.c0 = int(rest / rows) * channels;
       t.e = uniform(expert[at.j]);
