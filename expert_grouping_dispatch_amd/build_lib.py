@@ -76,7 +76,7 @@ def build_fast(verbose: bool = True) -> str:
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            f'-DMOE_MADE_FOR="torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"',
-           "-I", INCLUDE,
+           "-I", INCLUDE, "-I", CSRC,
            *[f"-isystem{d}" for d in cpp_extension.include_paths()], f"-isystem{os.path.join(rocm, 'include')}",
            f"-isystem{sysconfig.get_paths()['include']}", FAST_SRC, "-o", tmp, "-L", PKG, "-lmoe_route",
            "-Wl,-rpath,$ORIGIN", "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-lamdhip64"]

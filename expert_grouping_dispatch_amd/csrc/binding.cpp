@@ -14,6 +14,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "moe_experts_float.h"
+#include "python_call.h"
 
 #ifndef MOE_MADE_FOR  // the versions of torch and Python that this is compiled for, as the package compares them
 #error "MOE_MADE_FOR is not defined"
@@ -21,7 +22,10 @@
 
 namespace {
 
-constexpr int kElse = -1;
+using moe::guarded;
+using moe::kElse;
+using moe::status;
+using moe::unlocked;
 
 // The tensors of a call: each is checked against the device of the first.
 class Call {
@@ -70,18 +74,6 @@ bool number(PyObject* o, int64_t* out) {
   int over = 0;
   *out = PyLong_AsLongLongAndOverflow(o, &over);
   return over == 0 && fits(*out);
-}
-
-PyObject* status(int s) { return PyLong_FromLong(s); }
-
-// The status of a call into the library, made without the interpreter's lock: a launch that waits for room in a full
-// queue does not stop the other Python threads.  The caller's arguments hold the tensors meanwhile.
-template <class F>
-PyObject* unlocked(F call) {
-  PyThreadState* const state = PyEval_SaveThread();
-  const int s = call();  // a C entry point, throws nothing
-  PyEval_RestoreThread(state);
-  return status(s);
 }
 
 constexpr auto kBf16 = c10::ScalarType::BFloat16, kF8 = c10::ScalarType::Float8_e4m3fn, kF32 = c10::ScalarType::Float,
@@ -220,17 +212,6 @@ PyObject* layer_few_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 : moe_layer_few_f8(px, rows, int32_t(h), int32_t(k), static_cast<const int32_t*>(pi), pr, pm,
                                    int32_t(rank), int32_t(e), pg, psg, pd, psd, int32_t(i), po, ps, bytes, s);
   });
-}
-
-// No C++ exception may leave a call of Python's: the Python binding makes such a call again and says what is wrong.
-template <PyObject* (*kCall)(PyObject*, PyObject* const*, Py_ssize_t)>
-PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  try {
-    return kCall(self, a, n);
-  } catch (...) {
-    PyErr_Clear();
-    return status(kElse);
-  }
 }
 
 #define MOE_METHOD(name) {#name, reinterpret_cast<PyCFunction>(&guarded<name>), METH_FASTCALL, nullptr}
